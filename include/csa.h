@@ -3,7 +3,8 @@
  * Compressed Sparse Attention (CSA) and its compressor-only mode (HCA) over
  * THD-packed variable-length sequences (and fixed-shape BSND batches), on one
  * GPU; of the backward of its sparse MLA attention, the indexer's KL-loss
- * gradient and the THD compressor core that produces the compressed rows.
+ * gradient and the THD compressor core that produces the compressed rows; and
+ * of rotary positions and the same layers over paged caches, for new tokens.
  *
  * Sources (web pages, cited by title and section):
  *   [miles#2038]  "PR #2038 完整报告" (radixark/miles): "Enable THD
@@ -410,6 +411,185 @@ csa_status_t csa_indexer_topk_noalloc(const csa_bf16_t *q, const csa_bf16_t *k, 
                                       const int32_t *cu_seqlens_cmp_kv, int32_t batch,
                                       int32_t cmp_ratio, int32_t topk, int32_t *topk_idx,
                                       float *topk_val, csa_stream_t stream);
+
+/*
+ * Rotary positions and paged row caches: the calls with which a sequence is
+ * continued token by token after its prompt. The pages take every rotation as
+ * done upstream ([hp#RFC] section 2: the 512-wide row comes rotated) and have
+ * no counterpart to these entry points; they are what a server of such a
+ * layer needs beside the forward above.
+ *
+ * A paged cache is a pool of rows [num_pages, page_size, width] bf16 and a
+ * table pages [batch, max_pages] int32: row r of sequence b is row
+ * r % page_size of pool page pages[b, r / page_size]. Pages may have any size
+ * and order, and sequences may share pages they only read. Entries outside
+ * [0, num_pages) stand for absent pages: a call that needs one skips its rows
+ * and records it in the device error word.
+ *
+ * New tokens are rows t of the call's tensors: q_pos[t] (or row_pos[t]) is the
+ * token's position in its sequence, from 0, itself included in what it sees,
+ * and q_seq[t] the sequence (the table's row). q_seq NULL: token t belongs to
+ * sequence t (then total_tokens <= batch). A negative position marks a padding
+ * slot, whatever its q_seq. Several tokens may belong to one sequence (drafted
+ * tokens, a chunk of a prompt), in any order. A q_seq outside [0, batch) is
+ * recorded and its token treated as a padding slot.
+ */
+typedef enum { CSA_BF16 = 0, CSA_F32 = 1 } csa_dtype_t;
+typedef enum { CSA_ROPE_INTERLEAVED = 0, CSA_ROPE_HALF = 1 } csa_rope_layout_t;
+
+/*
+ * Rotation frequencies in radians per position, inv_freq [rope_dim / 2] fp64:
+ *     f_i = theta^(-2 i / rope_dim)
+ * factor 1 keeps them. A larger factor stretches positions for longer
+ * contexts: with original_len == 0 every f_i becomes f_i / factor; with
+ * original_len > 0 only the slow ones do, by the ramp over the pair index
+ *     lo = floor(d(beta_fast)), hi = ceil(d(beta_slow)),
+ *     d(b) = rope_dim ln(original_len / (2 pi b)) / (2 ln theta),
+ *     g_i = clamp((i - lo) / (hi - lo), 0, 1)   (lo, hi within [0, rope_dim - 1])
+ *     f_i := g_i f_i / factor + (1 - g_i) f_i
+ * (pairs turning more than beta_fast times over original_len keep their
+ * frequency). Any other table of the same form may be used in its place.
+ * Errors: NULL -> CSA_ERR_NULL; rope_dim < 2 or odd, or original_len < 0 ->
+ * CSA_ERR_SHAPE; theta <= 1, factor < 1, or, with original_len > 0,
+ * beta_slow <= 0 or beta_fast < beta_slow, or any of them not finite ->
+ * CSA_ERR_UNSUPPORTED.
+ */
+csa_status_t csa_rope_freqs(int32_t rope_dim, double theta, double factor, int32_t original_len,
+                            double beta_fast, double beta_slow, double *inv_freq,
+                            csa_stream_t stream);
+
+/*
+ * Rotary positions over the dims [rope_offset, rope_offset + rope_dim) of
+ * every head; the other dims are copied. With p the token's position,
+ * theta_i = p f_i and the pair (a, b) = (2 i, 2 i + 1) for
+ * CSA_ROPE_INTERLEAVED or (i, i + rope_dim / 2) for CSA_ROPE_HALF:
+ *     out_a = mscale (x_a cos theta_i - x_b sin theta_i)
+ *     out_b = mscale (x_b cos theta_i + x_a sin theta_i)
+ * inverse != 0 turns by -theta_i: the transpose of the forward map, so that it
+ * takes the gradient of out to the gradient of x (and turns an attention
+ * output back when the rows it sums were rotated). Computed in fp32 from
+ * angles reduced in fp64, rounded once.
+ * x, out: dtype (CSA_BF16 or CSA_F32); token t starts x_stride (out_stride)
+ * elements after token t - 1 and holds [heads, head_dim] contiguously. out may
+ * be x itself (with the same stride): only the rotary dims are touched then.
+ * positions [total_tokens] int32, or NULL with cu_seqlens [batch+1]: a token's
+ * place in its packed sequence. p = that value times pos_stride (for
+ * compressed rows of ratio r, pos_stride = r gives the first pooled token).
+ * inv_freq [rope_dim / 2] fp64, as from csa_rope_freqs.
+ * Errors: negative sizes, heads or head_dim < 1, rope_dim < 2 or odd, a rotary
+ * part outside the head, a stride below heads * head_dim (with more than one
+ * token) -> CSA_ERR_SHAPE; an unknown dtype or layout, rope_dim > 1024, heads
+ * > 65535, out overlapping x without being x -> CSA_ERR_UNSUPPORTED; x or out
+ * not aligned to its element -> CSA_ERR_UNSUPPORTED; NULL x/out/inv_freq, or
+ * both positions and cu_seqlens -> CSA_ERR_NULL. total_tokens == 0 launches
+ * nothing. A token not covered by cu_seqlens is rotated as position 0 and
+ * recorded in the device error word.
+ */
+csa_status_t csa_rope(const void *x, csa_dtype_t dtype, int64_t x_stride, const int32_t *positions,
+                      const int32_t *cu_seqlens, int32_t batch, int32_t pos_stride,
+                      const double *inv_freq, int32_t total_tokens, int32_t heads,
+                      int32_t head_dim, int32_t rope_offset, int32_t rope_dim,
+                      csa_rope_layout_t layout, float mscale, int32_t inverse, void *out,
+                      int64_t out_stride, csa_stream_t stream);
+
+/*
+ * Appends rows to a paged cache: row t goes to the slot of position row_pos[t]
+ * of sequence row_seq[t], its dims [rope_offset, rope_offset + rope_dim)
+ * rotated as by csa_rope at row_pos[t] * pos_stride (rope_dim 0: no rotation),
+ * rounded once to bf16. Serves the original-KV rows (width 512), the
+ * compressed rows and the indexer's rows alike; fp32 rows are what
+ * csa_compress_thd leaves.
+ * rows [total_rows, width], dtype; row t starts row_stride elements after row
+ * t - 1. Padding slots (row_pos < 0) write nothing. No other slot of the cache
+ * is touched. Slots named by several rows of one call hold a mixture of them
+ * afterwards: keep them distinct.
+ * Errors: negative sizes, width < 1, page_size < 1, rope_dim negative or odd
+ * or outside the row, row_stride < width (with more than one row), row_seq
+ * NULL with total_rows > batch -> CSA_ERR_SHAPE; an unknown dtype or layout,
+ * rope_dim > 1024, rows or cache not aligned to their element ->
+ * CSA_ERR_UNSUPPORTED; NULL rows/row_pos/pages/cache, or inv_freq with
+ * rope_dim > 0 -> CSA_ERR_NULL. total_rows == 0 launches nothing. A row whose
+ * sequence or page does not exist is skipped and recorded in the device error
+ * word.
+ */
+csa_status_t csa_cache_append(const void *rows, csa_dtype_t dtype, int64_t row_stride,
+                              const int32_t *row_seq, const int32_t *row_pos,
+                              const int32_t *pages, int32_t batch, int32_t max_pages,
+                              int32_t num_pages, int32_t page_size, int32_t total_rows,
+                              int32_t width, const double *inv_freq, int32_t rope_offset,
+                              int32_t rope_dim, csa_rope_layout_t layout, float mscale,
+                              int32_t pos_stride, csa_bf16_t *cache, csa_stream_t stream);
+
+/*
+ * csa_indexer_topk for new tokens over a paged cache of indexer rows
+ * k_cache [num_pages, page_size, index_dim]: the score is the same, the rows
+ * visible to a token at position p are j < floor((p + 1) / cmp_ratio) of its
+ * sequence, and topk_idx receives rows of the sequence (not of the pool), in
+ * ascending order, -1 padded; a padding slot gets -1 (-inf) throughout. Rows
+ * that the table holds no page for are recorded and rank last (-inf).
+ * csa_indexer_topk_paged_workspace_size: bytes for the scores, 4 for every
+ * token and row the table can hold (max_rows = max_pages * page_size).
+ * Errors: as csa_indexer_topk (q and k_cache 16-byte aligned, index_dim 64 or
+ * 128, 1 to 64 heads, cmp_ratio >= 2, topk >= 1), plus page_size < 1,
+ * max_pages * page_size above INT32_MAX, q_seq NULL with total_tokens > batch
+ * -> CSA_ERR_SHAPE; total_tokens > 65535 -> CSA_ERR_UNSUPPORTED; a short or
+ * not 256-byte aligned workspace -> CSA_ERR_WORKSPACE. k_cache and pages may
+ * be NULL when max_pages or num_pages is 0. total_tokens == 0 launches
+ * nothing.
+ */
+size_t csa_indexer_topk_paged_workspace_size(int32_t total_tokens, int32_t max_rows,
+                                             int32_t index_heads, int32_t index_dim, int32_t topk);
+
+csa_status_t csa_indexer_topk_paged(const csa_bf16_t *q, const csa_bf16_t *k_cache, const float *w,
+                                    const int32_t *pages, const int32_t *q_seq,
+                                    const int32_t *q_pos, int32_t batch, int32_t total_tokens,
+                                    int32_t index_heads, int32_t index_dim, int32_t num_pages,
+                                    int32_t page_size, int32_t max_pages, int32_t cmp_ratio,
+                                    int32_t topk, int32_t *topk_idx, float *topk_val,
+                                    void *workspace, size_t workspace_bytes, csa_stream_t stream);
+
+/*
+ * csa_sparse_mla_fwd for new tokens over paged caches. Token t at position p
+ * of its sequence attends the rows [max(0, p - ori_win_left), p] of ori_cache
+ * and, of cmp_cache, the rows of its sequence listed in cmp_sparse_indices[t]
+ * (entries that are negative or not visible are skipped, each remaining one
+ * counts on its own) or, with cmp_sparse_indices NULL, every visible one:
+ * j < floor((p + 1) / cmp_ratio). cmp_cache NULL means window only. Scale,
+ * sinks, out and lse as csa_sparse_mla_fwd; the weights enter the sum over the
+ * rows in bf16, everything else is fp32. Pages of rows no new token can see
+ * may be absent (a server releases them as the window moves on); a page that
+ * is needed and absent is recorded and its rows are left out. A token left
+ * without any row gets out = 0 and lse = its sink (-inf without sinks); a
+ * padding slot out = 0 and lse = -inf.
+ * The keys of all tokens are split evenly over the GPU whatever their lengths
+ * and joined through the workspace; the split follows from the sizes and
+ * positions alone, so equal calls give equal bits.
+ * ori_cache [ori_num_pages, ori_page_size, 512], cmp_cache [cmp_num_pages,
+ * cmp_page_size, 512] bf16; q, out [T, H, 512] bf16; softmax_lse [T, H] fp32,
+ * written only when return_softmax_lse != 0. workspace: at least
+ * csa_sparse_mla_paged_workspace_size(total_tokens, heads) bytes, 256-byte
+ * aligned; its contents do not matter before the call and mean nothing after
+ * it. Calls that may overlap on the GPU need workspaces of their own.
+ * Errors: NULL q/ori_cache/ori_pages/q_pos/out (cmp_pages with cmp_cache,
+ * softmax_lse when asked for) -> CSA_ERR_NULL; negative sizes, heads < 1, page
+ * sizes < 1, max_pages * page_size above INT32_MAX, topk < 1 with
+ * cmp_sparse_indices, q_seq NULL with total_tokens > batch -> CSA_ERR_SHAPE;
+ * head_dim != 512, heads > 64, ori_win_right != 0, cmp_ratio < 2 while
+ * cmp_cache is used, q/ori_cache/cmp_cache/out not 16-byte aligned ->
+ * CSA_ERR_UNSUPPORTED; a short or misaligned workspace -> CSA_ERR_WORKSPACE.
+ * total_tokens == 0 launches nothing.
+ */
+size_t csa_sparse_mla_paged_workspace_size(int32_t total_tokens, int32_t heads);
+
+csa_status_t csa_sparse_mla_paged(
+    const csa_bf16_t *q, const csa_bf16_t *ori_cache, const csa_bf16_t *cmp_cache,
+    const int32_t *cmp_sparse_indices, const int32_t *ori_pages, const int32_t *cmp_pages,
+    const int32_t *q_seq, const int32_t *q_pos, int32_t batch, int32_t total_tokens, int32_t heads,
+    int32_t head_dim, int32_t ori_num_pages, int32_t ori_page_size, int32_t ori_max_pages,
+    int32_t cmp_num_pages, int32_t cmp_page_size, int32_t cmp_max_pages, int32_t topk,
+    const float *sinks, float softmax_scale, int32_t cmp_ratio, int32_t ori_win_left,
+    int32_t ori_win_right, csa_bf16_t *out, float *softmax_lse, int32_t return_softmax_lse,
+    void *workspace, size_t workspace_bytes, csa_stream_t stream);
 
 /*
  * Synchronises `stream`, then returns and clears the device error word of the

@@ -1,6 +1,7 @@
 """GB300 (sm_103a) forward path of DeepSeek-V4 Compressed Sparse Attention
 (THD, and BSND batches), the backward of its sparse MLA attention and the
-indexer's KL-loss gradient.
+indexer's KL-loss gradient; rotary positions, and the same layers for new
+tokens over paged caches.
 
 Thin Python binding of the C ABI declared in ``include/csa.h`` (same call
 names). It only marshals arguments: every step of the path runs in the CUDA
@@ -25,6 +26,8 @@ __all__ = [
     "csa_sparse_mla_fwd", "csa_sparse_mla_bwd", "csa_device_error", "csa_indexer_topk_noalloc",
     "csa_indexer_kl_loss_grad", "csa_bsnd_mla_workspace_size", "csa_sparse_mla_fwd_bsnd",
     "csa_bsnd_indexer_workspace_size", "csa_indexer_topk_bsnd", "csa_compress_thd",
+    "csa_rope_freqs", "csa_rope", "csa_cache_append", "csa_indexer_topk_paged_workspace_size",
+    "csa_indexer_topk_paged", "csa_sparse_mla_paged_workspace_size", "csa_sparse_mla_paged",
     "csa_set_wait_limit_ns", "csa_set_pair_select_rows", "EXPORTED_SYMBOLS",
 ]
 
@@ -38,6 +41,8 @@ EXPORTED_SYMBOLS = (
     "csa_sparse_mla_bwd", "csa_device_error", "csa_indexer_topk_noalloc",
     "csa_indexer_kl_loss_grad", "csa_bsnd_mla_workspace_size", "csa_sparse_mla_fwd_bsnd",
     "csa_bsnd_indexer_workspace_size", "csa_indexer_topk_bsnd", "csa_compress_thd",
+    "csa_rope_freqs", "csa_rope", "csa_cache_append", "csa_indexer_topk_paged_workspace_size",
+    "csa_indexer_topk_paged", "csa_sparse_mla_paged_workspace_size", "csa_sparse_mla_paged",
     "csa_set_wait_limit_ns", "csa_set_pair_select_rows",
 )
 
@@ -54,6 +59,7 @@ class CsaError(RuntimeError):
 
 _lib = None
 _vp, _i32, _sz, _f32 = C.c_void_p, C.c_int32, C.c_size_t, C.c_float
+_i64, _f64 = C.c_int64, C.c_double
 
 
 def lib():
@@ -96,13 +102,26 @@ def lib():
                                             _i32, _i32, _vp, _vp, _vp, _sz, _vp]
         L.csa_compress_thd.argtypes = [_vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32,
                                        _i32, _vp, _vp]
+        L.csa_rope_freqs.argtypes = [_i32, _f64, _f64, _i32, _f64, _f64, _vp, _vp]
+        L.csa_rope.argtypes = [_vp, C.c_int, _i64, _vp, _vp, _i32, _i32, _vp, _i32, _i32, _i32,
+                               _i32, _i32, C.c_int, _f32, _i32, _vp, _i64, _vp]
+        L.csa_cache_append.argtypes = [_vp, C.c_int, _i64, _vp, _vp, _vp, _i32, _i32, _i32, _i32,
+                                       _i32, _i32, _vp, _i32, _i32, C.c_int, _f32, _i32, _vp, _vp]
+        L.csa_indexer_topk_paged_workspace_size.restype = _sz
+        L.csa_indexer_topk_paged_workspace_size.argtypes = [_i32] * 5
+        L.csa_indexer_topk_paged.argtypes = [_vp] * 6 + [_i32] * 9 + [_vp, _vp, _vp, _sz, _vp]
+        L.csa_sparse_mla_paged_workspace_size.restype = _sz
+        L.csa_sparse_mla_paged_workspace_size.argtypes = [_i32, _i32]
+        L.csa_sparse_mla_paged.argtypes = [_vp] * 8 + [_i32] * 11 + [_vp, _f32, _i32, _i32, _i32,
+                                                                     _vp, _vp, _i32, _vp, _sz, _vp]
         L.csa_set_wait_limit_ns.argtypes = [C.c_uint64]
         L.csa_set_pair_select_rows.argtypes = [_i32]
         for name in ("csa_compress_cu_seqlens", "csa_window_idx", "csa_indexer_topk",
                      "csa_sparse_mla_fwd", "csa_sparse_mla_bwd", "csa_device_error",
                      "csa_indexer_topk_noalloc", "csa_indexer_kl_loss_grad",
                      "csa_sparse_mla_fwd_bsnd", "csa_indexer_topk_bsnd", "csa_compress_thd",
-                     "csa_set_wait_limit_ns", "csa_set_pair_select_rows"):
+                     "csa_rope_freqs", "csa_rope", "csa_cache_append", "csa_indexer_topk_paged",
+                     "csa_sparse_mla_paged", "csa_set_wait_limit_ns", "csa_set_pair_select_rows"):
             getattr(L, name).restype = C.c_int
         _lib = L
     return _lib
@@ -432,6 +451,256 @@ def csa_compress_thd(kv, score, ape, cu_seqlens, cu_seqlens_cmp, total_cmp: int,
         cu_seqlens.numel() - 1, T, int(total_cmp), int(cmp_ratio), int(head_dim),
         1 if overlap else 0, _ptr(out), _stream(stream)), "csa_compress_thd")
     return out
+
+
+_DTYPES = {torch.bfloat16: 0, torch.float32: 1}
+_LAYOUTS = {"interleaved": 0, "half": 1}
+
+
+def _rows(t, name, ndim):
+    """A bf16 or fp32 CUDA tensor whose rows (everything past the first axis)
+    are contiguous; the stride between them is free. Returns (dtype code, stride)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
+    if t.dim() not in ndim:
+        raise ValueError(f"{name} must have {' or '.join(map(str, ndim))} dims, got {tuple(t.shape)}")
+    if t.numel() and not t[0].is_contiguous():
+        raise ValueError(f"{name} must have contiguous rows")
+    return code, t.stride(0)
+
+
+def _shape(t, name, shape):
+    if t is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+def _layout(layout):
+    if layout not in _LAYOUTS:
+        raise ValueError(f"layout must be one of {sorted(_LAYOUTS)}, got {layout!r}")
+    return _LAYOUTS[layout]
+
+
+class _Device:
+    """Checks that the tensors share one device and makes it current."""
+
+    def __init__(self, first, *others):
+        dev = first.device
+        for t in others:
+            if t is not None and t.device != dev:
+                raise ValueError(f"tensors on {dev} and {t.device} in one call")
+        self.index = dev.index
+        self.back = None
+
+    def __enter__(self):
+        cur = torch.cuda.current_device()
+        if cur != self.index:
+            self.back = cur
+            torch.cuda.set_device(self.index)
+
+    def __exit__(self, *exc):
+        if self.back is not None:
+            torch.cuda.set_device(self.back)
+
+
+def csa_rope_freqs(rope_dim: int, theta: float = 10000.0, factor: float = 1.0,
+                   original_len: int = 0, beta_fast: float = 32.0, beta_slow: float = 1.0,
+                   out=None, device=None, stream=None):
+    """Rotation frequencies [rope_dim / 2] fp64 in radians per position, for
+    :func:`csa_rope` and :func:`csa_cache_append`. ``factor`` > 1 stretches
+    positions for longer contexts: all pairs (``original_len`` 0) or the slow
+    ones, by parts."""
+    if out is None:
+        out = torch.empty((max(int(rope_dim), 0) // 2,), dtype=torch.float64,
+                          device=device or "cuda")
+    _need(out, "out", torch.float64, 1)
+    _shape(out, "out", (int(rope_dim) // 2,))
+    with _Device(out):
+        _check(lib().csa_rope_freqs(int(rope_dim), float(theta), float(factor), int(original_len),
+                                    float(beta_fast), float(beta_slow), _ptr(out),
+                                    _stream(stream)), "csa_rope_freqs")
+    return out
+
+
+def csa_rope(x, positions, inv_freq, rope_offset=None, layout: str = "interleaved",
+             mscale: float = 1.0, inverse: bool = False, cu_seqlens=None, pos_stride: int = 1,
+             out=None, stream=None):
+    """Rotary positions over ``2 * inv_freq.numel()`` dims of every head of x
+    [T, H, D] or [T, D] (bf16 or fp32, contiguous rows), starting at
+    ``rope_offset`` (None: the head's last dims); other dims are copied.
+
+    ``positions`` [T] int32, or None with ``cu_seqlens`` [batch+1]: the place
+    in the packed sequence; both times ``pos_stride``. ``inverse`` turns back,
+    which is also the backward. ``out`` may be ``x``. Returns out."""
+    code, x_stride = _rows(x, "x", (2, 3))
+    _need(positions, "positions", torch.int32, 1)
+    _need(cu_seqlens, "cu_seqlens", torch.int32, 1)
+    _need(inv_freq, "inv_freq", torch.float64, 1)
+    T, D = x.shape[0], x.shape[-1]
+    H = x.shape[1] if x.dim() == 3 else 1
+    _shape(positions, "positions", (T,))
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    elif out.dtype != x.dtype:
+        raise TypeError(f"out must be {x.dtype}, got {out.dtype}")
+    _shape(out, "out", tuple(x.shape))
+    out_stride = _rows(out, "out", (2, 3))[1]
+    n = 2 * inv_freq.numel()
+    off = D - n if rope_offset is None else int(rope_offset)
+    with _Device(x, positions, cu_seqlens, inv_freq, out):
+        _check(lib().csa_rope(
+            _ptr(x), code, x_stride, _ptr(positions), _ptr(cu_seqlens),
+            0 if cu_seqlens is None else cu_seqlens.numel() - 1, int(pos_stride), _ptr(inv_freq),
+            T, H, D, off, n, _layout(layout), float(mscale), 1 if inverse else 0, _ptr(out),
+            out_stride, _stream(stream)), "csa_rope")
+    return out
+
+
+def csa_cache_append(rows, row_seq, row_pos, pages, cache, inv_freq=None, rope_offset=None,
+                     layout: str = "interleaved", mscale: float = 1.0, pos_stride: int = 1,
+                     stream=None):
+    """Writes rows [T, width] (bf16 or fp32, contiguous rows) to the slots of
+    positions ``row_pos`` [T] of sequences ``row_seq`` [T] (None: row t is
+    sequence t's) in the paged ``cache`` [num_pages, page_size, width] bf16
+    with table ``pages`` [batch, max_pages], rotated as :func:`csa_rope` does
+    at ``row_pos * pos_stride`` when ``inv_freq`` is given. A negative
+    position skips the row. Returns cache."""
+    code, stride = _rows(rows, "rows", (2,))
+    _need(row_seq, "row_seq", torch.int32, 1)
+    _need(row_pos, "row_pos", torch.int32, 1)
+    _need(pages, "pages", torch.int32, 2)
+    _need(cache, "cache", torch.bfloat16, 3)
+    _need(inv_freq, "inv_freq", torch.float64, 1)
+    T, width = rows.shape
+    _shape(row_seq, "row_seq", (T,))
+    _shape(row_pos, "row_pos", (T,))
+    _shape(cache, "cache", (cache.shape[0], cache.shape[1], width))
+    n = 0 if inv_freq is None else 2 * inv_freq.numel()
+    off = width - n if rope_offset is None else int(rope_offset)
+    with _Device(rows, row_seq, row_pos, pages, cache, inv_freq):
+        _check(lib().csa_cache_append(
+            _ptr(rows), code, stride, _ptr(row_seq), _ptr(row_pos), _ptr(pages), pages.shape[0],
+            pages.shape[1], cache.shape[0], cache.shape[1], T, width, _ptr(inv_freq),
+            off, n, _layout(layout), float(mscale), int(pos_stride), _ptr(cache),
+            _stream(stream)), "csa_cache_append")
+    return cache
+
+
+def csa_indexer_topk_paged_workspace_size(total_tokens, max_rows, index_heads, index_dim,
+                                          topk) -> int:
+    return int(lib().csa_indexer_topk_paged_workspace_size(
+        int(total_tokens), int(max_rows), int(index_heads), int(index_dim), int(topk)))
+
+
+def csa_indexer_topk_paged(q, k_cache, w, pages, q_seq, q_pos, cmp_ratio: int, topk: int,
+                           return_value: bool = False, workspace=None, out=None, out_val=None,
+                           stream=None):
+    """Lightning-indexer top-k of new tokens q [T, Hi, Di], w [T, Hi] at
+    positions ``q_pos`` [T] (negative: padding) of sequences ``q_seq`` [T]
+    (None: token t is sequence t's) over the paged rows ``k_cache``
+    [num_pages, page_size, Di] with table ``pages`` [batch, max_pages].
+
+    Returns ``(topk_idx [T, topk] int32 rows of the sequence, -1 padded,
+    topk_val [T, topk] fp32 or None)``."""
+    _need(q, "q", torch.bfloat16, 3)
+    _need(k_cache, "k_cache", torch.bfloat16, 3)
+    _need(w, "w", torch.float32, 2)
+    _need(pages, "pages", torch.int32, 2)
+    _need(q_seq, "q_seq", torch.int32, 1)
+    _need(q_pos, "q_pos", torch.int32, 1)
+    T, Hi, Di = q.shape
+    topk = int(topk)
+    _shape(w, "w", (T, Hi))
+    _shape(q_seq, "q_seq", (T,))
+    _shape(q_pos, "q_pos", (T,))
+    n_pages, page, _ = k_cache.shape
+    _shape(k_cache, "k_cache", (n_pages, page, Di))
+    B, max_pages = pages.shape
+    if out is None:
+        out = torch.empty((T, max(topk, 0)), dtype=torch.int32, device=q.device)
+    if return_value and out_val is None:
+        out_val = torch.empty((T, max(topk, 0)), dtype=torch.float32, device=q.device)
+    _need(out, "out", torch.int32, 2)
+    _shape(out, "out", (T, topk))
+    if return_value:
+        _need(out_val, "out_val", torch.float32, 2)
+        _shape(out_val, "out_val", (T, topk))
+    need = csa_indexer_topk_paged_workspace_size(T, max_pages * page, Hi, Di, topk)
+    workspace, ws_bytes = _workspace(need, q.device, workspace)
+    with _Device(q, k_cache, w, pages, q_seq, q_pos, workspace, out, out_val):
+        _check(lib().csa_indexer_topk_paged(
+            _ptr(q), _ptr(k_cache), _ptr(w), _ptr(pages), _ptr(q_seq), _ptr(q_pos), B, T, Hi, Di,
+            n_pages, page, max_pages, int(cmp_ratio), topk, _ptr(out),
+            _ptr(out_val) if return_value else None, _ptr(workspace), ws_bytes,
+            _stream(stream)), "csa_indexer_topk_paged")
+    return out, (out_val if return_value else None)
+
+
+def csa_sparse_mla_paged_workspace_size(total_tokens, heads) -> int:
+    return int(lib().csa_sparse_mla_paged_workspace_size(int(total_tokens), int(heads)))
+
+
+def csa_sparse_mla_paged(q, ori_cache, cmp_cache, cmp_sparse_indices, ori_pages, cmp_pages, q_seq,
+                         q_pos, sinks, softmax_scale: float, cmp_ratio: int, ori_win_left: int,
+                         ori_win_right: int = 0, return_softmax_lse: bool = False,
+                         workspace=None, out=None, lse=None, stream=None):
+    """Sparse MLA attention of new tokens q [T, H, 512] at positions ``q_pos``
+    [T] (negative: padding) of sequences ``q_seq`` [T] (None: token t is
+    sequence t's) over the window rows of ``ori_cache`` [pages, page_size,
+    512] and the rows of ``cmp_cache`` listed in ``cmp_sparse_indices`` [T,
+    topk] (rows of the sequence; None: every visible row), each with its page
+    table [batch, max_pages]. ``cmp_cache`` None: window only.
+
+    Returns ``(out [T, H, 512], lse [T, H] or None)``."""
+    _need(q, "q", torch.bfloat16, 3)
+    _need(ori_cache, "ori_cache", torch.bfloat16, 3)
+    _need(cmp_cache, "cmp_cache", torch.bfloat16, 3)
+    _need(cmp_sparse_indices, "cmp_sparse_indices", torch.int32, 2)
+    _need(ori_pages, "ori_pages", torch.int32, 2)
+    _need(cmp_pages, "cmp_pages", torch.int32, 2)
+    _need(q_seq, "q_seq", torch.int32, 1)
+    _need(q_pos, "q_pos", torch.int32, 1)
+    _need(sinks, "sinks", torch.float32, 1)
+    T, H, D = q.shape
+    B, ori_max = ori_pages.shape
+    ori_n, ori_page, _ = ori_cache.shape
+    cmp_n = cmp_page = cmp_max = topk = 0
+    if cmp_cache is not None:
+        if cmp_pages is None:
+            raise ValueError("cmp_cache needs cmp_pages")
+        cmp_n, cmp_page, _ = cmp_cache.shape
+        cmp_max = cmp_pages.shape[1]
+        _shape(cmp_cache, "cmp_cache", (cmp_n, cmp_page, D))
+        _shape(cmp_pages, "cmp_pages", (B, cmp_max))
+        if cmp_sparse_indices is not None:
+            topk = cmp_sparse_indices.shape[1]
+            _shape(cmp_sparse_indices, "cmp_sparse_indices", (T, topk))
+    _shape(ori_cache, "ori_cache", (ori_n, ori_page, D))
+    _shape(q_seq, "q_seq", (T,))
+    _shape(q_pos, "q_pos", (T,))
+    _shape(sinks, "sinks", (H,))
+    if out is None:
+        out = torch.empty_like(q)
+    if return_softmax_lse and lse is None:
+        lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
+    _need(out, "out", torch.bfloat16, 3)
+    _shape(out, "out", (T, H, D))
+    if return_softmax_lse:
+        _need(lse, "lse", torch.float32, 2)
+        _shape(lse, "lse", (T, H))
+    workspace, ws_bytes = _workspace(csa_sparse_mla_paged_workspace_size(T, H), q.device, workspace)
+    with _Device(q, ori_cache, cmp_cache, cmp_sparse_indices, ori_pages, cmp_pages, q_seq, q_pos,
+                 sinks, workspace, out, lse):
+        _check(lib().csa_sparse_mla_paged(
+            _ptr(q), _ptr(ori_cache), _ptr(cmp_cache), _ptr(cmp_sparse_indices), _ptr(ori_pages),
+            _ptr(cmp_pages), _ptr(q_seq), _ptr(q_pos), B, T, H, D, ori_n, ori_page, ori_max,
+            cmp_n, cmp_page, cmp_max, topk, _ptr(sinks), float(softmax_scale), int(cmp_ratio),
+            int(ori_win_left), int(ori_win_right), _ptr(out),
+            _ptr(lse) if return_softmax_lse else None, 1 if return_softmax_lse else 0,
+            _ptr(workspace), ws_bytes, _stream(stream)), "csa_sparse_mla_paged")
+    return out, (lse if return_softmax_lse else None)
 
 
 def csa_device_error(stream=None):

@@ -27,6 +27,10 @@ enum KernelId : int32_t {
     kKerIndexerKl = 6,
     kKerBsnd = 7,
     kKerCompressor = 8,
+    kKerRope = 9,
+    kKerAppend = 10,
+    kKerIndexerPaged = 11,
+    kKerMlaPaged = 12,
 };
 
 __device__ __forceinline__ void report_error(int32_t *err, int32_t kind, int32_t kernel,

@@ -1,0 +1,118 @@
+// Internal launchers of the rotation and of the paged-cache operators. The
+// arguments are already validated by paged_api.cu.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "csa.h"
+
+namespace csa {
+
+struct RopeFreqsArgs {
+    double theta, factor, beta_fast, beta_slow;
+    int32_t rope_dim, original_len;
+    double *inv_freq;  // [rope_dim / 2]
+};
+
+cudaError_t launch_rope_freqs(const RopeFreqsArgs &a, cudaStream_t stream);
+
+struct RopeArgs {
+    const void *x;             // [T, H, D], token stride x_stride
+    void *out;                 // [T, H, D], token stride out_stride
+    const int32_t *positions;  // [T] or nullptr
+    const int32_t *cu;         // [batch+1] when positions is nullptr
+    const double *inv_freq;    // [n / 2] radians per position
+    int32_t *err;
+    int64_t x_stride, out_stride;  // elements
+    int32_t T, H, D, off, n, batch, pos_stride;
+    int32_t f32, half, inverse;
+    float mscale;
+};
+
+cudaError_t launch_rope(const RopeArgs &a, cudaStream_t stream);
+
+struct AppendArgs {
+    const void *rows;         // [T, D], row stride row_stride
+    const int32_t *row_seq;   // [T] or nullptr (row t belongs to sequence t)
+    const int32_t *row_pos;   // [T], negative: skipped
+    const int32_t *pages;     // [batch, max_pages]
+    const double *inv_freq;   // [n / 2] or nullptr (n = 0)
+    __nv_bfloat16 *cache;     // [num_pages, page_size, D]
+    int32_t *err;
+    int64_t row_stride;
+    int32_t T, D, off, n, pos_stride;
+    int32_t batch, max_pages, num_pages, page_size;
+    int32_t f32, half;
+    float mscale;
+};
+
+cudaError_t launch_cache_append(const AppendArgs &a, cudaStream_t stream);
+
+// One paged row cache as the kernels see it.
+struct PagedRows {
+    const __nv_bfloat16 *base;  // [num_pages, page_size, width]
+    const int32_t *pages;       // [batch, max_pages]
+    int32_t num_pages, page_size, max_pages;
+};
+
+struct IndexerPagedArgs {
+    const __nv_bfloat16 *q;  // [T, Hi, Di]
+    PagedRows k;             // width Di
+    const float *w;          // [T, Hi]
+    const int32_t *q_seq;    // [T] or nullptr
+    const int32_t *q_pos;    // [T]
+    int32_t *topk_idx;       // [T, topk]
+    float *topk_val;         // [T, topk] or nullptr
+    float *scores;           // workspace: [T, row_pad] scores
+    int32_t *err;
+    int32_t T, Hi, Di, batch, cmp_ratio, topk, max_rows;
+    int64_t row_pad;         // floats between two tokens' scores
+};
+
+size_t indexer_paged_workspace_bytes(int32_t T, int64_t max_rows);
+cudaError_t launch_indexer_topk_paged(IndexerPagedArgs a, cudaStream_t stream);
+
+struct MlaPagedArgs {
+    const __nv_bfloat16 *q;  // [T, H, 512]
+    PagedRows ori;           // width 512
+    PagedRows cmp;           // width 512; base nullptr: window only
+    const int32_t *idx;      // [T, topk] or nullptr (every visible row)
+    const int32_t *q_seq;    // [T] or nullptr
+    const int32_t *q_pos;    // [T]
+    const float *sinks;      // [H] or nullptr
+    __nv_bfloat16 *out;      // [T, H, 512]
+    float *lse;              // [T, H] or nullptr
+    void *workspace;
+    int32_t *err;
+    int32_t T, H, batch, topk, cmp_ratio, window;
+    float softmax_scale;
+    uint64_t wait_ns;
+};
+
+size_t mla_paged_workspace_bytes(int32_t T, int32_t H);
+cudaError_t launch_sparse_mla_paged(MlaPagedArgs a, cudaStream_t stream);
+
+#ifdef __CUDACC__
+// Row of the pool (in rows) holding logical row r of sequence b, or -1 when
+// the table has no page for it or names one outside the pool.
+__device__ __forceinline__ int64_t paged_row(const PagedRows &p, int32_t b, int32_t r) {
+    const uint32_t pg = (uint32_t)r / (uint32_t)p.page_size;
+    if (pg >= (uint32_t)p.max_pages) return -1;
+    const int32_t phys = __ldg(p.pages + (int64_t)b * p.max_pages + pg);
+    if ((uint32_t)phys >= (uint32_t)p.num_pages) return -1;
+    return (int64_t)phys * p.page_size + (r - (int32_t)pg * p.page_size);
+}
+
+// Sequence of token t: -1 for a padding slot (negative position), -2 when the
+// sequence number is outside the batch.
+__device__ __forceinline__ int32_t paged_seq(const int32_t *q_seq, int32_t batch, int32_t t,
+                                             int32_t pos) {
+    if (pos < 0) return -1;
+    const int32_t b = q_seq ? __ldg(q_seq + t) : t;
+    return (uint32_t)b < (uint32_t)batch ? b : -2;
+}
+#endif
+
+}  // namespace csa

@@ -1,0 +1,285 @@
+// Rotary positions over part of a head, and the same rotation on the way into
+// a paged row cache (sm_103a).
+//
+//     theta = p f_i (radians; p the position, f_i in 64 bits)
+//     y_a = m (x_a cos theta - x_b sin theta)
+//     y_b = m (x_b cos theta + x_a sin theta)
+// for the pairs (a, b) of the rotary part: neighbours (interleaved) or i and
+// i + n/2 (half). The inverse turns by -theta, which for m > 0 is the
+// transpose of the forward map, hence also its backward.
+//
+// Memory bound: a block first turns its tokens' angles into a shared table of
+// (cos, sin), computed once for all heads of a token, and then streams 16-byte
+// pieces. Angles: p f_i is formed and reduced to a fraction of a turn in 64
+// bits (at p = 2^20 a 32-bit product is off by up to 2^-5 radians); the
+// fraction, at most half a turn, is then exact to 2^-25 in 32 bits, and
+// sincospif gives the factors.
+#include "common.cuh"
+#include "internal.h"
+#include "paged.h"
+
+namespace csa {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kTable = 2048;    // (cos, sin) pairs per block: 16 KB
+constexpr int kMaxRows = 128;   // tokens per block
+
+__device__ __forceinline__ float2 cos_sin(int64_t p, double f, float sign, float m) {
+    double turns = (double)p * f * 0.15915494309189533577;  // / 2 pi
+    turns -= rint(turns);
+    float s, c;
+    sincospif(2.0f * (float)turns, &s, &c);
+    return make_float2(m * c, m * sign * s);
+}
+
+// V consecutive elements <-> fp32
+template <typename T, int V>
+__device__ __forceinline__ void load_v(const T *p, float (&v)[V]) {
+    if constexpr (V == 1) {
+        v[0] = (float)p[0];
+    } else if constexpr (sizeof(T) == 2) {
+        static_assert(V == 8, "16 bytes of bf16");
+        const uint4 u = *reinterpret_cast<const uint4 *>(p);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __uint_as_float(w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i) {
+            const float4 u = reinterpret_cast<const float4 *>(p)[i];
+            v[4 * i] = u.x;
+            v[4 * i + 1] = u.y;
+            v[4 * i + 2] = u.z;
+            v[4 * i + 3] = u.w;
+        }
+    }
+}
+
+// rounded to nearest even once, on the way out
+template <typename T, int V>
+__device__ __forceinline__ void store_v(T *p, const float (&v)[V]) {
+    if constexpr (V == 1) {
+        p[0] = (T)v[0];
+    } else if constexpr (sizeof(T) == 2) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t *>(&b);
+        }
+        *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i)
+            reinterpret_cast<float4 *>(p)[i] =
+                make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    }
+}
+
+// V pairs, from pair j of the rotary part (x and y point at its first
+// element), turned by tab[j ..]. Interleaved: elements 2j .. 2j + 2V; half:
+// j .. j + V and n/2 + j .. n/2 + j + V.
+template <typename Ti, typename To, int V, bool HALF>
+__device__ __forceinline__ void turn_pairs(const Ti *x, To *y, const float2 *tab, int j, int n) {
+    const int i0 = HALF ? j : 2 * j, i1 = HALF ? n / 2 + j : 2 * j + V;
+    float u[V], v[V];
+    load_v<Ti, V>(x + i0, u);
+    load_v<Ti, V>(x + i1, v);
+    auto one = [&](float &a, float &b, float2 cs) {
+        const float ra = fmaf(a, cs.x, -b * cs.y), rb = fmaf(b, cs.x, a * cs.y);
+        a = ra;
+        b = rb;
+    };
+    if constexpr (HALF || V == 1) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) one(u[e], v[e], tab[j + e]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < V; e += 2) {
+            one(u[e], u[e + 1], tab[j + e / 2]);
+            one(v[e], v[e + 1], tab[j + V / 2 + e / 2]);
+        }
+    }
+    store_v<To, V>(y + i0, u);
+    store_v<To, V>(y + i1, v);
+}
+
+__global__ void rope_freqs_kernel(RopeFreqsArgs a) {
+    const int i = blockIdx.x * blockDim.x + threadIdx.x, half = a.rope_dim / 2;
+    if (i >= half) return;
+    const double f = pow(a.theta, -2.0 * i / a.rope_dim);
+    double g = f / a.factor;
+    if (a.original_len > 0) {
+        // By parts: pairs turning more than beta_fast times over the original
+        // length keep their frequency, those turning less than beta_slow times
+        // are stretched by the factor, and a ramp over the pair index joins them.
+        const double two_pi = 6.283185307179586477, lt = 2.0 * log(a.theta);
+        const double lo = floor(a.rope_dim * log(a.original_len / (a.beta_fast * two_pi)) / lt);
+        const double hi = ceil(a.rope_dim * log(a.original_len / (a.beta_slow * two_pi)) / lt);
+        const double l = fmax(lo, 0.0), h = fmin(hi, a.rope_dim - 1.0);
+        const double ramp = fmin(fmax((i - l) / fmax(h - l, 1e-3), 0.0), 1.0);
+        g = g * ramp + f * (1.0 - ramp);
+    }
+    a.inv_freq[i] = g;
+}
+
+// Block: `tb` tokens x `hb` heads.
+template <typename T, int V, bool HALF>
+__global__ void __launch_bounds__(kThreads) rope_kernel(RopeArgs a, int tb, int hb) {
+    __shared__ float2 tab[kTable];
+    const int32_t t0 = blockIdx.x * tb, h0 = blockIdx.y * hb;
+    const int nt = min(tb, a.T - t0), nh = min(hb, a.H - h0), np = a.n / 2;
+    const float sign = a.inverse ? -1.0f : 1.0f;
+    for (int i = threadIdx.x; i < nt * np; i += kThreads) {
+        const int r = i / np;
+        const int32_t t = t0 + r;
+        int64_t p = 0;
+        if (a.positions) {
+            p = __ldg(a.positions + t);
+        } else {
+            const int32_t b = find_segment(a.cu, a.batch, t);
+            if (b >= 0)
+                p = t - __ldg(a.cu + b);
+            else
+                report_error(a.err, kErrCheck, kKerRope, 1);
+        }
+        tab[i] = cos_sin(p * a.pos_stride, __ldg(a.inv_freq + (i - r * np)), sign, a.mscale);
+    }
+    __syncthreads();
+    const T *x = static_cast<const T *>(a.x) + (int64_t)h0 * a.D;
+    T *y = static_cast<T *>(a.out) + (int64_t)h0 * a.D;
+    const int ur = np / V, rows = nt * nh;  // turned units per (token, head)
+    for (int i = threadIdx.x; i < rows * ur; i += kThreads) {
+        const int row = i / ur, u = i - row * ur, r = row / nh, h = row - r * nh;
+        const int64_t o = (int64_t)h * a.D + a.off;
+        turn_pairs<T, T, V, HALF>(x + (t0 + r) * a.x_stride + o, y + (t0 + r) * a.out_stride + o,
+                                  tab + r * np, u * V, a.n);
+    }
+    if (a.x == a.out) return;
+    const int uc = (a.D - a.n) / V;  // copied units
+    for (int i = threadIdx.x; i < rows * uc; i += kThreads) {
+        const int row = i / uc, u = i - row * uc, r = row / nh, h = row - r * nh;
+        const int e = u * V < a.off ? u * V : u * V + a.n;
+        const int64_t o = (int64_t)h * a.D + e;
+        float v[V];
+        load_v<T, V>(x + (t0 + r) * a.x_stride + o, v);
+        store_v<T, V>(y + (t0 + r) * a.out_stride + o, v);
+    }
+}
+
+// Block: `tb` rows. Rows whose slot cannot be named are skipped.
+template <typename T, int V, bool HALF>
+__global__ void __launch_bounds__(kThreads) cache_append_kernel(AppendArgs a, int tb) {
+    __shared__ float2 tab[kTable];
+    __shared__ int64_t slot[kMaxRows];
+    const int32_t t0 = blockIdx.x * tb;
+    const int nt = min(tb, a.T - t0), np = a.n / 2;
+    for (int r = threadIdx.x; r < nt; r += blockDim.x) {
+        const int32_t p = __ldg(a.row_pos + t0 + r);
+        const int32_t b = paged_seq(a.row_seq, a.batch, t0 + r, p);
+        int64_t s = -1;
+        if (b >= 0) s = paged_row({a.cache, a.pages, a.num_pages, a.page_size, a.max_pages}, b, p);
+        if (b == -2 || (b >= 0 && s < 0)) report_error(a.err, kErrCheck, kKerAppend, b < 0 ? 1 : 2);
+        slot[r] = s;
+    }
+    for (int i = threadIdx.x; i < nt * np; i += blockDim.x) {
+        const int r = i / np;
+        const int64_t p = __ldg(a.row_pos + t0 + r);
+        tab[i] = cos_sin(p * a.pos_stride, __ldg(a.inv_freq + (i - r * np)), 1.0f, a.mscale);
+    }
+    __syncthreads();
+    const T *x = static_cast<const T *>(a.rows);
+    const int ur = np / V, uc = (a.D - a.n) / V;
+    for (int i = threadIdx.x; i < nt * ur; i += blockDim.x) {
+        const int r = i / ur, u = i - r * ur;
+        if (slot[r] >= 0)
+            turn_pairs<T, __nv_bfloat16, V, HALF>(x + (t0 + r) * a.row_stride + a.off,
+                                                  a.cache + slot[r] * a.D + a.off, tab + r * np,
+                                                  u * V, a.n);
+    }
+    for (int i = threadIdx.x; i < nt * uc; i += blockDim.x) {
+        const int r = i / uc, u = i - r * uc;
+        const int e = u * V < a.off ? u * V : u * V + a.n;
+        if (slot[r] < 0) continue;
+        float v[V];
+        load_v<T, V>(x + (t0 + r) * a.row_stride + e, v);
+        store_v<__nv_bfloat16, V>(a.cache + slot[r] * a.D + e, v);
+    }
+}
+
+bool aligned(const void *p, int64_t stride_bytes) {
+    return ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)stride_bytes) & 15u) == 0;
+}
+
+}  // namespace
+
+cudaError_t launch_rope_freqs(const RopeFreqsArgs &a, cudaStream_t stream) {
+    rope_freqs_kernel<<<(a.rope_dim / 2 + 63) / 64, 64, 0, stream>>>(a);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_rope(const RopeArgs &a, cudaStream_t stream) {
+    const int es = a.f32 ? 4 : 2, V = 16 / es;
+    // 16-byte pieces when every row and both parts of it start on 16 bytes
+    const bool vec = aligned(a.x, a.x_stride * es) && aligned(a.out, a.out_stride * es) &&
+                     a.D % V == 0 && a.off % V == 0 && a.n % (2 * V) == 0;
+    const int units = (a.x == a.out ? a.n : a.D) / (vec ? V : 1);
+    // rows (token, head) per block: about eight units a thread, fewer while
+    // that leaves SMs without a block
+    int64_t rows = max(1, 8 * kThreads / max(units, 1));
+    rows = min(rows, max((int64_t)1, (int64_t)a.T * a.H / 304));
+    const int hb = (int)min((int64_t)a.H, rows);
+    const int tb = (int)max((int64_t)1, min(min(rows / hb, (int64_t)kMaxRows), (int64_t)(kTable / (a.n / 2))));
+    const dim3 grid((a.T + tb - 1) / tb, (a.H + hb - 1) / hb);
+#define CSA_ROPE(T, VV)                                                          \
+    do {                                                                         \
+        if (a.half)                                                              \
+            rope_kernel<T, VV, true><<<grid, kThreads, 0, stream>>>(a, tb, hb);  \
+        else                                                                     \
+            rope_kernel<T, VV, false><<<grid, kThreads, 0, stream>>>(a, tb, hb); \
+    } while (0)
+    if (a.f32) {
+        if (vec) CSA_ROPE(float, 4);
+        else CSA_ROPE(float, 1);
+    } else {
+        if (vec) CSA_ROPE(__nv_bfloat16, 8);
+        else CSA_ROPE(__nv_bfloat16, 1);
+    }
+#undef CSA_ROPE
+    return cudaGetLastError();
+}
+
+cudaError_t launch_cache_append(const AppendArgs &a, cudaStream_t stream) {
+    const int es = a.f32 ? 4 : 2;
+    const bool vec = aligned(a.rows, a.row_stride * es) && aligned(a.cache, a.D * 2) &&
+                     a.D % 8 == 0 && a.off % 8 == 0 && a.n % 16 == 0;
+    const int units = a.D / (vec ? 8 : 1);
+    int rows = max(1, 4 * kThreads / max(units, 1));
+    rows = min(rows, max(1, a.T / 304));
+    int tb = min(rows, kMaxRows);
+    if (a.n > 0) tb = max(1, min(tb, kTable / (a.n / 2)));
+    const dim3 grid((a.T + tb - 1) / tb);
+#define CSA_APPEND(T, VV)                                                          \
+    do {                                                                           \
+        if (a.half)                                                                \
+            cache_append_kernel<T, VV, true><<<grid, kThreads, 0, stream>>>(a, tb); \
+        else                                                                       \
+            cache_append_kernel<T, VV, false><<<grid, kThreads, 0, stream>>>(a, tb); \
+    } while (0)
+    if (a.f32) {
+        if (vec) CSA_APPEND(float, 8);
+        else CSA_APPEND(float, 1);
+    } else {
+        if (vec) CSA_APPEND(__nv_bfloat16, 8);
+        else CSA_APPEND(__nv_bfloat16, 1);
+    }
+#undef CSA_APPEND
+    return cudaGetLastError();
+}
+
+}  // namespace csa
