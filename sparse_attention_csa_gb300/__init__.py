@@ -139,8 +139,8 @@ def _ptr(t):
 
 
 def _stream(stream):
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:  # the current device's current stream
+        return _vp(torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()))
     return _vp(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
@@ -495,7 +495,7 @@ class _Device:
         self.back = None
 
     def __enter__(self):
-        cur = torch.cuda.current_device()
+        cur = torch._C._cuda_getDevice()
         if cur != self.index:
             self.back = cur
             torch.cuda.set_device(self.index)
