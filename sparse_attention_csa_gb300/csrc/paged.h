@@ -69,6 +69,7 @@ struct IndexerPagedArgs {
     int32_t *err;
     int32_t T, Hi, Di, batch, cmp_ratio, topk, max_rows;
     int64_t row_pad;         // floats between two tokens' scores
+    uint64_t wait_ns;
 };
 
 size_t indexer_paged_workspace_bytes(int32_t T, int64_t max_rows);

@@ -202,6 +202,7 @@ csa_status_t csa_indexer_topk_paged(const csa_bf16_t *q, const csa_bf16_t *k_cac
     a.cmp_ratio = cmp_ratio;
     a.topk = topk;
     a.max_rows = a.k.max_pages > 0 ? (int32_t)max_rows : 0;
+    a.wait_ns = csa::pipeline_wait_limit_ns();
     return from_cuda(csa::launch_indexer_topk_paged(a, (cudaStream_t)stream));
 }
 
