@@ -133,7 +133,7 @@ indexer_paged_score_kernel(const __grid_constant__ IndexerPagedArgs a) {
 
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
-            tc::mbar_init(&ms->q_full[i], kLoaders + 4);
+            tc::mbar_init(&ms->q_full[i], kLoaders);
             tc::mbar_init(&ms->q_empty[i], 1 + 128);
         }
         for (int i = 0; i < S::kStages; ++i) {
@@ -159,6 +159,7 @@ indexer_paged_score_kernel(const __grid_constant__ IndexerPagedArgs a) {
         *reinterpret_cast<uint4 *>(smem + S::kOffQ + buf * S::kQ + (u >> 3) * 8192 + h * 128 +
                                    (u & 7) * 16) = make_uint4(0, 0, 0, 0);
     }
+    if (tid < 128) ms->w[tid >> 6][tid & 63] = 0.0f;
     // everything above is local: wait for the kernels before this one
     grid_dependency_wait();
     launch_dependents();
@@ -181,7 +182,7 @@ indexer_paged_score_kernel(const __grid_constant__ IndexerPagedArgs a) {
     }
     tc::tc_fence_after();
     const uint32_t tmem = ms->tmem_base;
-    const int64_t per = (N + gridDim.x - 1) / gridDim.x;
+    const int64_t per = div64(N + gridDim.x - 1, gridDim.x);
     const int64_t s = min(c * per, N), e = min(s + per, N);
     if (s == e) {  // no run left for this CTA
         __syncthreads();
@@ -298,10 +299,12 @@ indexer_paged_score_kernel(const __grid_constant__ IndexerPagedArgs a) {
                                    (((y & 7) ^ (h & 7)) << 4),
                                q + (int64_t)u * 8, 16);
                 }
-                if (li < 64) ms->w[np & 1][li] = li < a.Hi ? __ldg(a.w + (int64_t)p.t * a.Hi + li) : 0.0f;
+                if (li < a.Hi)  // weights past Hi stay zero
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(
+                                     tc::smem_u32(&ms->w[np & 1][li])),
+                                 "l"(a.w + (int64_t)p.t * a.Hi + li)
+                                 : "memory");
                 cp_async_arrive(&ms->q_full[np & 1]);
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&ms->q_full[np & 1]);
                 ++np;
                 for (int32_t j = p.j0; j < p.j1; ++j, ++g) {
                     const uint32_t st = g % S::kStages;
@@ -412,16 +415,28 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// 32 bits of CTA `rank`'s shared memory, at this CTA's address p
-__device__ __forceinline__ uint32_t peer_u32(const void *p, uint32_t rank) {
-    uint32_t at, v;
+// 4 or 16 bytes of CTA `rank`'s shared memory, at this CTA's address p
+__device__ __forceinline__ uint32_t peer_addr(const void *p, uint32_t rank) {
+    uint32_t at;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(tc::smem_u32(p)), "r"(rank));
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    return at;
+}
+__device__ __forceinline__ uint32_t peer_u32(const void *p, uint32_t rank) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(peer_addr(p, rank)) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint4 peer_u128(const void *p, uint32_t rank) {
+    uint4 v;
+    asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(peer_addr(p, rank))
+                 : "memory");
     return v;
 }
 
 struct Sel {
-    uint32_t hist[kBins];
+    alignas(16) uint32_t hist[kBins];
     uint32_t digit[2][256];
     uint32_t cand[kCand];
     uint32_t all[kCand];
@@ -430,13 +445,14 @@ struct Sel {
     uint32_t counts[2];     // this CTA's rows above the threshold and on it
     uint32_t pick[3];
     int32_t scan[kSelThreads / 32 + 1];
-    uint32_t warp_gt[kSelThreads / 32], warp_eq[kSelThreads / 32];
+    uint32_t warps[kSelThreads / 32];
 };
 
-// kHeld: the CTA's share fits its registers; else every sweep reads it again.
-template <bool kHeld>
+// C CTAs a token. kHeld: a CTA's share fits its registers; else every sweep
+// reads it again.
+template <int C, bool kHeld>
 __global__ void __launch_bounds__(kSelThreads, 2)
-indexer_paged_select_kernel(const __grid_constant__ IndexerPagedArgs a, int32_t C) {
+indexer_paged_select_kernel(const __grid_constant__ IndexerPagedArgs a, int32_t after_scores) {
     __shared__ Sel sm;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = C > 1 ? cluster_rank() : 0;
@@ -445,20 +461,26 @@ indexer_paged_select_kernel(const __grid_constant__ IndexerPagedArgs a, int32_t 
         if (C > 1) cluster_sync();
         else __syncthreads();
     };
-    auto peer = [&](const void *p, uint32_t r) {
-        return C > 1 ? peer_u32(p, r) : *static_cast<const volatile uint32_t *>(p);
+    // one word of every CTA, CTA r's in lane r (`none` in the other lanes)
+    auto gather = [&](const uint32_t *p, uint32_t none) -> uint32_t {
+        if (lane >= C) return none;
+        return C > 1 ? peer_u32(p, lane) : *static_cast<const volatile uint32_t *>(p);
     };
     for (int i = tid; i < kBins; i += kSelThreads) sm.hist[i] = 0;
     if (tid < 256) sm.digit[0][tid] = 0;
+    if (tid < 2) sm.counts[tid] = 0;
     if (tid == 0) {
         sm.n_cand = 0;
         sm.range[0] = 0xffffffffu;
         sm.range[1] = 0u;
     }
-    grid_dependency_wait();
-    launch_dependents();
+    // The score kernel lets this one start only after its own wait for the
+    // kernels before it: behind it, the positions are there already.
+    if (!after_scores) grid_dependency_wait();
     int32_t seq;
     const int32_t n = visible_rows(a, t, &seq, tid == 0 && rank == 0);
+    if (after_scores) grid_dependency_wait();
+    launch_dependents();
     const float *sc = a.scores + (int64_t)t * a.row_pad;
     int32_t *idx = a.topk_idx + (int64_t)t * K;
     float *val = a.topk_val ? a.topk_val + (int64_t)t * K : nullptr;
@@ -484,8 +506,7 @@ indexer_paged_select_kernel(const __grid_constant__ IndexerPagedArgs a, int32_t 
                              : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         }
     };
-    // f(i, e, row, score) for every row of a chunk that exists
-    auto each = [&](int32_t c0, auto f) {
+    auto each = [&](int32_t c0, auto f) {  // every row of a chunk that exists
 #pragma unroll
         for (int i = 0; i < kQuads; ++i) {
             const int32_t r = row_at(c0, i);
@@ -505,8 +526,8 @@ indexer_paged_select_kernel(const __grid_constant__ IndexerPagedArgs a, int32_t 
             }
         }
     };
-    __syncthreads();
     if (kHeld) fetch(r0);
+    __syncthreads();
     // ---- smallest and largest key
     {
         uint32_t lo = 0xffffffffu, hi = 0u;
@@ -523,11 +544,8 @@ indexer_paged_select_kernel(const __grid_constant__ IndexerPagedArgs a, int32_t 
         }
     }
     sync();
-    uint32_t lo = 0xffffffffu, hi = 0u;
-    for (int32_t r = 0; r < C; ++r) {
-        lo = min(lo, peer(&sm.range[0], r));
-        hi = max(hi, peer(&sm.range[1], r));
-    }
+    const uint32_t lo = __reduce_min_sync(0xffffffffu, gather(&sm.range[0], 0xffffffffu));
+    const uint32_t hi = __reduce_max_sync(0xffffffffu, gather(&sm.range[1], 0u));
     auto key_float = [](uint32_t k) { return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k); };
     const float fl = key_float(lo), span = key_float(hi) - fl;
     // no bins without a finite, positive span: all rows are candidates of bin 0
@@ -540,20 +558,24 @@ indexer_paged_select_kernel(const __grid_constant__ IndexerPagedArgs a, int32_t 
     sweep([&](float s) { atomicAdd(&sm.hist[bin_of(s)], 1u); });
     sync();
     {
-        int32_t c4[4], local = 0;  // bins 2047 - 4 tid downwards
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            c4[e] = 0;
-            for (int32_t r = 0; r < C; ++r) c4[e] += (int32_t)peer(&sm.hist[kBins - 1 - 4 * tid - e], r);
-            local += c4[e];
-        }
         static_assert(kBins == 4 * kSelThreads, "four bins a thread");
+        const int top = kBins - 1 - 4 * tid;  // this thread's bins: top, top - 1, top - 2, top - 3
+        int32_t c4[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int r = 0; r < C; ++r) {
+            const uint4 h = C > 1 ? peer_u128(&sm.hist[top - 3], r)
+                                  : *reinterpret_cast<const uint4 *>(&sm.hist[top - 3]);
+            c4[0] += (int32_t)h.w;
+            c4[1] += (int32_t)h.z;
+            c4[2] += (int32_t)h.y;
+            c4[3] += (int32_t)h.x;
+        }
         int32_t total;
-        int32_t above = block_exclusive_scan<kSelThreads>(local, sm.scan, &total);
+        int32_t above = block_exclusive_scan<kSelThreads>((c4[0] + c4[1]) + (c4[2] + c4[3]), sm.scan, &total);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             if (above < K && K <= above + c4[e]) {
-                sm.pick[0] = kBins - 1 - 4 * tid - e;
+                sm.pick[0] = top - e;
                 sm.pick[1] = above;
                 sm.pick[2] = c4[e];
             }
@@ -573,11 +595,12 @@ indexer_paged_select_kernel(const __grid_constant__ IndexerPagedArgs a, int32_t 
                 if (bin_of(s) == bin) sm.cand[atomicAdd(&sm.n_cand, 1u)] = float_key(s);
             });
             sync();
-            int32_t at = 0;
-            for (int32_t r = 0; r < C; ++r) {
-                const int32_t m = (int32_t)peer(&sm.n_cand, r);
-                if (tid < m) sm.all[at + tid] = peer(&sm.cand[tid], r);
-                at += m;
+            const uint32_t m = gather(&sm.n_cand, 0u);  // lane r: CTA r's candidates
+            if (warp < C) {  // warp w fetches CTA w's
+                const uint32_t at = __reduce_add_sync(0xffffffffu, lane < warp ? m : 0u);
+                const uint32_t mine = __shfl_sync(0xffffffffu, m, warp);
+                for (uint32_t i = lane; i < mine; i += 32)
+                    sm.all[at + i] = C > 1 ? peer_u32(&sm.cand[i], warp) : sm.cand[i];
             }
             __syncthreads();
             if (tid < n_bin) {
@@ -597,6 +620,7 @@ indexer_paged_select_kernel(const __grid_constant__ IndexerPagedArgs a, int32_t 
             prefix = sm.pick[0];
             left -= (int32_t)sm.pick[1];
         } else {
+#pragma unroll 1
             for (int pass = 0; pass < 4; ++pass) {
                 const int shift = 24 - 8 * pass;
                 uint32_t *h = sm.digit[pass & 1];
@@ -608,7 +632,9 @@ indexer_paged_select_kernel(const __grid_constant__ IndexerPagedArgs a, int32_t 
                 sync();
                 int32_t cnt = 0;
                 if (tid < 256)
-                    for (int32_t r = 0; r < C; ++r) cnt += (int32_t)peer(&h[255 - tid], r);
+#pragma unroll
+                    for (int r = 0; r < C; ++r)
+                        cnt += (int32_t)(C > 1 ? peer_u32(&h[255 - tid], r) : h[255 - tid]);
                 int32_t total;
                 const int32_t above = block_exclusive_scan<kSelThreads>(cnt, sm.scan, &total);
                 if (tid < 256 && above < left && left <= above + cnt) {
@@ -623,33 +649,35 @@ indexer_paged_select_kernel(const __grid_constant__ IndexerPagedArgs a, int32_t 
             }
         }
     }
-    // ---- emission in row order
-    auto above_of = [&](float s) { return bin_of(s) > bin || (bin_of(s) == bin && (float_key(s) & mask) > prefix); };
-    auto equal_of = [&](float s) { return bin_of(s) == bin && (float_key(s) & mask) == prefix; };
-    uint32_t n_gt = 0, n_eq = 0;
-    sweep([&](float s) {
-        n_gt += above_of(s);
-        n_eq += equal_of(s);
-    });
-    if (tid < 2) sm.counts[tid] = 0;
-    __syncthreads();
-    n_gt = __reduce_add_sync(0xffffffffu, n_gt);
-    n_eq = __reduce_add_sync(0xffffffffu, n_eq);
-    if (lane == 0) {
-        atomicAdd(&sm.counts[0], n_gt);
-        atomicAdd(&sm.counts[1], n_eq);
-    }
-    sync();
+    // ---- emission in row order: 1 for a row above the threshold, 65536 for
+    // one on it
+    auto kind = [&](float s) -> uint32_t {
+        const uint32_t b = bin_of(s), k = float_key(s) & mask;
+        return b > bin || (b == bin && k > prefix) ? 1u : b == bin && k == prefix ? 65536u : 0u;
+    };
     uint32_t gt_before = 0, eq_before = 0;
-    for (uint32_t r = 0; r < rank; ++r) {
-        gt_before += peer(&sm.counts[0], r);
-        eq_before += peer(&sm.counts[1], r);
+    if (C > 1) {
+        uint32_t n_gt = 0, n_eq = 0;
+        sweep([&](float s) {
+            const uint32_t k = kind(s);
+            n_gt += k & 1u;
+            n_eq += k >> 16;
+        });
+        n_gt = __reduce_add_sync(0xffffffffu, n_gt);
+        n_eq = __reduce_add_sync(0xffffffffu, n_eq);
+        if (lane == 0) {
+            atomicAdd(&sm.counts[0], n_gt);
+            atomicAdd(&sm.counts[1], n_eq);
+        }
+        sync();
+        const uint32_t pg = gather(&sm.counts[0], 0u), pe = gather(&sm.counts[1], 0u);
+        gt_before = __reduce_add_sync(0xffffffffu, lane < rank ? pg : 0u);
+        eq_before = __reduce_add_sync(0xffffffffu, lane < rank ? pe : 0u);
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // done with the peers
     }
-    if (C > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // done with the peers
     for (int32_t c0 = r0; c0 < r1; c0 += kSelRows) {
         if (!kHeld) fetch(c0);
-        // counts of this thread's quads, packed (above | equal << 16)
-        uint32_t quad[kQuads], sum = 0;
+        uint32_t quad[kQuads], sum = 0;  // this thread's counts
 #pragma unroll
         for (int i = 0; i < kQuads; ++i) {
             const int32_t r = row_at(c0, i);
@@ -657,29 +685,25 @@ indexer_paged_select_kernel(const __grid_constant__ IndexerPagedArgs a, int32_t 
             quad[i] = 0;
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                if (r + e < r1) quad[i] += above_of(v[e]) ? 1u : equal_of(v[e]) ? 65536u : 0u;
+                if (r + e < r1) quad[i] += kind(v[e]);
             sum += quad[i];
         }
         // a warp's counts stay below 2^16 each (128 kQuads rows)
         const uint32_t in_warp = __reduce_add_sync(0xffffffffu, sum);
         __syncthreads();
-        if (lane == 0) {
-            sm.warp_gt[warp] = in_warp & 0xffffu;
-            sm.warp_eq[warp] = in_warp >> 16;
-        }
+        if (lane == 0) sm.warps[warp] = in_warp;
         __syncthreads();
-        uint32_t gt = gt_before, eq = eq_before;
-        for (int w = 0; w < kSelThreads / 32; ++w) {
-            if (w < warp) {
-                gt += sm.warp_gt[w];
-                eq += sm.warp_eq[w];
-            }
-            gt_before += sm.warp_gt[w];
-            eq_before += sm.warp_eq[w];
-        }
+        static_assert(kSelThreads / 32 <= 16 && kSelRows < 65536, "packed counts");
+        const uint32_t others = lane < kSelThreads / 32 ? sm.warps[lane] : 0u;
+        const uint32_t before = __reduce_add_sync(0xffffffffu, lane < warp ? others : 0u);
+        const uint32_t chunk = __reduce_add_sync(0xffffffffu, others);
+        uint32_t gt = gt_before + (before & 0xffffu), eq = eq_before + (before >> 16);
+        gt_before += chunk & 0xffffu;
+        eq_before += chunk >> 16;
         if (in_warp != 0) {
 #pragma unroll
             for (int i = 0; i < kQuads; ++i) {
+                if (!__any_sync(0xffffffffu, quad[i] != 0)) continue;
                 uint32_t x = quad[i];
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
@@ -694,15 +718,14 @@ indexer_paged_select_kernel(const __grid_constant__ IndexerPagedArgs a, int32_t 
                 if (quad[i])
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        if (r + e >= r1) break;
-                        const bool up = above_of(v[e]), on = equal_of(v[e]);
-                        if (up || (on && e1 < (uint32_t)left)) {
+                        const uint32_t k = r + e < r1 ? kind(v[e]) : 0u;
+                        if (k == 1u || (k && e1 < (uint32_t)left)) {
                             const uint32_t at = g1 + min(e1, (uint32_t)left);
                             idx[at] = r + e;
                             if (val) val[at] = v[e];
                         }
-                        g1 += up;
-                        e1 += on;
+                        g1 += k & 1u;
+                        e1 += k >> 16;
                     }
                 gt += all & 0xffffu;
                 eq += all >> 16;
@@ -710,6 +733,24 @@ indexer_paged_select_kernel(const __grid_constant__ IndexerPagedArgs a, int32_t 
         }
     }
     if (C > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // peers are done with sm
+}
+
+template <int C>
+cudaError_t launch_select(const IndexerPagedArgs &a, bool held, bool after_scores, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)a.T * C);
+    cfg.blockDim = dim3(kSelThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = C;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = C > 1 ? 2 : 1;
+    return held ? cudaLaunchKernelEx(&cfg, indexer_paged_select_kernel<C, true>, a, (int32_t)after_scores)
+                : cudaLaunchKernelEx(&cfg, indexer_paged_select_kernel<C, false>, a, (int32_t)after_scores);
 }
 
 template <int DI>
@@ -734,7 +775,8 @@ cudaError_t launch_indexer_topk_paged(IndexerPagedArgs a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
-    if (a.max_rows > 0 && (a.max_rows > a.topk || a.topk_val)) {
+    const bool scored = a.max_rows > 0 && (a.max_rows > a.topk || a.topk_val);
+    if (scored) {
         e = a.Di == 128 ? launch_scores<128>(a, sms, stream) : launch_scores<64>(a, sms, stream);
         if (e != cudaSuccess) return e;
     }
@@ -745,21 +787,13 @@ cudaError_t launch_indexer_topk_paged(IndexerPagedArgs a, cudaStream_t stream) {
     while (C < kMaxCluster && ((int64_t)C * kSelRows < a.max_rows ||
                                ((int64_t)a.T * 2 * C <= 2 * sms && (int64_t)C * 4096 <= a.max_rows)))
         C *= 2;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)a.T * C);
-    cfg.blockDim = dim3(kSelThreads);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = (unsigned)C;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = C > 1 ? 2 : 1;
-    return (int64_t)C * kSelRows >= a.max_rows
-               ? cudaLaunchKernelEx(&cfg, indexer_paged_select_kernel<true>, a, (int32_t)C)
-               : cudaLaunchKernelEx(&cfg, indexer_paged_select_kernel<false>, a, (int32_t)C);
+    const bool held = (int64_t)C * kSelRows >= a.max_rows;
+    switch (C) {
+        case 1: return launch_select<1>(a, held, scored, stream);
+        case 2: return launch_select<2>(a, held, scored, stream);
+        case 4: return launch_select<4>(a, held, scored, stream);
+        default: return launch_select<8>(a, held, scored, stream);
+    }
 }
 
 }  // namespace csa

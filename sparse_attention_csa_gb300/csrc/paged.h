@@ -114,6 +114,12 @@ __device__ __forceinline__ int32_t paged_seq(const int32_t *q_seq, int32_t batch
     const int32_t b = q_seq ? __ldg(q_seq + t) : t;
     return (uint32_t)b < (uint32_t)batch ? b : -2;
 }
+
+// a / b, by a 32-bit division when both fit.
+__device__ __forceinline__ int64_t div64(int64_t a, int64_t b) {
+    if (((a | b) >> 32) == 0) return (int64_t)((uint32_t)a / (uint32_t)b);
+    return a / b;
+}
 #endif
 
 }  // namespace csa

@@ -260,12 +260,6 @@ __device__ __forceinline__ float reduce_scatter16(const float (&x)[16], int lane
 }
 __device__ __forceinline__ int sum_index(int lane) { return ((lane >> 4) << 3) | (lane & 7); }
 
-// a / b, by a 32-bit division when both fit.
-__device__ __forceinline__ int64_t div64(int64_t a, int64_t b) {
-    if (((a | b) >> 32) == 0) return (int64_t)((uint32_t)a / (uint32_t)b);
-    return a / b;
-}
-
 __global__ void __launch_bounds__(kThreads, 1)
 sparse_mla_paged_kernel(const __grid_constant__ CUtensorMap q_map,
                         const __grid_constant__ MlaPagedArgs a) {
