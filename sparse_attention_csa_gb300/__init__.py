@@ -457,9 +457,17 @@ _DTYPES = {torch.bfloat16: 0, torch.float32: 1}
 _LAYOUTS = {"interleaved": 0, "half": 1}
 
 
+def _first(t, name, dtype, ndim):
+    """The shape and device of a call's first tensor (contiguous, of `dtype`)."""
+    _need(t, name, dtype, ndim)
+    if t is None:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    return t.shape, t.get_device()
+
+
 def _rows(t, name, ndim):
     """A bf16 or fp32 CUDA tensor whose rows (everything past the first axis)
-    are contiguous; the stride between them is free. Returns (dtype code, stride)."""
+    are contiguous; the stride between them is free. Returns the dtype code."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     code = _DTYPES.get(t.dtype)
@@ -467,14 +475,31 @@ def _rows(t, name, ndim):
         raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
     if t.dim() not in ndim:
         raise ValueError(f"{name} must have {' or '.join(map(str, ndim))} dims, got {tuple(t.shape)}")
-    if t.numel() and not t[0].is_contiguous():
+    if not t.is_contiguous() and t.numel() and not t[0].is_contiguous():
         raise ValueError(f"{name} must have contiguous rows")
-    return code, t.stride(0)
+    return code
 
 
-def _shape(t, name, shape):
-    if t is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+def _match(dev, *specs):
+    """Each (tensor or None, name, dtype, shape): on device `dev`, contiguous,
+    of that dtype and shape."""
+    for t, name, dtype, shape in specs:
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError(f"{name} must be a CUDA tensor")
+        if t.dtype is not dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        if t.get_device() != dev:
+            raise ValueError(f"{name} is on cuda:{t.get_device()}, the call on cuda:{dev}")
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _layout(layout):
@@ -483,26 +508,21 @@ def _layout(layout):
     return _LAYOUTS[layout]
 
 
-class _Device:
-    """Checks that the tensors share one device and makes it current."""
-
-    def __init__(self, first, *others):
-        dev = first.device
-        for t in others:
-            if t is not None and t.device != dev:
-                raise ValueError(f"tensors on {dev} and {t.device} in one call")
-        self.index = dev.index
-        self.back = None
-
-    def __enter__(self):
-        cur = torch._C._cuda_getDevice()
-        if cur != self.index:
-            self.back = cur
-            torch.cuda.set_device(self.index)
-
-    def __exit__(self, *exc):
-        if self.back is not None:
-            torch.cuda.set_device(self.back)
+def _launch(dev, where, stream, *args):
+    """Calls entry point `where` with device `dev` current, on `stream` (None:
+    that device's current stream)."""
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(dev)
+    elif hasattr(stream, "cuda_stream"):
+        stream = stream.cuda_stream
+    fn = getattr(lib(), where)
+    if torch._C._cuda_getDevice() == dev:
+        rc = fn(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, stream)
+    if rc != 0:
+        raise CsaError(rc, where)
 
 
 def csa_rope_freqs(rope_dim: int, theta: float = 10000.0, factor: float = 1.0,
@@ -512,15 +532,13 @@ def csa_rope_freqs(rope_dim: int, theta: float = 10000.0, factor: float = 1.0,
     :func:`csa_rope` and :func:`csa_cache_append`. ``factor`` > 1 stretches
     positions for longer contexts: all pairs (``original_len`` 0) or the slow
     ones, by parts."""
+    rope_dim = int(rope_dim)
     if out is None:
-        out = torch.empty((max(int(rope_dim), 0) // 2,), dtype=torch.float64,
-                          device=device or "cuda")
-    _need(out, "out", torch.float64, 1)
-    _shape(out, "out", (int(rope_dim) // 2,))
-    with _Device(out):
-        _check(lib().csa_rope_freqs(int(rope_dim), float(theta), float(factor), int(original_len),
-                                    float(beta_fast), float(beta_slow), _ptr(out),
-                                    _stream(stream)), "csa_rope_freqs")
+        out = torch.empty((max(rope_dim, 0) // 2,), dtype=torch.float64, device=device or "cuda")
+    _, dev = _first(out, "out", torch.float64, 1)
+    _match(dev, (out, "out", torch.float64, (max(rope_dim, 0) // 2,)))
+    _launch(dev, "csa_rope_freqs", stream, rope_dim, theta, factor, int(original_len), beta_fast,
+            beta_slow, out.data_ptr())
     return out
 
 
@@ -534,27 +552,29 @@ def csa_rope(x, positions, inv_freq, rope_offset=None, layout: str = "interleave
     ``positions`` [T] int32, or None with ``cu_seqlens`` [batch+1]: the place
     in the packed sequence; both times ``pos_stride``. ``inverse`` turns back,
     which is also the backward. ``out`` may be ``x``. Returns out."""
-    code, x_stride = _rows(x, "x", (2, 3))
-    _need(positions, "positions", torch.int32, 1)
-    _need(cu_seqlens, "cu_seqlens", torch.int32, 1)
-    _need(inv_freq, "inv_freq", torch.float64, 1)
-    T, D = x.shape[0], x.shape[-1]
-    H = x.shape[1] if x.dim() == 3 else 1
-    _shape(positions, "positions", (T,))
+    code = _rows(x, "x", (2, 3))
+    dev, shape = x.get_device(), x.shape
+    T, D = shape[0], shape[-1]
+    H = shape[1] if len(shape) == 3 else 1
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    elif out.dtype != x.dtype:
-        raise TypeError(f"out must be {x.dtype}, got {out.dtype}")
-    _shape(out, "out", tuple(x.shape))
-    out_stride = _rows(out, "out", (2, 3))[1]
-    n = 2 * inv_freq.numel()
-    off = D - n if rope_offset is None else int(rope_offset)
-    with _Device(x, positions, cu_seqlens, inv_freq, out):
-        _check(lib().csa_rope(
-            _ptr(x), code, x_stride, _ptr(positions), _ptr(cu_seqlens),
-            0 if cu_seqlens is None else cu_seqlens.numel() - 1, int(pos_stride), _ptr(inv_freq),
-            T, H, D, off, n, _layout(layout), float(mscale), 1 if inverse else 0, _ptr(out),
-            out_stride, _stream(stream)), "csa_rope")
+        out = torch.empty(shape, dtype=x.dtype, device=x.device)
+    elif out is not x:
+        if _rows(out, "out", (2, 3)) != code:
+            raise TypeError(f"out must be {x.dtype}, got {out.dtype}")
+        if out.shape != shape or out.get_device() != dev:
+            raise ValueError(f"out must be {list(shape)} on {x.device}, got {list(out.shape)} on "
+                             f"{out.device}")
+    _need(inv_freq, "inv_freq", torch.float64, 1)
+    _need(cu_seqlens, "cu_seqlens", torch.int32, 1)
+    half = 0 if inv_freq is None else inv_freq.shape[0]
+    batch = 0 if cu_seqlens is None else cu_seqlens.shape[0] - 1
+    _match(dev, (positions, "positions", torch.int32, (T,)),
+           (inv_freq, "inv_freq", torch.float64, (half,)),
+           (cu_seqlens, "cu_seqlens", torch.int32, (batch + 1,)))
+    _launch(dev, "csa_rope", stream, x.data_ptr(), code, x.stride(0), _addr(positions),
+            _addr(cu_seqlens), batch, pos_stride, _addr(inv_freq), T, H, D,
+            D - 2 * half if rope_offset is None else rope_offset, 2 * half, _layout(layout), mscale,
+            1 if inverse else 0, out.data_ptr(), out.stride(0))
     return out
 
 
@@ -567,31 +587,28 @@ def csa_cache_append(rows, row_seq, row_pos, pages, cache, inv_freq=None, rope_o
     with table ``pages`` [batch, max_pages], rotated as :func:`csa_rope` does
     at ``row_pos * pos_stride`` when ``inv_freq`` is given. A negative
     position skips the row. Returns cache."""
-    code, stride = _rows(rows, "rows", (2,))
-    _need(row_seq, "row_seq", torch.int32, 1)
-    _need(row_pos, "row_pos", torch.int32, 1)
-    _need(pages, "pages", torch.int32, 2)
-    _need(cache, "cache", torch.bfloat16, 3)
-    _need(inv_freq, "inv_freq", torch.float64, 1)
+    code = _rows(rows, "rows", (2,))
+    dev = rows.get_device()
     T, width = rows.shape
-    _shape(row_seq, "row_seq", (T,))
-    _shape(row_pos, "row_pos", (T,))
-    _shape(cache, "cache", (cache.shape[0], cache.shape[1], width))
-    n = 0 if inv_freq is None else 2 * inv_freq.numel()
-    off = width - n if rope_offset is None else int(rope_offset)
-    with _Device(rows, row_seq, row_pos, pages, cache, inv_freq):
-        _check(lib().csa_cache_append(
-            _ptr(rows), code, stride, _ptr(row_seq), _ptr(row_pos), _ptr(pages), pages.shape[0],
-            pages.shape[1], cache.shape[0], cache.shape[1], T, width, _ptr(inv_freq),
-            off, n, _layout(layout), float(mscale), int(pos_stride), _ptr(cache),
-            _stream(stream)), "csa_cache_append")
+    (n_pages, page, _), _ = _first(cache, "cache", torch.bfloat16, 3)
+    (batch, max_pages), _ = _first(pages, "pages", torch.int32, 2)
+    _need(inv_freq, "inv_freq", torch.float64, 1)
+    half = 0 if inv_freq is None else inv_freq.shape[0]
+    _match(dev, (row_seq, "row_seq", torch.int32, (T,)), (row_pos, "row_pos", torch.int32, (T,)),
+           (pages, "pages", torch.int32, (batch, max_pages)),
+           (cache, "cache", torch.bfloat16, (n_pages, page, width)),
+           (inv_freq, "inv_freq", torch.float64, (half,)))
+    _launch(dev, "csa_cache_append", stream, rows.data_ptr(), code, rows.stride(0), _addr(row_seq),
+            _addr(row_pos), pages.data_ptr(), batch, max_pages, n_pages, page, T, width,
+            _addr(inv_freq), width - 2 * half if rope_offset is None else rope_offset, 2 * half,
+            _layout(layout), mscale, pos_stride, cache.data_ptr())
     return cache
 
 
 def csa_indexer_topk_paged_workspace_size(total_tokens, max_rows, index_heads, index_dim,
                                           topk) -> int:
-    return int(lib().csa_indexer_topk_paged_workspace_size(
-        int(total_tokens), int(max_rows), int(index_heads), int(index_dim), int(topk)))
+    return lib().csa_indexer_topk_paged_workspace_size(int(total_tokens), int(max_rows),
+                                                       int(index_heads), int(index_dim), int(topk))
 
 
 def csa_indexer_topk_paged(q, k_cache, w, pages, q_seq, q_pos, cmp_ratio: int, topk: int,
@@ -604,42 +621,34 @@ def csa_indexer_topk_paged(q, k_cache, w, pages, q_seq, q_pos, cmp_ratio: int, t
 
     Returns ``(topk_idx [T, topk] int32 rows of the sequence, -1 padded,
     topk_val [T, topk] fp32 or None)``."""
-    _need(q, "q", torch.bfloat16, 3)
-    _need(k_cache, "k_cache", torch.bfloat16, 3)
-    _need(w, "w", torch.float32, 2)
-    _need(pages, "pages", torch.int32, 2)
-    _need(q_seq, "q_seq", torch.int32, 1)
-    _need(q_pos, "q_pos", torch.int32, 1)
-    T, Hi, Di = q.shape
+    (T, Hi, Di), dev = _first(q, "q", torch.bfloat16, 3)
+    (n_pages, page, _), _ = _first(k_cache, "k_cache", torch.bfloat16, 3)
+    (batch, max_pages), _ = _first(pages, "pages", torch.int32, 2)
     topk = int(topk)
-    _shape(w, "w", (T, Hi))
-    _shape(q_seq, "q_seq", (T,))
-    _shape(q_pos, "q_pos", (T,))
-    n_pages, page, _ = k_cache.shape
-    _shape(k_cache, "k_cache", (n_pages, page, Di))
-    B, max_pages = pages.shape
     if out is None:
         out = torch.empty((T, max(topk, 0)), dtype=torch.int32, device=q.device)
-    if return_value and out_val is None:
+    if not return_value:
+        out_val = None
+    elif out_val is None:
         out_val = torch.empty((T, max(topk, 0)), dtype=torch.float32, device=q.device)
-    _need(out, "out", torch.int32, 2)
-    _shape(out, "out", (T, topk))
-    if return_value:
-        _need(out_val, "out_val", torch.float32, 2)
-        _shape(out_val, "out_val", (T, topk))
-    need = csa_indexer_topk_paged_workspace_size(T, max_pages * page, Hi, Di, topk)
+    _match(dev, (k_cache, "k_cache", torch.bfloat16, (n_pages, page, Di)),
+           (w, "w", torch.float32, (T, Hi)), (pages, "pages", torch.int32, (batch, max_pages)),
+           (q_seq, "q_seq", torch.int32, (T,)), (q_pos, "q_pos", torch.int32, (T,)),
+           (out, "out", torch.int32, (T, max(topk, 0))),
+           (out_val, "out_val", torch.float32, (T, max(topk, 0))))
+    need = csa_indexer_topk_paged_workspace_size(T, max_pages * page, Hi, Di, topk) \
+        if max_pages * page < 2 ** 31 else 0
     workspace, ws_bytes = _workspace(need, q.device, workspace)
-    with _Device(q, k_cache, w, pages, q_seq, q_pos, workspace, out, out_val):
-        _check(lib().csa_indexer_topk_paged(
-            _ptr(q), _ptr(k_cache), _ptr(w), _ptr(pages), _ptr(q_seq), _ptr(q_pos), B, T, Hi, Di,
-            n_pages, page, max_pages, int(cmp_ratio), topk, _ptr(out),
-            _ptr(out_val) if return_value else None, _ptr(workspace), ws_bytes,
-            _stream(stream)), "csa_indexer_topk_paged")
-    return out, (out_val if return_value else None)
+    if workspace is not None and workspace.get_device() != dev:
+        raise ValueError(f"workspace is on {workspace.device}, the call on cuda:{dev}")
+    _launch(dev, "csa_indexer_topk_paged", stream, q.data_ptr(), k_cache.data_ptr(), _addr(w),
+            pages.data_ptr(), _addr(q_seq), _addr(q_pos), batch, T, Hi, Di, n_pages, page, max_pages,
+            cmp_ratio, topk, out.data_ptr(), _addr(out_val), _addr(workspace), ws_bytes)
+    return out, out_val
 
 
 def csa_sparse_mla_paged_workspace_size(total_tokens, heads) -> int:
-    return int(lib().csa_sparse_mla_paged_workspace_size(int(total_tokens), int(heads)))
+    return lib().csa_sparse_mla_paged_workspace_size(int(total_tokens), int(heads))
 
 
 def csa_sparse_mla_paged(q, ori_cache, cmp_cache, cmp_sparse_indices, ori_pages, cmp_pages, q_seq,
@@ -654,53 +663,41 @@ def csa_sparse_mla_paged(q, ori_cache, cmp_cache, cmp_sparse_indices, ori_pages,
     table [batch, max_pages]. ``cmp_cache`` None: window only.
 
     Returns ``(out [T, H, 512], lse [T, H] or None)``."""
-    _need(q, "q", torch.bfloat16, 3)
-    _need(ori_cache, "ori_cache", torch.bfloat16, 3)
-    _need(cmp_cache, "cmp_cache", torch.bfloat16, 3)
-    _need(cmp_sparse_indices, "cmp_sparse_indices", torch.int32, 2)
-    _need(ori_pages, "ori_pages", torch.int32, 2)
-    _need(cmp_pages, "cmp_pages", torch.int32, 2)
-    _need(q_seq, "q_seq", torch.int32, 1)
-    _need(q_pos, "q_pos", torch.int32, 1)
-    _need(sinks, "sinks", torch.float32, 1)
-    T, H, D = q.shape
-    B, ori_max = ori_pages.shape
-    ori_n, ori_page, _ = ori_cache.shape
+    (T, H, D), dev = _first(q, "q", torch.bfloat16, 3)
+    (ori_n, ori_page, _), _ = _first(ori_cache, "ori_cache", torch.bfloat16, 3)
+    (batch, ori_max), _ = _first(ori_pages, "ori_pages", torch.int32, 2)
     cmp_n = cmp_page = cmp_max = topk = 0
-    if cmp_cache is not None:
-        if cmp_pages is None:
-            raise ValueError("cmp_cache needs cmp_pages")
-        cmp_n, cmp_page, _ = cmp_cache.shape
-        cmp_max = cmp_pages.shape[1]
-        _shape(cmp_cache, "cmp_cache", (cmp_n, cmp_page, D))
-        _shape(cmp_pages, "cmp_pages", (B, cmp_max))
+    if cmp_cache is None:
+        cmp_sparse_indices = cmp_pages = None
+    else:
+        (cmp_n, cmp_page, _), _ = _first(cmp_cache, "cmp_cache", torch.bfloat16, 3)
+        cmp_max = _first(cmp_pages, "cmp_pages", torch.int32, 2)[0][1]
         if cmp_sparse_indices is not None:
-            topk = cmp_sparse_indices.shape[1]
-            _shape(cmp_sparse_indices, "cmp_sparse_indices", (T, topk))
-    _shape(ori_cache, "ori_cache", (ori_n, ori_page, D))
-    _shape(q_seq, "q_seq", (T,))
-    _shape(q_pos, "q_pos", (T,))
-    _shape(sinks, "sinks", (H,))
+            topk = _first(cmp_sparse_indices, "cmp_sparse_indices", torch.int32, 2)[0][1]
     if out is None:
         out = torch.empty_like(q)
-    if return_softmax_lse and lse is None:
+    if not return_softmax_lse:
+        lse = None
+    elif lse is None:
         lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
-    _need(out, "out", torch.bfloat16, 3)
-    _shape(out, "out", (T, H, D))
-    if return_softmax_lse:
-        _need(lse, "lse", torch.float32, 2)
-        _shape(lse, "lse", (T, H))
-    workspace, ws_bytes = _workspace(csa_sparse_mla_paged_workspace_size(T, H), q.device, workspace)
-    with _Device(q, ori_cache, cmp_cache, cmp_sparse_indices, ori_pages, cmp_pages, q_seq, q_pos,
-                 sinks, workspace, out, lse):
-        _check(lib().csa_sparse_mla_paged(
-            _ptr(q), _ptr(ori_cache), _ptr(cmp_cache), _ptr(cmp_sparse_indices), _ptr(ori_pages),
-            _ptr(cmp_pages), _ptr(q_seq), _ptr(q_pos), B, T, H, D, ori_n, ori_page, ori_max,
-            cmp_n, cmp_page, cmp_max, topk, _ptr(sinks), float(softmax_scale), int(cmp_ratio),
-            int(ori_win_left), int(ori_win_right), _ptr(out),
-            _ptr(lse) if return_softmax_lse else None, 1 if return_softmax_lse else 0,
-            _ptr(workspace), ws_bytes, _stream(stream)), "csa_sparse_mla_paged")
-    return out, (lse if return_softmax_lse else None)
+    _match(dev, (ori_cache, "ori_cache", torch.bfloat16, (ori_n, ori_page, D)),
+           (cmp_cache, "cmp_cache", torch.bfloat16, (cmp_n, cmp_page, D)),
+           (cmp_sparse_indices, "cmp_sparse_indices", torch.int32, (T, topk)),
+           (ori_pages, "ori_pages", torch.int32, (batch, ori_max)),
+           (cmp_pages, "cmp_pages", torch.int32, (batch, cmp_max)),
+           (q_seq, "q_seq", torch.int32, (T,)), (q_pos, "q_pos", torch.int32, (T,)),
+           (sinks, "sinks", torch.float32, (H,)), (out, "out", torch.bfloat16, (T, H, D)),
+           (lse, "lse", torch.float32, (T, H)))
+    workspace, ws_bytes = _workspace(lib().csa_sparse_mla_paged_workspace_size(T, H), q.device,
+                                     workspace)
+    if workspace is not None and workspace.get_device() != dev:
+        raise ValueError(f"workspace is on {workspace.device}, the call on cuda:{dev}")
+    _launch(dev, "csa_sparse_mla_paged", stream, q.data_ptr(), ori_cache.data_ptr(),
+            _addr(cmp_cache), _addr(cmp_sparse_indices), ori_pages.data_ptr(), _addr(cmp_pages),
+            _addr(q_seq), _addr(q_pos), batch, T, H, D, ori_n, ori_page, ori_max, cmp_n, cmp_page,
+            cmp_max, topk, _addr(sinks), softmax_scale, cmp_ratio, ori_win_left, ori_win_right,
+            out.data_ptr(), _addr(lse), 1 if return_softmax_lse else 0, _addr(workspace), ws_bytes)
+    return out, lse
 
 
 def csa_device_error(stream=None):

@@ -589,20 +589,34 @@ indexer_paged_select_kernel(const __grid_constant__ IndexerPagedArgs a, int32_t 
     // rows of the bin: those with (key & mask) above prefix are taken, those
     // equal to it in row order while `left` lasts
     uint32_t mask = 0u, prefix = 0u;
-    if (left < n_bin) {
-        if (n_bin <= kCand) {
-            sweep([&](float s) {
-                if (bin_of(s) == bin) sm.cand[atomicAdd(&sm.n_cand, 1u)] = float_key(s);
-            });
-            sync();
-            const uint32_t m = gather(&sm.n_cand, 0u);  // lane r: CTA r's candidates
-            if (warp < C) {  // warp w fetches CTA w's
-                const uint32_t at = __reduce_add_sync(0xffffffffu, lane < warp ? m : 0u);
-                const uint32_t mine = __shfl_sync(0xffffffffu, m, warp);
-                for (uint32_t i = lane; i < mine; i += 32)
-                    sm.all[at + i] = C > 1 ? peer_u32(&sm.cand[i], warp) : sm.cand[i];
-            }
-            __syncthreads();
+    // rows above the threshold and on it in the CTAs before this one
+    uint32_t gt_before = 0, eq_before = 0;
+    if (n_bin <= kCand) {
+        uint32_t n_gt = 0;
+        sweep([&](float s) {
+            const uint32_t b = bin_of(s);
+            n_gt += b > bin;
+            if (b == bin) sm.cand[atomicAdd(&sm.n_cand, 1u)] = float_key(s);
+        });
+        n_gt = __reduce_add_sync(0xffffffffu, n_gt);
+        if (C > 1 && lane == 0) atomicAdd(&sm.counts[0], n_gt);
+        sync();
+        const uint32_t m = gather(&sm.n_cand, 0u);  // lane r: CTA r's candidates
+        if (warp < C) {  // warp w fetches CTA w's
+            const uint32_t at = __reduce_add_sync(0xffffffffu, lane < warp ? m : 0u);
+            const uint32_t mine = __shfl_sync(0xffffffffu, m, warp);
+            for (uint32_t i = lane; i < mine; i += 32)
+                sm.all[at + i] = C > 1 ? peer_u32(&sm.cand[i], warp) : sm.cand[i];
+        }
+        uint32_t start = 0;  // candidates of the CTAs before this one
+        if (C > 1) {
+            const uint32_t pg = gather(&sm.counts[0], 0u);
+            gt_before = __reduce_add_sync(0xffffffffu, lane < rank ? pg : 0u);
+            start = __reduce_add_sync(0xffffffffu, lane < rank ? m : 0u);
+            asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // done with the peers
+        }
+        __syncthreads();
+        if (left < n_bin) {
             if (tid < n_bin) {
                 const uint32_t mine = sm.all[tid];
                 int32_t gt = 0, eq = 0;
@@ -619,7 +633,15 @@ indexer_paged_select_kernel(const __grid_constant__ IndexerPagedArgs a, int32_t 
             mask = 0xffffffffu;
             prefix = sm.pick[0];
             left -= (int32_t)sm.pick[1];
-        } else {
+        }
+        if (C > 1) {
+            const bool in = (uint32_t)tid < start;
+            const uint32_t k = in ? sm.all[tid] & mask : 0u;
+            gt_before += __syncthreads_count(in && k > prefix);
+            eq_before = __syncthreads_count(in && k == prefix);
+        }
+    } else {
+        if (left < n_bin) {
 #pragma unroll 1
             for (int pass = 0; pass < 4; ++pass) {
                 const int shift = 24 - 8 * pass;
@@ -648,6 +670,25 @@ indexer_paged_select_kernel(const __grid_constant__ IndexerPagedArgs a, int32_t 
                 __syncthreads();
             }
         }
+        if (C > 1) {
+            uint32_t n_gt = 0, n_eq = 0;
+            sweep([&](float s) {
+                const uint32_t b = bin_of(s), k = float_key(s) & mask;
+                n_gt += b > bin || (b == bin && k > prefix);
+                n_eq += b == bin && k == prefix;
+            });
+            n_gt = __reduce_add_sync(0xffffffffu, n_gt);
+            n_eq = __reduce_add_sync(0xffffffffu, n_eq);
+            if (lane == 0) {
+                atomicAdd(&sm.counts[0], n_gt);
+                atomicAdd(&sm.counts[1], n_eq);
+            }
+            sync();
+            const uint32_t pg = gather(&sm.counts[0], 0u), pe = gather(&sm.counts[1], 0u);
+            gt_before = __reduce_add_sync(0xffffffffu, lane < rank ? pg : 0u);
+            eq_before = __reduce_add_sync(0xffffffffu, lane < rank ? pe : 0u);
+            asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // done with the peers
+        }
     }
     // ---- emission in row order: 1 for a row above the threshold, 65536 for
     // one on it
@@ -655,26 +696,6 @@ indexer_paged_select_kernel(const __grid_constant__ IndexerPagedArgs a, int32_t 
         const uint32_t b = bin_of(s), k = float_key(s) & mask;
         return b > bin || (b == bin && k > prefix) ? 1u : b == bin && k == prefix ? 65536u : 0u;
     };
-    uint32_t gt_before = 0, eq_before = 0;
-    if (C > 1) {
-        uint32_t n_gt = 0, n_eq = 0;
-        sweep([&](float s) {
-            const uint32_t k = kind(s);
-            n_gt += k & 1u;
-            n_eq += k >> 16;
-        });
-        n_gt = __reduce_add_sync(0xffffffffu, n_gt);
-        n_eq = __reduce_add_sync(0xffffffffu, n_eq);
-        if (lane == 0) {
-            atomicAdd(&sm.counts[0], n_gt);
-            atomicAdd(&sm.counts[1], n_eq);
-        }
-        sync();
-        const uint32_t pg = gather(&sm.counts[0], 0u), pe = gather(&sm.counts[1], 0u);
-        gt_before = __reduce_add_sync(0xffffffffu, lane < rank ? pg : 0u);
-        eq_before = __reduce_add_sync(0xffffffffu, lane < rank ? pe : 0u);
-        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // done with the peers
-    }
     for (int32_t c0 = r0; c0 < r1; c0 += kSelRows) {
         if (!kHeld) fetch(c0);
         uint32_t quad[kQuads], sum = 0;  // this thread's counts
