@@ -457,12 +457,13 @@ _DTYPES = {torch.bfloat16: 0, torch.float32: 1}
 _LAYOUTS = {"interleaved": 0, "half": 1}
 
 
-def _first(t, name, dtype, ndim):
-    """The shape and device of a call's first tensor (contiguous, of `dtype`)."""
-    _need(t, name, dtype, ndim)
-    if t is None:
+def _dims(t, name, ndim):
+    """The shape of a tensor argument with `ndim` axes."""
+    if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a CUDA tensor")
-    return t.shape, t.get_device()
+    if t.dim() != ndim:
+        raise ValueError(f"{name} must have {ndim} dims, got {tuple(t.shape)}")
+    return t.shape
 
 
 def _rows(t, name, ndim):
@@ -535,7 +536,7 @@ def csa_rope_freqs(rope_dim: int, theta: float = 10000.0, factor: float = 1.0,
     rope_dim = int(rope_dim)
     if out is None:
         out = torch.empty((max(rope_dim, 0) // 2,), dtype=torch.float64, device=device or "cuda")
-    _, dev = _first(out, "out", torch.float64, 1)
+    dev = out.get_device()
     _match(dev, (out, "out", torch.float64, (max(rope_dim, 0) // 2,)))
     _launch(dev, "csa_rope_freqs", stream, rope_dim, theta, factor, int(original_len), beta_fast,
             beta_slow, out.data_ptr())
@@ -564,10 +565,8 @@ def csa_rope(x, positions, inv_freq, rope_offset=None, layout: str = "interleave
         if out.shape != shape or out.get_device() != dev:
             raise ValueError(f"out must be {list(shape)} on {x.device}, got {list(out.shape)} on "
                              f"{out.device}")
-    _need(inv_freq, "inv_freq", torch.float64, 1)
-    _need(cu_seqlens, "cu_seqlens", torch.int32, 1)
-    half = 0 if inv_freq is None else inv_freq.shape[0]
-    batch = 0 if cu_seqlens is None else cu_seqlens.shape[0] - 1
+    half = 0 if inv_freq is None else _dims(inv_freq, "inv_freq", 1)[0]
+    batch = 0 if cu_seqlens is None else _dims(cu_seqlens, "cu_seqlens", 1)[0] - 1
     _match(dev, (positions, "positions", torch.int32, (T,)),
            (inv_freq, "inv_freq", torch.float64, (half,)),
            (cu_seqlens, "cu_seqlens", torch.int32, (batch + 1,)))
@@ -590,10 +589,9 @@ def csa_cache_append(rows, row_seq, row_pos, pages, cache, inv_freq=None, rope_o
     code = _rows(rows, "rows", (2,))
     dev = rows.get_device()
     T, width = rows.shape
-    (n_pages, page, _), _ = _first(cache, "cache", torch.bfloat16, 3)
-    (batch, max_pages), _ = _first(pages, "pages", torch.int32, 2)
-    _need(inv_freq, "inv_freq", torch.float64, 1)
-    half = 0 if inv_freq is None else inv_freq.shape[0]
+    n_pages, page, _ = _dims(cache, "cache", 3)
+    batch, max_pages = _dims(pages, "pages", 2)
+    half = 0 if inv_freq is None else _dims(inv_freq, "inv_freq", 1)[0]
     _match(dev, (row_seq, "row_seq", torch.int32, (T,)), (row_pos, "row_pos", torch.int32, (T,)),
            (pages, "pages", torch.int32, (batch, max_pages)),
            (cache, "cache", torch.bfloat16, (n_pages, page, width)),
@@ -621,9 +619,10 @@ def csa_indexer_topk_paged(q, k_cache, w, pages, q_seq, q_pos, cmp_ratio: int, t
 
     Returns ``(topk_idx [T, topk] int32 rows of the sequence, -1 padded,
     topk_val [T, topk] fp32 or None)``."""
-    (T, Hi, Di), dev = _first(q, "q", torch.bfloat16, 3)
-    (n_pages, page, _), _ = _first(k_cache, "k_cache", torch.bfloat16, 3)
-    (batch, max_pages), _ = _first(pages, "pages", torch.int32, 2)
+    T, Hi, Di = _dims(q, "q", 3)
+    n_pages, page, _ = _dims(k_cache, "k_cache", 3)
+    batch, max_pages = _dims(pages, "pages", 2)
+    dev = q.get_device()
     topk = int(topk)
     if out is None:
         out = torch.empty((T, max(topk, 0)), dtype=torch.int32, device=q.device)
@@ -631,7 +630,8 @@ def csa_indexer_topk_paged(q, k_cache, w, pages, q_seq, q_pos, cmp_ratio: int, t
         out_val = None
     elif out_val is None:
         out_val = torch.empty((T, max(topk, 0)), dtype=torch.float32, device=q.device)
-    _match(dev, (k_cache, "k_cache", torch.bfloat16, (n_pages, page, Di)),
+    _match(dev, (q, "q", torch.bfloat16, (T, Hi, Di)),
+           (k_cache, "k_cache", torch.bfloat16, (n_pages, page, Di)),
            (w, "w", torch.float32, (T, Hi)), (pages, "pages", torch.int32, (batch, max_pages)),
            (q_seq, "q_seq", torch.int32, (T,)), (q_pos, "q_pos", torch.int32, (T,)),
            (out, "out", torch.int32, (T, max(topk, 0))),
@@ -663,24 +663,26 @@ def csa_sparse_mla_paged(q, ori_cache, cmp_cache, cmp_sparse_indices, ori_pages,
     table [batch, max_pages]. ``cmp_cache`` None: window only.
 
     Returns ``(out [T, H, 512], lse [T, H] or None)``."""
-    (T, H, D), dev = _first(q, "q", torch.bfloat16, 3)
-    (ori_n, ori_page, _), _ = _first(ori_cache, "ori_cache", torch.bfloat16, 3)
-    (batch, ori_max), _ = _first(ori_pages, "ori_pages", torch.int32, 2)
+    T, H, D = _dims(q, "q", 3)
+    ori_n, ori_page, _ = _dims(ori_cache, "ori_cache", 3)
+    batch, ori_max = _dims(ori_pages, "ori_pages", 2)
+    dev = q.get_device()
     cmp_n = cmp_page = cmp_max = topk = 0
     if cmp_cache is None:
         cmp_sparse_indices = cmp_pages = None
     else:
-        (cmp_n, cmp_page, _), _ = _first(cmp_cache, "cmp_cache", torch.bfloat16, 3)
-        cmp_max = _first(cmp_pages, "cmp_pages", torch.int32, 2)[0][1]
+        cmp_n, cmp_page, _ = _dims(cmp_cache, "cmp_cache", 3)
+        cmp_max = _dims(cmp_pages, "cmp_pages", 2)[1]
         if cmp_sparse_indices is not None:
-            topk = _first(cmp_sparse_indices, "cmp_sparse_indices", torch.int32, 2)[0][1]
+            topk = _dims(cmp_sparse_indices, "cmp_sparse_indices", 2)[1]
     if out is None:
         out = torch.empty_like(q)
     if not return_softmax_lse:
         lse = None
     elif lse is None:
         lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
-    _match(dev, (ori_cache, "ori_cache", torch.bfloat16, (ori_n, ori_page, D)),
+    _match(dev, (q, "q", torch.bfloat16, (T, H, D)),
+           (ori_cache, "ori_cache", torch.bfloat16, (ori_n, ori_page, D)),
            (cmp_cache, "cmp_cache", torch.bfloat16, (cmp_n, cmp_page, D)),
            (cmp_sparse_indices, "cmp_sparse_indices", torch.int32, (T, topk)),
            (ori_pages, "ori_pages", torch.int32, (batch, ori_max)),

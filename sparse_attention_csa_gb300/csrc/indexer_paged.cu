@@ -775,12 +775,9 @@ cudaError_t launch_select(const IndexerPagedArgs &a, bool held, bool after_score
 }
 
 template <int DI>
-cudaError_t launch_scores(const IndexerPagedArgs &a, int sms, cudaStream_t stream) {
-    auto *kernel = indexer_paged_score_kernel<DI>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)Score<DI>::kSmem);
-    if (e != cudaSuccess) return e;
-    return launch_early(kernel, dim3(sms), dim3(kThreads), Score<DI>::kSmem, stream, a);
+cudaError_t allow_smem() {
+    return cudaFuncSetAttribute(indexer_paged_score_kernel<DI>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)Score<DI>::kSmem);
 }
 
 }  // namespace
@@ -791,14 +788,22 @@ size_t indexer_paged_workspace_bytes(int32_t T, int64_t max_rows) {
 
 cudaError_t launch_indexer_topk_paged(IndexerPagedArgs a, cudaStream_t stream) {
     a.row_pad = ((int64_t)a.max_rows + 63) / 64 * 64;
-    int dev = 0, sms = 0;
-    cudaError_t e = cudaGetDevice(&dev);
+    static PerContext pc;
+    int sms, dev;
+    bool first;
+    unsigned long long ctx;
+    cudaError_t e = enter_context(pc, &sms, &first, &ctx, &dev);
     if (e != cudaSuccess) return e;
-    e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e != cudaSuccess) return e;
+    if (first) {
+        if ((e = allow_smem<64>()) != cudaSuccess || (e = allow_smem<128>()) != cudaSuccess) return e;
+        entered_context(pc, dev, ctx);
+    }
     const bool scored = a.max_rows > 0 && (a.max_rows > a.topk || a.topk_val);
     if (scored) {
-        e = a.Di == 128 ? launch_scores<128>(a, sms, stream) : launch_scores<64>(a, sms, stream);
+        e = a.Di == 128 ? launch_early(indexer_paged_score_kernel<128>, dim3(sms), dim3(kThreads),
+                                       Score<128>::kSmem, stream, a)
+                        : launch_early(indexer_paged_score_kernel<64>, dim3(sms), dim3(kThreads),
+                                       Score<64>::kSmem, stream, a);
         if (e != cudaSuccess) return e;
     }
     // CTAs a token: enough to hold the longest row the table allows in their

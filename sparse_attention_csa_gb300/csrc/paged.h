@@ -6,9 +6,41 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "csa.h"
+#include "tmap.h"
 
 namespace csa {
+
+// Number of SMs of the current device, and whether this is the first call of
+// this place (a static of the caller's) in the device's present context: a
+// kernel's attributes are set once for each.
+constexpr int kPagedDevices = 64;
+struct PerContext {
+    std::atomic<unsigned long long> seen[kPagedDevices];
+    std::atomic<int> sms[kPagedDevices];
+};
+inline cudaError_t enter_context(PerContext &pc, int *sms, bool *first, unsigned long long *ctx,
+                                 int *device) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kPagedDevices) return cudaErrorInvalidDevice;
+    *device = dev;
+    *ctx = current_context_id();
+    *first = *ctx == 0 || pc.seen[dev].load(std::memory_order_acquire) != *ctx;
+    *sms = pc.sms[dev].load(std::memory_order_relaxed);
+    if (*sms == 0) {
+        e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+        if (e != cudaSuccess) return e;
+        pc.sms[dev].store(*sms, std::memory_order_relaxed);
+    }
+    return cudaSuccess;
+}
+inline void entered_context(PerContext &pc, int device, unsigned long long ctx) {
+    pc.seen[device].store(ctx, std::memory_order_release);
+}
 
 struct RopeFreqsArgs {
     double theta, factor, beta_fast, beta_slow;

@@ -10,9 +10,17 @@
 //
 // Memory bound: a block first turns its tokens' angles into a shared table of
 // (cos, sin), computed once for all heads of a token, and then streams 16-byte
-// pieces. Angles: p f_i is formed and reduced to a fraction of a turn in 64
-// bits (at p = 2^20 a 32-bit product is off by up to 2^-5 radians); the
-// fraction, at most half a turn, is then exact to 2^-25 in 32 bits, and
+// pieces. (Several pieces a thread in flight at once cost more in registers,
+// hence blocks on an SM, than they gained: 8192 x 64 heads of 512 bf16 dims,
+// 1.07 GB, 247 us with four, 166 us with one.)
+//
+// Angles need 64 bits (at p = 2^20 a 32-bit product p f is off by up to 2^-5
+// radians), but 64-bit floating point is slow here. So a block turns each
+// frequency once into a fraction of a turn per position in fixed point, in
+// units of 2^-64 turns; p times that, modulo 2^64, is the angle without its
+// whole turns: three integer multiplications, exact but for the frequency's
+// own rounding (2^-65 turns, times p). Its upper 32 bits, as a signed
+// fraction, are half a turn at most and exact to 2^-25 turns as a float, and
 // sincospif gives the factors.
 #include "common.cuh"
 #include "internal.h"
@@ -25,12 +33,20 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kTable = 2048;    // (cos, sin) pairs per block: 16 KB
 constexpr int kMaxRows = 128;   // tokens per block
+constexpr int kMaxPairs = 512;  // rope_dim <= 1024
+constexpr int kPieces = 4;      // copied pieces a thread of the append takes
 
-__device__ __forceinline__ float2 cos_sin(int64_t p, double f, float sign, float m) {
-    double turns = (double)p * f * 0.15915494309189533577;  // / 2 pi
-    turns -= rint(turns);
+// Turns per position of frequency f (radians), modulo 1, in units of 2^-64.
+__device__ __forceinline__ uint64_t fixed_turns(double f) {
+    double turns = f * 0.15915494309189533577;  // / 2 pi
+    turns -= floor(turns);
+    return __double2ull_rn(turns * 18446744073709551616.0);
+}
+
+__device__ __forceinline__ float2 cos_sin(int64_t p, uint64_t turns, float sign, float m) {
+    const int32_t frac = (int32_t)(((uint64_t)p * turns) >> 32);
     float s, c;
-    sincospif(2.0f * (float)turns, &s, &c);
+    sincospif((float)frac * 0x1p-31f, &s, &c);
     return make_float2(m * c, m * sign * s);
 }
 
@@ -130,11 +146,29 @@ __global__ void rope_freqs_kernel(RopeFreqsArgs a) {
 
 // Block: `tb` tokens x `hb` heads.
 template <typename T, int V, bool HALF>
-__global__ void __launch_bounds__(kThreads) rope_kernel(RopeArgs a, int tb, int hb) {
+__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs a, int tb, int hb) {
     __shared__ float2 tab[kTable];
+    __shared__ uint64_t turns[kMaxPairs];
     const int32_t t0 = blockIdx.x * tb, h0 = blockIdx.y * hb;
     const int nt = min(tb, a.T - t0), nh = min(hb, a.H - h0), np = a.n / 2;
     const float sign = a.inverse ? -1.0f : 1.0f;
+    grid_dependency_wait();
+    launch_dependents();
+    const T *x = static_cast<const T *>(a.x) + t0 * a.x_stride + (int64_t)h0 * a.D;
+    T *y = static_cast<T *>(a.out) + t0 * a.out_stride + (int64_t)h0 * a.D;
+    const int rows = nt * nh;
+    for (int i = threadIdx.x; i < np; i += kThreads) turns[i] = fixed_turns(__ldg(a.inv_freq + i));
+    if (a.x != a.out) {  // first: the copies need no angles
+        const int uc = (a.D - a.n) / V;  // copied units per (token, head)
+        for (int i = threadIdx.x; i < rows * uc; i += kThreads) {
+            const int row = i / uc, u = i - row * uc, r = row / nh, h = row - r * nh;
+            const int64_t o = (int64_t)h * a.D + (u * V < a.off ? u * V : u * V + a.n);
+            float v[V];
+            load_v<T, V>(x + r * a.x_stride + o, v);
+            store_v<T, V>(y + r * a.out_stride + o, v);
+        }
+    }
+    __syncthreads();
     for (int i = threadIdx.x; i < nt * np; i += kThreads) {
         const int r = i / np;
         const int32_t t = t0 + r;
@@ -148,38 +182,44 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(RopeArgs a, int tb, int 
             else
                 report_error(a.err, kErrCheck, kKerRope, 1);
         }
-        tab[i] = cos_sin(p * a.pos_stride, __ldg(a.inv_freq + (i - r * np)), sign, a.mscale);
+        tab[i] = cos_sin(p * a.pos_stride, turns[i - r * np], sign, a.mscale);
     }
     __syncthreads();
-    const T *x = static_cast<const T *>(a.x) + (int64_t)h0 * a.D;
-    T *y = static_cast<T *>(a.out) + (int64_t)h0 * a.D;
-    const int ur = np / V, rows = nt * nh;  // turned units per (token, head)
+    const int ur = np / V;  // turned units
     for (int i = threadIdx.x; i < rows * ur; i += kThreads) {
         const int row = i / ur, u = i - row * ur, r = row / nh, h = row - r * nh;
         const int64_t o = (int64_t)h * a.D + a.off;
-        turn_pairs<T, T, V, HALF>(x + (t0 + r) * a.x_stride + o, y + (t0 + r) * a.out_stride + o,
-                                  tab + r * np, u * V, a.n);
-    }
-    if (a.x == a.out) return;
-    const int uc = (a.D - a.n) / V;  // copied units
-    for (int i = threadIdx.x; i < rows * uc; i += kThreads) {
-        const int row = i / uc, u = i - row * uc, r = row / nh, h = row - r * nh;
-        const int e = u * V < a.off ? u * V : u * V + a.n;
-        const int64_t o = (int64_t)h * a.D + e;
-        float v[V];
-        load_v<T, V>(x + (t0 + r) * a.x_stride + o, v);
-        store_v<T, V>(y + (t0 + r) * a.out_stride + o, v);
+        turn_pairs<T, T, V, HALF>(x + r * a.x_stride + o, y + r * a.out_stride + o, tab + r * np, u * V,
+                                  a.n);
     }
 }
 
 // Block: `tb` rows. Rows whose slot cannot be named are skipped.
 template <typename T, int V, bool HALF>
-__global__ void __launch_bounds__(kThreads) cache_append_kernel(AppendArgs a, int tb) {
+__global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_constant__ AppendArgs a, int tb) {
     __shared__ float2 tab[kTable];
+    __shared__ uint64_t turns[kMaxPairs];
     __shared__ int64_t slot[kMaxRows];
     const int32_t t0 = blockIdx.x * tb;
     const int nt = min(tb, a.T - t0), np = a.n / 2;
-    for (int r = threadIdx.x; r < nt; r += blockDim.x) {
+    grid_dependency_wait();
+    launch_dependents();
+    const T *x = static_cast<const T *>(a.rows) + t0 * a.row_stride;
+    const int ur = np / V, uc = (a.D - a.n) / V;
+    // fp32: the dims that are only copied are on their way while the slots are
+    // found (8005 rows of 512: 8.4 us, 9.4 without). bf16 rows, half as long,
+    // lose by it (16368 rows of 512: 16 us, 10.9 without).
+    constexpr int kAhead = sizeof(T) == 4 ? kPieces : 0;
+    float v[kAhead + 1][V];
+#pragma unroll
+    for (int z = 0; z < kAhead; ++z) {
+        const int i = threadIdx.x + z * kThreads;
+        if (i < nt * uc) {
+            const int r = i / uc, u = i - r * uc;
+            load_v<T, V>(x + r * a.row_stride + (u * V < a.off ? u * V : u * V + a.n), v[z]);
+        }
+    }
+    for (int r = threadIdx.x; r < nt; r += kThreads) {
         const int32_t p = __ldg(a.row_pos + t0 + r);
         const int32_t b = paged_seq(a.row_seq, a.batch, t0 + r, p);
         int64_t s = -1;
@@ -187,28 +227,38 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(AppendArgs a, in
         if (b == -2 || (b >= 0 && s < 0)) report_error(a.err, kErrCheck, kKerAppend, b < 0 ? 1 : 2);
         slot[r] = s;
     }
-    for (int i = threadIdx.x; i < nt * np; i += blockDim.x) {
-        const int r = i / np;
-        const int64_t p = __ldg(a.row_pos + t0 + r);
-        tab[i] = cos_sin(p * a.pos_stride, __ldg(a.inv_freq + (i - r * np)), 1.0f, a.mscale);
-    }
+    for (int i = threadIdx.x; i < np; i += kThreads) turns[i] = fixed_turns(__ldg(a.inv_freq + i));
     __syncthreads();
-    const T *x = static_cast<const T *>(a.rows);
-    const int ur = np / V, uc = (a.D - a.n) / V;
-    for (int i = threadIdx.x; i < nt * ur; i += blockDim.x) {
-        const int r = i / ur, u = i - r * ur;
-        if (slot[r] >= 0)
-            turn_pairs<T, __nv_bfloat16, V, HALF>(x + (t0 + r) * a.row_stride + a.off,
-                                                  a.cache + slot[r] * a.D + a.off, tab + r * np,
-                                                  u * V, a.n);
+#pragma unroll
+    for (int z = 0; z < kAhead; ++z) {
+        const int i = threadIdx.x + z * kThreads;
+        if (i < nt * uc) {
+            const int r = i / uc, u = i - r * uc;
+            if (slot[r] >= 0)
+                store_v<__nv_bfloat16, V>(a.cache + slot[r] * a.D + (u * V < a.off ? u * V : u * V + a.n),
+                                          v[z]);
+        }
     }
-    for (int i = threadIdx.x; i < nt * uc; i += blockDim.x) {
+    for (int i = threadIdx.x + kAhead * kThreads; i < nt * uc; i += kThreads) {
         const int r = i / uc, u = i - r * uc;
         const int e = u * V < a.off ? u * V : u * V + a.n;
         if (slot[r] < 0) continue;
-        float v[V];
-        load_v<T, V>(x + (t0 + r) * a.row_stride + e, v);
-        store_v<__nv_bfloat16, V>(a.cache + slot[r] * a.D + e, v);
+        float w[V];
+        load_v<T, V>(x + r * a.row_stride + e, w);
+        store_v<__nv_bfloat16, V>(a.cache + slot[r] * a.D + e, w);
+    }
+    if (np == 0) return;
+    for (int i = threadIdx.x; i < nt * np; i += kThreads) {
+        const int r = i / np;
+        const int64_t p = __ldg(a.row_pos + t0 + r);
+        tab[i] = cos_sin(p * a.pos_stride, turns[i - r * np], 1.0f, a.mscale);
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < nt * ur; i += kThreads) {
+        const int r = i / ur, u = i - r * ur;
+        if (slot[r] >= 0)
+            turn_pairs<T, __nv_bfloat16, V, HALF>(x + r * a.row_stride + a.off,
+                                                  a.cache + slot[r] * a.D + a.off, tab + r * np, u * V, a.n);
     }
 }
 
@@ -229,9 +279,9 @@ cudaError_t launch_rope(const RopeArgs &a, cudaStream_t stream) {
     const bool vec = aligned(a.x, a.x_stride * es) && aligned(a.out, a.out_stride * es) &&
                      a.D % V == 0 && a.off % V == 0 && a.n % (2 * V) == 0;
     const int units = (a.x == a.out ? a.n : a.D) / (vec ? V : 1);
-    // rows (token, head) per block: about eight units a thread, fewer while
+    // rows (token, head) per block: about sixteen units a thread, fewer while
     // that leaves SMs without a block
-    int64_t rows = max(1, 8 * kThreads / max(units, 1));
+    int64_t rows = max(1, 16 * kThreads / max(units, 1));
     rows = min(rows, max((int64_t)1, (int64_t)a.T * a.H / 304));
     const int hb = (int)min((int64_t)a.H, rows);
     const int tb = (int)max((int64_t)1, min(min(rows / hb, (int64_t)kMaxRows), (int64_t)(kTable / (a.n / 2))));
@@ -239,19 +289,15 @@ cudaError_t launch_rope(const RopeArgs &a, cudaStream_t stream) {
 #define CSA_ROPE(T, VV)                                                          \
     do {                                                                         \
         if (a.half)                                                              \
-            rope_kernel<T, VV, true><<<grid, kThreads, 0, stream>>>(a, tb, hb);  \
+            return launch_early(rope_kernel<T, VV, true>, grid, dim3(kThreads), 0, stream, a, tb, hb);  \
         else                                                                     \
-            rope_kernel<T, VV, false><<<grid, kThreads, 0, stream>>>(a, tb, hb); \
+            return launch_early(rope_kernel<T, VV, false>, grid, dim3(kThreads), 0, stream, a, tb, hb); \
     } while (0)
-    if (a.f32) {
-        if (vec) CSA_ROPE(float, 4);
-        else CSA_ROPE(float, 1);
-    } else {
-        if (vec) CSA_ROPE(__nv_bfloat16, 8);
-        else CSA_ROPE(__nv_bfloat16, 1);
-    }
+    if (a.f32 && vec) CSA_ROPE(float, 4);
+    if (a.f32) CSA_ROPE(float, 1);
+    if (vec) CSA_ROPE(__nv_bfloat16, 8);
+    CSA_ROPE(__nv_bfloat16, 1);
 #undef CSA_ROPE
-    return cudaGetLastError();
 }
 
 cudaError_t launch_cache_append(const AppendArgs &a, cudaStream_t stream) {
@@ -259,7 +305,7 @@ cudaError_t launch_cache_append(const AppendArgs &a, cudaStream_t stream) {
     const bool vec = aligned(a.rows, a.row_stride * es) && aligned(a.cache, a.D * 2) &&
                      a.D % 8 == 0 && a.off % 8 == 0 && a.n % 16 == 0;
     const int units = a.D / (vec ? 8 : 1);
-    int rows = max(1, 4 * kThreads / max(units, 1));
+    int rows = max(1, kPieces * kThreads / max(units, 1));
     rows = min(rows, max(1, a.T / 304));
     int tb = min(rows, kMaxRows);
     if (a.n > 0) tb = max(1, min(tb, kTable / (a.n / 2)));
@@ -267,19 +313,15 @@ cudaError_t launch_cache_append(const AppendArgs &a, cudaStream_t stream) {
 #define CSA_APPEND(T, VV)                                                          \
     do {                                                                           \
         if (a.half)                                                                \
-            cache_append_kernel<T, VV, true><<<grid, kThreads, 0, stream>>>(a, tb); \
+            return launch_early(cache_append_kernel<T, VV, true>, grid, dim3(kThreads), 0, stream, a, tb); \
         else                                                                       \
-            cache_append_kernel<T, VV, false><<<grid, kThreads, 0, stream>>>(a, tb); \
+            return launch_early(cache_append_kernel<T, VV, false>, grid, dim3(kThreads), 0, stream, a, tb); \
     } while (0)
-    if (a.f32) {
-        if (vec) CSA_APPEND(float, 8);
-        else CSA_APPEND(float, 1);
-    } else {
-        if (vec) CSA_APPEND(__nv_bfloat16, 8);
-        else CSA_APPEND(__nv_bfloat16, 1);
-    }
+    if (a.f32 && vec) CSA_APPEND(float, 8);
+    if (a.f32) CSA_APPEND(float, 1);
+    if (vec) CSA_APPEND(__nv_bfloat16, 8);
+    CSA_APPEND(__nv_bfloat16, 1);
 #undef CSA_APPEND
-    return cudaGetLastError();
 }
 
 }  // namespace csa

@@ -862,14 +862,18 @@ size_t mla_paged_workspace_bytes(int32_t T, int32_t H) {
 }
 
 cudaError_t launch_sparse_mla_paged(MlaPagedArgs a, cudaStream_t stream) {
-    int dev = 0, sms = 0;
-    cudaError_t e = cudaGetDevice(&dev);
+    static PerContext pc;
+    int sms, dev;
+    bool first;
+    unsigned long long ctx;
+    cudaError_t e = enter_context(pc, &sms, &first, &ctx, &dev);
     if (e != cudaSuccess) return e;
-    e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(sparse_mla_paged_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)kSmemBytes);
-    if (e != cudaSuccess) return e;
+    if (first) {
+        e = cudaFuncSetAttribute(sparse_mla_paged_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)kSmemBytes);
+        if (e != cudaSuccess) return e;
+        entered_context(pc, dev, ctx);
+    }
     CUtensorMap q_map;
     if (!encode_bf16_3d(&q_map, a.q, 512, a.H, a.T, 64, a.H, 1)) return cudaErrorInvalidValue;
     const int grid = min(sms, kMaxGrid);
