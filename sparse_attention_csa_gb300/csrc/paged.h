@@ -142,8 +142,8 @@ __device__ __forceinline__ int64_t paged_row(const PagedRows &p, int32_t b, int3
 // sequence number is outside the batch.
 __device__ __forceinline__ int32_t paged_seq(const int32_t *q_seq, int32_t batch, int32_t t,
                                              int32_t pos) {
+    const int32_t b = q_seq ? __ldg(q_seq + t) : t;  // not behind the position's load
     if (pos < 0) return -1;
-    const int32_t b = q_seq ? __ldg(q_seq + t) : t;
     return (uint32_t)b < (uint32_t)batch ? b : -2;
 }
 

@@ -15,27 +15,27 @@
 // which the CTA that holds a token's first tile describes and a second kernel
 // joins. The split depends on the sizes alone, so results repeat bit by bit.
 //
-// A tile. All heads share a row, which is both key and value, so the products
-// are transposed, with the tile on the MMA's M side, and a tile is loaded once
-// for both:
-//     S^T: keys x heads, K = 512.  64 keys fill half of M = 128, which costs
-//          the tensor core as much as all of it, so the other half of M takes
-//          the same keys' dims 256-511 and N = 128 the heads against the low
-//          and the high dims of Q: 16 MMAs (64 cycles each) in place of 32 (58
-//          each). Of the four blocks of the result the two matching ones are
-//          added. Rows of the low and the high half alternate in groups of 8,
-//          so a key's two partial scores sit 8 lanes apart in one warp.
-//     O^T: 4 slabs of 128 dims x 64 heads, K = 64 keys, the same bytes read
-//          MN-major.
-// Shared memory holds Q (64 KB), two tiles (128 KB) and two P (16 KB); tensor
-// memory two S^T (256 columns) and O^T (256). The scores of a tile are issued
-// while the previous tile's softmax runs. Rows are gathered by cp.async; their
+// A tile. All heads share a row, which is both key and value, so a tile is
+// loaded once for two products:
+//     S = Q K^T: heads x keys, K = 512. 64 heads fill half of M = 128, which
+//          costs the tensor core as much as all of it, so the other half of M
+//          takes the heads' dims 256-511 and N = 128 the keys' low and high
+//          dims: 16 MMAs (64 cycles each) in place of 32 (58 each). Of the
+//          four blocks of the result the two matching ones are added; rows of
+//          the low and the high half alternate in groups of 8, so a head's
+//          two partial scores sit 8 lanes apart in one warp. Q is the operand
+//          in tensor memory (128 columns), which leaves shared memory to
+//          three tiles; a token's Q comes through the tiles' stages like one.
+//     O^T += V^T P^T: 4 slabs of 128 dims x 64 heads, K = 64 keys; V is the
+//          K tile's bytes read MN-major.
+// Shared memory holds three tiles (192 KB) and two P (16 KB); tensor memory Q
+// (128 columns), S (128) and O^T (256). The scores of the next tile are
+// computed while this one's softmax runs. Rows are gathered by cp.async; their
 // pages are found some tiles ahead by a warp of its own.
 #include "common.cuh"
 #include "internal.h"
 #include "paged.h"
 #include "tc_ptx.cuh"
-#include "tmap.h"
 
 namespace csa {
 
@@ -54,20 +54,22 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
 // shared memory map (offsets from a 1024-byte aligned base)
-constexpr uint32_t kOffQ = 0;       // 4 dim groups x [low, high] x [64 heads x 128 B]
-constexpr uint32_t kOffKV = 65536;  // 2 stages x 4 dim groups x 8 x [low, high] x [8 keys x 128 B]
-constexpr uint32_t kStage = 65536;
-constexpr uint32_t kOffP = 196608;  // 2 x [64 keys x 64 heads] bf16, MN-major
-constexpr uint32_t kOffMisc = 212992;
+constexpr int kStages = 3;
+constexpr uint32_t kStage = 65536;  // 4 dim groups x 8 x [low, high] x [8 keys x 128 B]
+constexpr uint32_t kOffP = kStages * kStage;  // 2 x [64 heads x 64 keys] bf16, K-major
+constexpr uint32_t kOffMisc = kOffP + 16384;
 
 // tensor memory columns
-constexpr uint32_t kColS = 0;    // 2 x 128
+constexpr uint32_t kColQ = 0;    // [low, high] heads x 256 dims, two a column
+constexpr uint32_t kColS = 128;  // [low, high] heads x [low, high] keys
 constexpr uint32_t kColO = 256;  // 4 slabs of 128 d x 64 heads
 constexpr uint32_t kTmemCols = 512;
 
 struct Join {
-    int32_t t, first, last, pad;  // token split over CTAs first..last (t < 0: none)
+    int32_t t, first, last, pad;  // token t is spread over CTAs first..last
 };
+// Join entries: one a token while there are no more tokens than CTAs, else one
+// a CTA, of the token that starts in it and goes on in others.
 
 // Workspace: Join [kMaxGrid], then m and l [2 kMaxGrid][64], then the sums
 // [2 kMaxGrid][ceil(H / 4)][512][4 heads]: a thread of the epilogue holds one
@@ -167,9 +169,9 @@ struct Piece {
 };
 
 struct Misc {
-    uint64_t q_full, q_empty;
-    uint64_t kv_full[2], kv_empty[2];
-    uint64_t s_full[2], p_full[2];
+    uint64_t q_full;
+    uint64_t kv_full[kStages], kv_empty[kStages];
+    uint64_t s_full, s_empty, p_full[2];
     uint64_t o_full, o_empty, drain;
     uint64_t ring_full[kRing], ring_empty[kRing];
     const __nv_bfloat16 *ring[kRing][kTile];  // pool rows of a tile's slots, nullptr: no key
@@ -180,11 +182,10 @@ struct Misc {
     int32_t run_t;         // token holding the CTA's next tile
     int32_t n_pieces;
     int32_t scan[kThreads / 32 + 1];
-    uint32_t valid[2][2];  // per stage and loader warp: 32 slot bits
+    uint32_t valid[kStages][2];  // per stage and loader warp: 32 slot bits
     Piece piece[kPieces];
-    alignas(16) float red[2][4][64];  // [tile parity][lane quarter][head]
-    alignas(16) float m[64];          // running maximum (base 2)
-    alignas(16) float fac[64];        // a rescaling's or the epilogue's factor
+    float red[2][2][64];       // [tile parity][warpgroup][head]
+    alignas(16) float fac[64];  // a rescaling's or the epilogue's factor
 };
 
 constexpr size_t kSmemBytes = kOffMisc + sizeof(Misc) + 1024;
@@ -210,20 +211,43 @@ struct Ctx {
     }
 };
 
-// AND / OR of v over the 128 threads of named barrier `id`.
-__device__ __forceinline__ bool bar_and(uint32_t id, bool v) {
+// AND / OR of v over the 256 softmax threads.
+__device__ __forceinline__ bool all_of(bool v) {
     uint32_t out;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.u32 p, %1, 0;\n\t"
-        "bar.red.and.pred q, %2, 128, p;\n\t"
+        "bar.red.and.pred q, 1, 256, p;\n\t"
         "selp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(out)
-        : "r"((uint32_t)v), "r"(id)
+        : "r"((uint32_t)v)
         : "memory");
     return out != 0;
 }
-__device__ __forceinline__ bool bar_or(uint32_t id, bool v) { return !bar_and(id, !v); }
+__device__ __forceinline__ bool any_of(bool v) { return !all_of(!v); }
+
+// D += A B with A in tensor memory (lane = row, two bf16 of K a column).
+__device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                            uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint4 (&v)[8]) {
+    float f[32];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        f[4 * i] = __uint_as_float(v[i].x);
+        f[4 * i + 1] = __uint_as_float(v[i].y);
+        f[4 * i + 2] = __uint_as_float(v[i].z);
+        f[4 * i + 3] = __uint_as_float(v[i].w);
+    }
+    tc::tmem_st32(taddr, f);  // the bits as they are
+}
 
 // 16 bytes global -> shared; `bytes` 0 writes zeros (nothing is read then).
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32_t bytes) {
@@ -237,32 +261,8 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
                  : "memory");
 }
 
-// Heads of one thread: 16 of its warpgroup's 32, by bit 3 of its lane. The 16
-// lanes that agree in that bit hold 16 keys of the same heads:
-// reduces each of the 16 values over them; a lane keeps value sum_index(lane).
-template <bool kMax>
-__device__ __forceinline__ float reduce_scatter16(const float (&x)[16], int lane) {
-    float v[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = x[i];
-#pragma unroll
-    for (int s = 0; s < 4; ++s) {
-        const int bit = s == 0 ? 16 : 8 >> s, w = 8 >> s;  // bits 4, 2, 1, 0; 8, 4, 2, 1 values kept
-        const bool hi = lane & bit;
-#pragma unroll
-        for (int i = 0; i < w; ++i) {
-            const float other = __shfl_xor_sync(0xffffffffu, hi ? v[i] : v[w + i], bit);
-            const float mine = hi ? v[w + i] : v[i];
-            v[i] = kMax ? fmaxf(mine, other) : mine + other;
-        }
-    }
-    return v[0];
-}
-__device__ __forceinline__ int sum_index(int lane) { return ((lane >> 4) << 3) | (lane & 7); }
-
 __global__ void __launch_bounds__(kThreads, 1)
-sparse_mla_paged_kernel(const __grid_constant__ CUtensorMap q_map,
-                        const __grid_constant__ MlaPagedArgs a) {
+sparse_mla_paged_kernel(const __grid_constant__ MlaPagedArgs a) {
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem = reinterpret_cast<unsigned char *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -273,14 +273,14 @@ sparse_mla_paged_kernel(const __grid_constant__ CUtensorMap q_map,
     const int32_t c = blockIdx.x;
 
     if (tid == 0) {
-        tc::mbar_init(&ms->q_full, 1);
-        tc::mbar_init(&ms->q_empty, 1);
-        for (int i = 0; i < 2; ++i) {
+        tc::mbar_init(&ms->q_full, 256);
+        for (int i = 0; i < kStages; ++i) {
             tc::mbar_init(&ms->kv_full[i], kLoaders + 2);
             tc::mbar_init(&ms->kv_empty[i], 1);
-            tc::mbar_init(&ms->s_full[i], 1);
-            tc::mbar_init(&ms->p_full[i], 256);
         }
+        tc::mbar_init(&ms->s_full, 1);
+        tc::mbar_init(&ms->s_empty, 256);
+        for (int i = 0; i < 2; ++i) tc::mbar_init(&ms->p_full[i], 256);
         tc::mbar_init(&ms->o_full, 1);
         tc::mbar_init(&ms->o_empty, 256);
         tc::mbar_init(&ms->drain, 1);
@@ -294,18 +294,25 @@ sparse_mla_paged_kernel(const __grid_constant__ CUtensorMap q_map,
     if (warp == kMmaWarp) {
         tc::tmem_alloc(&ms->tmem_base, kTmemCols);
         tc::tmem_relinquish();
-        if (lane == 0) tc::tma_prefetch_desc(&q_map);
-    }
-    // heads past H: zero rows of Q, never written again
-    for (int i = tid; i < (64 - a.H) * 64; i += kThreads) {
-        const int h = a.H + (i >> 6), u = i & 63;
-        *reinterpret_cast<uint4 *>(smem + kOffQ + (u >> 3) * 8192 + h * 128 + (u & 7) * 16) =
-            make_uint4(0, 0, 0, 0);
     }
     // everything above is local: wait for the kernels before this one
     grid_dependency_wait();
     launch_dependents();
-    if (tid == 0) ws.join[c] = {-1, 0, 0, 0};
+    const bool by_token = a.T <= (int32_t)gridDim.x;
+    if (tid == 0 && !by_token) ws.join[c] = {-1, 0, 0, 0};
+    // The lists and tables, when a line each for the grid's threads covers
+    // them, are on their way to L2 while the runs are worked out.
+    {
+        const int64_t line = (int64_t)c * kThreads + tid, lines = (int64_t)gridDim.x * kThreads;
+        auto send_for = [&](const int32_t *p, int64_t n) {
+            const int64_t bytes = n * 4;
+            if (p && bytes <= lines * 128 && line * 128 < bytes)
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const char *>(p) + line * 128));
+        };
+        send_for(a.idx, (int64_t)a.T * a.topk);
+        send_for(a.ori.pages, (int64_t)a.batch * a.ori.max_pages);
+        if (a.cmp.base) send_for(a.cmp.pages, (int64_t)a.batch * a.cmp.max_pages);
+    }
     tc::fence_proxy_async_smem();
     tc::tc_fence_before();
 
@@ -352,7 +359,7 @@ sparse_mla_paged_kernel(const __grid_constant__ CUtensorMap q_map,
     __syncthreads();
 
     // counters of each role, kept across batches of pieces
-    uint32_t g = 0, np = 0, nq = 0;
+    uint32_t g = 0, np = 0;
     bool issued = false;
     int64_t done = s;
     while (done < e) {
@@ -379,7 +386,9 @@ sparse_mla_paged_kernel(const __grid_constant__ CUtensorMap q_map,
             p.slot = p.j0 == 0 && p.j1 == n ? -1 : 2 * c + (p.j0 == 0 ? 1 : 0);
             p.k = k;
             ms->piece[x] = p;
-            if (p.slot == 2 * c + 1)  // starts here, goes on in other CTAs
+            if (by_token && p.j0 == 0)
+                ws.join[t] = {t, c, p.slot < 0 ? c : (int32_t)div64(b + n - 1, per), 0};
+            else if (p.slot == 2 * c + 1)  // starts here, goes on in other CTAs
                 ws.join[c] = {t, c, (int32_t)div64(b + n - 1, per), 0};
             if (x == kPieces - 1 || t + 1 == a.T || b + n >= e) {
                 ms->n_pieces = x + 1;
@@ -395,78 +404,61 @@ sparse_mla_paged_kernel(const __grid_constant__ CUtensorMap q_map,
         }
 
         if (warp == kMmaWarp) {
-            // ================================================ Q and MMA warp
+            // ===================================================== MMA warp
             if (lane == 0) {
                 constexpr uint32_t id_s = tc::idesc_bf16(128, 128, false, false);
-                constexpr uint32_t id_o = tc::idesc_bf16(128, 64, true, true);
-                const uint64_t ds_a = tc::smem_desc(tc::smem_u32(smem + kOffKV), 16, 1024);
-                const uint64_t ds_b = tc::smem_desc(tc::smem_u32(smem + kOffQ), 16, 1024);
-                const uint64_t do_a = tc::smem_desc(tc::smem_u32(smem + kOffKV), 1024, 2048);
-                const uint64_t do_b = tc::smem_desc(tc::smem_u32(smem + kOffP), 8192, 1024);
-                auto load_q = [&](int32_t i) {  // rows past H stay zero
-                    ++nq;
-                    tc::mbar_expect_tx(&ms->q_full, (uint32_t)a.H * 1024u);
-                    for (int ch = 0; ch < 8; ++ch)
-                        tc::tma_load_3d(smem + kOffQ + (ch & 3) * 16384 + (ch >> 2) * 8192, &q_map,
-                                        &ms->q_full, 64 * ch, 0, ms->piece[i].t);
-                };
+                constexpr uint32_t id_o = tc::idesc_bf16(128, 64, true, false);
+                const uint64_t ds_b = tc::smem_desc(tc::smem_u32(smem), 16, 1024);
+                const uint64_t do_a = tc::smem_desc(tc::smem_u32(smem), 1024, 2048);
+                const uint64_t do_b = tc::smem_desc(tc::smem_u32(smem + kOffP), 16, 1024);
                 bool ok = true;
-                if (np == 0) load_q(0);
                 for (int32_t i = 0; i < n_pieces && ok; ++i, ++np) {
                     const int32_t nt = ms->piece[i].j1 - ms->piece[i].j0;
-                    if (i == 0 && np > 0) {  // a later batch's first piece
-                        if (!(ok = cx.wait(&ms->q_empty, (np & 1) ^ 1, 25))) break;
-                        load_q(0);
-                    }
+                    ++g;  // the stage of Q
                     if (!(ok = cx.wait(&ms->q_full, np & 1, 20))) break;
                     // O^T of tile jo and scores of tile js, whichever is ready
                     // first, O^T before scores: it frees a stage, and the load
                     // that follows is the longest part of a tile's way.
                     int32_t js = 0, jo = 0;
-                    const uint32_t g0 = g;
+                    const uint32_t k0 = g - np - 1;  // key tiles before this piece
                     uint64_t since = 0;
                     while (jo < nt) {
-                        const uint32_t xs = g0 + js, xo = g0 + jo;
+                        const uint32_t xs = k0 + js, xo = k0 + jo;  // key tiles
+                        const uint32_t gs = g + js, go = g + jo;    // their stages
                         if (jo < js && tc::mbar_try_wait(&ms->p_full[xo & 1], (xo >> 1) & 1, 20)) {
                             if (jo == 0 && !(ok = cx.wait(&ms->o_empty, (np & 1) ^ 1, 23))) break;
                             tc::tc_fence_after();
-                            const uint32_t st = (xo & 1) * kStage, pb = (xo & 1) * 8192;
-#pragma unroll
-                            for (int d = 0; d < 4; ++d) {
-#pragma unroll
-                                for (int kk = 0; kk < 4; ++kk)
-                                    tc::mma_bf16(tmem + kColO + 64 * d,
-                                                 tc::desc_add(do_a, st + d * 16384 + kk * 4096),
-                                                 tc::desc_add(do_b, pb + kk * 2048), id_o, (jo | kk) != 0);
-                            }
-                            tc::mma_commit(&ms->kv_empty[xo & 1]);
-                            ++jo;
-                            since = 0;
-                            continue;
-                        }
-                        if (js < nt && js <= jo + 1 &&
-                            tc::mbar_try_wait(&ms->kv_full[xs & 1], (xs >> 1) & 1, 20)) {
-                            tc::fence_proxy_async_smem();  // cp.async wrote through the generic proxy
-                            tc::tc_fence_after();
-                            const uint32_t st = (xs & 1) * kStage;
+                            const uint32_t st = (go % kStages) * kStage, pb = (xo & 1) * 8192;
 #pragma unroll
                             for (int d = 0; d < 4; ++d)
 #pragma unroll
                                 for (int kk = 0; kk < 4; ++kk)
-                                    tc::mma_bf16(tmem + kColS + 128 * (xs & 1),
-                                                 tc::desc_add(ds_a, st + d * 16384 + kk * 32),
-                                                 tc::desc_add(ds_b, d * 16384 + kk * 32), id_s,
-                                                 (d | kk) != 0);
-                            issued = true;
-                            tc::mma_commit(&ms->s_full[xs & 1]);
+                                    tc::mma_bf16(tmem + kColO + 64 * d,
+                                                 tc::desc_add(do_a, st + d * 16384 + kk * 4096),
+                                                 tc::desc_add(do_b, pb + kk * 32), id_o, (jo | kk) != 0);
+                            tc::mma_commit(&ms->kv_empty[go % kStages]);
+                            ++jo;
                             since = 0;
-                            if (++js == nt) {  // Q is read: the next piece's, under this O^T
-                                tc::mma_commit(&ms->q_empty);
-                                if (i + 1 < n_pieces) {
-                                    if (!(ok = cx.wait(&ms->q_empty, np & 1, 25))) break;
-                                    load_q(i + 1);
-                                }
-                            }
+                            continue;
+                        }
+                        // js <= jo + 1: P of tile js goes where P of tile js - 2 was
+                        if (js < nt && js <= jo + 1 &&
+                            tc::mbar_try_wait(&ms->kv_full[gs % kStages], (gs / kStages) & 1, 20) &&
+                            (xs == 0 || tc::mbar_try_wait(&ms->s_empty, (xs - 1) & 1, 20))) {
+                            tc::fence_proxy_async_smem();  // cp.async wrote through the generic proxy
+                            tc::tc_fence_after();
+                            const uint32_t st = (gs % kStages) * kStage;
+#pragma unroll
+                            for (int d = 0; d < 4; ++d)
+#pragma unroll
+                                for (int kk = 0; kk < 4; ++kk)
+                                    mma_bf16_ta(tmem + kColS, tmem + kColQ + 8 * (4 * d + kk),
+                                                tc::desc_add(ds_b, st + d * 16384 + kk * 32), id_s,
+                                                (d | kk) != 0);
+                            issued = true;
+                            tc::mma_commit(&ms->s_full);
+                            ++js;
+                            since = 0;
                             continue;
                         }
                         const uint64_t now = tc::globaltimer();
@@ -478,32 +470,32 @@ sparse_mla_paged_kernel(const __grid_constant__ CUtensorMap q_map,
                         }
                     }
                     if (!ok) break;
-                    g = g0 + nt;
+                    g += nt;
                     tc::mma_commit(&ms->o_full);
                 }
             }
             __syncwarp();
         } else if (warp == 8 || warp == 9) {
             // ================================================= loader warps
-            // Warp w copies slots 32 w .. 32 w + 31 of every tile.
+            // Warp w copies rows 32 w .. 32 w + 31 of every tile.
             const int w = warp - 8;
             bool ok = true;
             for (int32_t i = 0; i < n_pieces && ok; ++i) {
-                const int32_t nt = ms->piece[i].j1 - ms->piece[i].j0;
+                const int32_t nt = 1 + ms->piece[i].j1 - ms->piece[i].j0;  // Q, then the keys
                 for (int32_t j = 0; j < nt; ++j, ++g) {
                     ok = __all_sync(0xffffffffu,
                                     cx.wait(&ms->ring_full[g % kRing], (g / kRing) & 1, 40));
                     if (!ok) break;
                     const __nv_bfloat16 *mine = ms->ring[g % kRing][32 * w + lane];
                     tc::mbar_arrive(&ms->ring_empty[g % kRing]);
-                    const uint32_t m = __ballot_sync(0xffffffffu, mine != nullptr);
-                    ok = __all_sync(0xffffffffu, cx.wait(&ms->kv_empty[g & 1], ((g >> 1) & 1) ^ 1, 41));
+                    const uint32_t m = __ballot_sync(0xffffffffu, mine != nullptr), st = g % kStages;
+                    ok = __all_sync(0xffffffffu, cx.wait(&ms->kv_empty[st], ((g / kStages) & 1) ^ 1, 41));
                     if (!ok) break;
                     // Half a row (512 bytes) an instruction: pieces of 128 bytes
                     // of several rows took twice as long to issue. Lane: dim
                     // group lane / 8, 16-byte unit lane % 8 of its 128 bytes.
-                    const uint32_t stage = tc::smem_u32(smem + kOffKV + (g & 1) * kStage) +
-                                           (lane >> 3) * 16384 + w * 4 * 2048;
+                    const uint32_t stage =
+                        tc::smem_u32(smem + st * kStage) + (lane >> 3) * 16384 + w * 4 * 2048;
                     const int u = lane & 7;
 #pragma unroll
                     for (int r = 0; r < 32; ++r) {
@@ -515,10 +507,10 @@ sparse_mla_paged_kernel(const __grid_constant__ CUtensorMap q_map,
                         cp_async16(dst, src + lane * 8, bytes);
                         cp_async16(dst + 1024, src + 256 + lane * 8, bytes);
                     }
-                    cp_async_arrive(&ms->kv_full[g & 1]);
+                    cp_async_arrive(&ms->kv_full[st]);
                     if (lane == 0) {
-                        ms->valid[g & 1][w] = m;
-                        tc::mbar_arrive(&ms->kv_full[g & 1]);
+                        ms->valid[st][w] = m;
+                        tc::mbar_arrive(&ms->kv_full[st]);
                     }
                 }
             }
@@ -534,6 +526,15 @@ sparse_mla_paged_kernel(const __grid_constant__ CUtensorMap q_map,
                 const Keys kt = ms->piece[i].k;
                 auto at = [&](int32_t j, int x) { return (uint32_t)j * kTile + 32 * x + lane; };
                 auto row_of = [&](int32_t j, int x) { return j < j1 ? slot_row(a, kt, tt, at(j, x)) : -1; };
+                // Q first: heads past H are zero rows
+                ok = __all_sync(0xffffffffu, cx.wait(&ms->ring_empty[g % kRing], ((g / kRing) & 1) ^ 1, 51));
+                if (!ok) break;
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+                    ms->ring[g % kRing][32 * x + lane] =
+                        32 * x + lane < a.H ? a.q + ((int64_t)tt * a.H + 32 * x + lane) * 512 : nullptr;
+                tc::mbar_arrive(&ms->ring_full[g % kRing]);
+                ++g;
                 int32_t r0[2], r1[2], r2[2];
                 Slot s0[2], s1[2];
 #pragma unroll
@@ -551,12 +552,8 @@ sparse_mla_paged_kernel(const __grid_constant__ CUtensorMap q_map,
                     ok = __all_sync(0xffffffffu,
                                     cx.wait(&ms->ring_empty[g % kRing], ((g / kRing) & 1) ^ 1, 50));
                     if (!ok) break;
-                    const __nv_bfloat16 *row[2];
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        row[x] = slot_ptr(a, s0[x]);
-                        ms->ring[g % kRing][32 * x + lane] = row[x];
-                    }
+                    for (int x = 0; x < 2; ++x) ms->ring[g % kRing][32 * x + lane] = slot_ptr(a, s0[x]);
                     tc::mbar_arrive(&ms->ring_full[g % kRing]);
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
@@ -568,110 +565,125 @@ sparse_mla_paged_kernel(const __grid_constant__ CUtensorMap q_map,
             }
         } else {
             // =========================================== softmax + epilogue
-            // Warpgroup wg: heads 32 wg .. 32 wg + 31. A thread's lane of S^T
-            // is key slot `slot_k`, low or high dims by `hi`; it takes the 16
-            // heads from hb on, its partner 8 lanes away the others.
-            const int wg = warp >> 2, q4 = warp & 3, h0 = 32 * wg, hi = (lane >> 3) & 1;
-            const int hb = h0 + 16 * hi, slot_k = 16 * q4 + 8 * (lane >> 4) + (lane & 7);
-            const uint32_t bar = 1 + wg;
+            // A thread's lane of S is head `h`, low or high dims by `hi`; of
+            // the 32 keys of its warpgroup wg it takes 16 (key0 on), its
+            // partner 8 lanes away the others.
+            const int wg = warp >> 2, q4 = warp & 3, hi = (lane >> 3) & 1;
+            const int h = 16 * q4 + 8 * (lane >> 4) + (lane & 7);
             const uint32_t lane_addr = tmem + ((uint32_t)(32 * q4) << 16);
             const float sc = a.softmax_scale * kLog2e;
-            bool ok = true, stop = false;
+            // Q of the piece whose stage is next, to tensor memory: this
+            // thread's row is dims 256 hi .. + 255 of head h, its warpgroup's
+            // half of the columns.
+            auto take_q = [&]() -> bool {
+                if (!all_of(cx.wait(&ms->kv_full[g % kStages], (g / kStages) & 1, 34))) return false;
+                const unsigned char *q = smem + (g % kStages) * kStage + 2 * wg * 16384 + (h >> 3) * 2048 +
+                                         hi * 1024 + (h & 7) * 128;
+#pragma unroll
+                for (int d = 0; d < 2; ++d) {
+                    uint4 v[8];
+#pragma unroll
+                    for (int u = 0; u < 8; ++u)
+                        v[u] = *reinterpret_cast<const uint4 *>(q + d * 16384 + ((u ^ (h & 7)) << 4));
+                    tmem_st32(lane_addr + kColQ + 64 * wg + 32 * d, v);
+                }
+                tc::tmem_wait_st();
+                tc::tc_fence_before();
+                tc::mbar_arrive(&ms->q_full);
+                tc::named_bar_sync(1, 256);
+                if (tid == 0) tc::mbar_arrive(&ms->kv_empty[g % kStages]);
+                ++g;
+                return true;
+            };
+            bool ok = true, stop = !take_q();
             for (int32_t i = 0; i < n_pieces && !stop; ++i, ++np) {
                 const int32_t tt = ms->piece[i].t, nt = ms->piece[i].j1 - ms->piece[i].j0;
                 const int32_t slot = ms->piece[i].slot;
-                float lp[16], m_cur[16];
-#pragma unroll
-                for (int x = 0; x < 16; ++x) {
-                    lp[x] = 0.0f;
-                    m_cur[x] = -INFINITY;
-                }
-                for (int32_t j = 0; j < nt; ++j, ++g) {
-                    ok = cx.wait(&ms->kv_full[g & 1], (g >> 1) & 1, 30) &&
-                         cx.wait(&ms->s_full[g & 1], (g >> 1) & 1, 31);
+                float m = -INFINITY, l = 0.0f;  // running maximum (base 2); this thread's share of the sum
+                uint32_t k = g - np - 1;  // key tiles so far
+                for (int32_t j = 0; j < nt; ++j, ++g, ++k) {
+                    ok = cx.wait(&ms->kv_full[g % kStages], (g / kStages) & 1, 30) &&
+                         cx.wait(&ms->s_full, k & 1, 31);
                     tc::tc_fence_after();
-                    const bool key = (ms->valid[g & 1][q4 >> 1] >> (slot_k & 31)) & 1u;
-                    float v[16];
-                    auto load_scores = [&]() {
-                        float lo[32], up[32];
-                        const uint32_t addr = lane_addr + kColS + 128 * (g & 1) + h0;
-                        tc::tmem_ld32(addr, lo);
-                        tc::tmem_ld32(addr + 64, up);
+                    const uint32_t valid = ms->valid[g % kStages][wg] >> (16 * hi);
+                    float s[16];
+                    {
+                        // columns 64 wg on: groups of 8 keys, low and high dims in turn
+                        float c0[32], c1[32];
+                        tc::tmem_ld32(lane_addr + kColS + 64 * wg, c0);
+                        tc::tmem_ld32(lane_addr + kColS + 64 * wg + 32, c1);
                         tc::tmem_wait_ld();
+                        tc::tc_fence_before();
+                        tc::mbar_arrive(&ms->s_empty);
 #pragma unroll
-                        for (int x = 0; x < 16; ++x)
-                            v[x] = (hi ? up[16 + x] : lo[x]) +
-                                   __shfl_xor_sync(0xffffffffu, hi ? up[x] : lo[16 + x], 8);
-                    };
-                    load_scores();
+                        for (int x = 0; x < 16; ++x) {
+                            const int c = 16 * (x >> 3) + (x & 7);  // low dims of key x of 16; high: + 8
+                            const float own = hi ? c1[c + 8] : c0[c], give = hi ? c0[c + 8] : c1[c];
+                            s[x] = own + __shfl_xor_sync(0xffffffffu, give, 8);
+                        }
+                    }
                     // Scores in base 2 above the running maximum, which the
                     // first tile sets (its largest weight is then exactly 1 in
                     // bf16) and later ones move only when a score exceeds it
                     // by more than kLazyMax, so that O^T is rarely rescaled;
-                    // the warpgroup agrees on it.
+                    // all softmax threads agree on it.
+                    float v[16];
                     bool over = !ok || j == 0;
                     if (j > 0) {
 #pragma unroll
                         for (int x = 0; x < 16; ++x) {
-                            v[x] = key ? fmaf(v[x], sc, -m_cur[x]) : -INFINITY;
+                            v[x] = (valid >> x) & 1u ? fmaf(s[x], sc, -m) : -INFINITY;
                             over |= v[x] > kLazyMax;
                         }
-                        over = bar_or(bar, over);
+                        over = any_of(over);
                     }
                     if (over) {
-                        if (j > 0) {
-                            ok = ok && cx.wait(&ms->kv_empty[(g - 1) & 1], ((g - 1) >> 1) & 1, 33);
-                            tc::tc_fence_after();
-                            load_scores();
+                        if (j > 0)
+                            ok = ok && cx.wait(&ms->kv_empty[(g - 1) % kStages], ((g - 1) / kStages) & 1, 33);
+                        float mt = -INFINITY;
+#pragma unroll
+                        for (int x = 0; x < 16; ++x) {
+                            v[x] = (valid >> x) & 1u ? s[x] * sc : -INFINITY;
+                            mt = fmaxf(mt, v[x]);
                         }
-                        if (!bar_and(bar, ok)) {
+                        mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 8));
+                        float(*red)[64] = ms->red[k & 1];
+                        if (!hi) red[wg][h] = mt;
+                        if (!all_of(ok)) {
                             stop = true;
                             break;
                         }
-#pragma unroll
-                        for (int x = 0; x < 16; ++x) v[x] = key ? v[x] * sc : -INFINITY;
-                        float(*red)[64] = ms->red[g & 1];
-                        red[q4][hb + sum_index(lane)] = reduce_scatter16<true>(v, lane);
-                        tc::named_bar_sync(bar, 128);
-                        bool scale = false;
-                        float al[16];
-#pragma unroll
-                        for (int x = 0; x < 16; ++x) {
-                            const float mt = fmaxf(fmaxf(red[0][hb + x], red[1][hb + x]),
-                                                   fmaxf(red[2][hb + x], red[3][hb + x]));
-                            const bool up = mt > m_cur[x] + kLazyMax;
-                            al[x] = 1.0f;
-                            if (up && m_cur[x] != -INFINITY) {
-                                al[x] = tc::ex2_approx(m_cur[x] - mt);
-                                scale = true;
-                            }
-                            if (up) m_cur[x] = mt;
-                            lp[x] *= al[x];
-                            v[x] = m_cur[x] == -INFINITY ? -INFINITY : v[x] - m_cur[x];
+                        mt = fmaxf(red[0][h], red[1][h]);
+                        float al = 1.0f;
+                        if (mt > m + kLazyMax) {  // always with the first keys: m is -inf
+                            al = m == -INFINITY ? 1.0f : tc::ex2_approx(m - mt);
+                            m = mt;
                         }
-                        if (q4 == 0 && (lane & 23) == 0) {  // one lane for each 16 heads
+                        l *= al;
 #pragma unroll
-                            for (int x = 0; x < 16; ++x) {
-                                ms->m[hb + x] = m_cur[x];
-                                ms->fac[hb + x] = al[x];
-                            }
-                        }
-                        if (j > 0 && bar_or(bar, scale)) {
+                        for (int x = 0; x < 16; ++x) v[x] = m == -INFINITY ? -INFINITY : v[x] - m;
+                        if (j > 0) {
+                            if (wg == 0 && !hi) ms->fac[h] = al;
+                            if (any_of(al != 1.0f)) {
+                                tc::tc_fence_after();
+                                const int h0 = 32 * wg;
 #pragma unroll 1
-                            for (int d = 0; d < 4; ++d) {
-                                float o[32];
-                                const uint32_t addr = lane_addr + kColO + 64 * d + h0;
-                                tc::tmem_ld32(addr, o);
-                                tc::tmem_wait_ld();
+                                for (int d = 0; d < 4; ++d) {
+                                    float o[32];
+                                    const uint32_t addr = lane_addr + kColO + 64 * d + h0;
+                                    tc::tmem_ld32(addr, o);
+                                    tc::tmem_wait_ld();
 #pragma unroll
-                                for (int x = 0; x < 32; ++x) o[x] *= ms->fac[h0 + x];
-                                tc::tmem_st32(addr, o);
+                                    for (int x = 0; x < 32; ++x) o[x] *= ms->fac[h0 + x];
+                                    tc::tmem_st32(addr, o);
+                                }
+                                tc::tmem_wait_st();
                             }
-                            tc::tmem_wait_st();
                         }
                     }
-                    // weights (bf16) -> row of P^T: 32 bytes of its 128
-                    unsigned char *prow = smem + kOffP + (g & 1) * 8192 + slot_k * 128;
+                    // weights (bf16) -> 32 bytes of row h of P
+                    unsigned char *prow = smem + kOffP + (k & 1) * 8192 + h * 128;
+                    float sum = 0.0f;
 #pragma unroll
                     for (int c8 = 0; c8 < 2; ++c8) {
                         uint32_t w4[4];
@@ -679,26 +691,31 @@ sparse_mla_paged_kernel(const __grid_constant__ CUtensorMap q_map,
                         for (int y = 0; y < 4; ++y) {
                             const int x = 8 * c8 + 2 * y;
                             const float p0 = tc::ex2_approx(v[x]), p1 = tc::ex2_approx(v[x + 1]);
-                            lp[x] += p0;
-                            lp[x + 1] += p1;
+                            sum += p0 + p1;
                             const __nv_bfloat162 pb = __floats2bfloat162_rn(p0, p1);
                             w4[y] = *reinterpret_cast<const uint32_t *>(&pb);
                         }
-                        *reinterpret_cast<uint4 *>(prow + (((hb / 8 + c8) ^ (slot_k & 7)) << 4)) =
+                        *reinterpret_cast<uint4 *>(prow + (((4 * wg + 2 * hi + c8) ^ (h & 7)) << 4)) =
                             make_uint4(w4[0], w4[1], w4[2], w4[3]);
                     }
+                    l += sum;
                     tc::fence_proxy_async_smem();
                     tc::tc_fence_before();
-                    tc::mbar_arrive(&ms->p_full[g & 1]);
+                    tc::mbar_arrive(&ms->p_full[k & 1]);
                 }
                 if (stop) break;
+                // the next piece's scores may start under this one's last O^T
+                if (i + 1 < n_pieces && !take_q()) break;
                 // ---- row sums, then O^T
-                float(*red)[64] = ms->red[g & 1];  // no step of this token reads it any more
-                red[q4][hb + sum_index(lane)] = reduce_scatter16<false>(lp, lane);
-                tc::named_bar_sync(bar, 128);
-                if (q4 == 0) {
-                    const int h = h0 + lane;
-                    const float l = (red[0][h] + red[1][h]) + (red[2][h] + red[3][h]), m = ms->m[h];
+                float(*red)[64] = ms->red[k & 1];  // no step of this token reads it any more
+                l += __shfl_xor_sync(0xffffffffu, l, 8);
+                if (!hi) red[wg][h] = l;
+                if (!all_of(ok)) {
+                    stop = true;
+                    break;
+                }
+                if (wg == 0 && !hi) {
+                    l = red[0][h] + red[1][h];
                     float f = 1.0f;  // O^T times this
                     if (slot < 0) {
                         const float sk = a.sinks && h < a.H && ms->piece[i].k.seq >= 0
@@ -710,21 +727,21 @@ sparse_mla_paged_kernel(const __grid_constant__ CUtensorMap q_map,
                         f = Z > 0.0f ? w / Z : 0.0f;
                         if (a.lse && h < a.H)
                             a.lse[(int64_t)tt * a.H + h] = (M + tc::lg2_approx(Z)) * kLn2;
-                    } else if (h < a.H) {
+                    } else {  // all 64: the join reads them by fours
                         ws.m[slot * 64 + h] = m;
                         ws.l[slot * 64 + h] = l;
                     }
                     ms->fac[h] = f;
                 }
                 ok = cx.wait(&ms->o_full, np & 1, 32);
-                if (!bar_and(bar, ok)) {
+                if (!all_of(ok)) {
                     stop = true;
                     break;
                 }
                 tc::tc_fence_after();
                 // Lane of O^T slab d: dim 64 d + lane of the low (q4 < 2) or the
-                // high half, 32 heads a thread
-                const int n_h = min(32, a.H - h0);
+                // high half; heads 32 wg on
+                const int h0 = 32 * wg, n_h = min(32, a.H - h0);
                 const int dim = (q4 >> 1) * 256 + 32 * (q4 & 1) + lane;
                 __nv_bfloat16 *outp = a.out + ((int64_t)tt * a.H + h0) * 512 + dim;
 #pragma unroll 1
@@ -749,7 +766,7 @@ sparse_mla_paged_kernel(const __grid_constant__ CUtensorMap q_map,
                                 outp[x * 512 + 64 * d] = __float2bfloat16_rn(o[x] * ms->fac[h0 + x]);
                     }
                 }
-                tc::named_bar_sync(bar, 128);  // fac, m and red are read
+                tc::named_bar_sync(1, 256);  // fac and red are read
             }
         }
         __syncthreads();
@@ -758,10 +775,9 @@ sparse_mla_paged_kernel(const __grid_constant__ CUtensorMap q_map,
 
     // ------------------------------------------------------------- teardown
     if (warp == 8 || warp == 9) asm volatile("cp.async.wait_all;" ::: "memory");
-    if (tid == 32 * kMmaWarp) {  // no copy outlives the CTA, no MMA its tensor memory
-        if (nq > 0 && !tc::mbar_wait(&ms->q_full, (nq - 1) & 1)) cx.fail(26);
-        if (issued) tc::mma_commit(&ms->drain);
-        if (issued && !tc::mbar_wait(&ms->drain, 0)) cx.fail(24);
+    if (tid == 32 * kMmaWarp && issued) {  // no MMA outlives its tensor memory
+        tc::mma_commit(&ms->drain);
+        if (!tc::mbar_wait(&ms->drain, 0)) cx.fail(24);
     }
     tc::tc_fence_before();
     __syncthreads();
@@ -769,12 +785,18 @@ sparse_mla_paged_kernel(const __grid_constant__ CUtensorMap q_map,
     if (warp == kMmaWarp) tc::tmem_dealloc(tmem, kTmemCols);
 }
 
-// Block (c, y): heads 4 y .. 4 y + 3 of the token whose first tile CTA c held
-// and that other CTAs went on with; two dims a thread. The first parts' sums
-// are on their way before their factors are known.
+// Joins the tokens that several CTAs worked on. Block (x, y) takes token x
+// (with more tokens than CTAs: the split token whose first tile CTA x held)
+// and its heads by fours, y, y + gridDim.y and so on; ND dims a thread. Few
+// blocks, about four an SM: they start only as the first kernel's CTAs leave
+// (its registers fill the SM), and a grid of 32 blocks for each CTA, most
+// without work, took 8 us to drain. The first parts' sums are on their way
+// before their factors are known.
 constexpr int kJoinThreads = 256;
+constexpr int kJoinBlocks = 4;  // on an SM
 
-__global__ void __launch_bounds__(kJoinThreads)
+template <int ND>
+__global__ void __launch_bounds__(kJoinThreads, kJoinBlocks)
 sparse_mla_paged_join_kernel(const __grid_constant__ MlaPagedArgs a) {
     __shared__ float w_s[4][kMaxGrid];
     __shared__ float inv_s[4];
@@ -782,75 +804,72 @@ sparse_mla_paged_join_kernel(const __grid_constant__ MlaPagedArgs a) {
     grid_dependency_wait();
     launch_dependents();
     const Join jn = ws.join[blockIdx.x];
-    if (jn.t < 0) return;
-    const int quad = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (jn.first >= jn.last) return;  // one CTA had the whole token
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int32_t parts = jn.last - jn.first + 1;
     // slot of part i: the first CTA's second slot, then the others' first ones
     auto slot = [&](int32_t i) { return 2 * (jn.first + i) + (i == 0 ? 1 : 0); };
-    constexpr int kB = 6;
-    float4 v[kB][2];
-    auto fetch = [&](int32_t i0) {
+    constexpr int kB = 8 / ND;
+    constexpr int kDims = ND * kJoinThreads, kSlices = 512 / kDims;
+#pragma unroll 1
+    for (int32_t item = blockIdx.y; item < ws.quads * kSlices; item += gridDim.y) {
+        const int32_t quad = item / kSlices, dim = (item % kSlices) * kDims + tid;
+        float4 v[kB][ND];
+        auto fetch = [&](int32_t i0) {
 #pragma unroll
-        for (int i = 0; i < kB; ++i)
-            if (i0 + i < parts) {
-                v[i][0] = *ws.sums(slot(i0 + i), quad, tid);
-                v[i][1] = *ws.sums(slot(i0 + i), quad, tid + 256);
+            for (int i = 0; i < kB; ++i)
+#pragma unroll
+                for (int y = 0; y < ND; ++y)
+                    if (i0 + i < parts) v[i][y] = *ws.sums(slot(i0 + i), quad, dim + y * kJoinThreads);
+        };
+        fetch(0);
+        const int h = 4 * quad + warp;
+        if (warp < 4) {  // one warp a head: the parts' factors
+            const float sk = a.sinks && h < a.H ? __ldg(a.sinks + h) * kLog2e : -INFINITY;
+            float M = sk, z = 0.0f;
+            for (int32_t p = lane; p < parts; p += 32) M = fmaxf(M, ws.m[slot(p) * 64 + h]);
+            M = warp_max(M);
+            for (int32_t p = lane; p < parts; p += 32) {
+                const float m = ws.m[slot(p) * 64 + h];
+                const float f = m == -INFINITY ? 0.0f : tc::ex2_approx(m - M);
+                w_s[warp][p] = f;
+                z = fmaf(ws.l[slot(p) * 64 + h], f, z);
             }
-    };
-    fetch(0);
-    const int h = 4 * quad + warp;
-    if (warp < 4 && h < a.H) {  // one warp a head: the parts' factors
-        const float sk = a.sinks ? __ldg(a.sinks + h) * kLog2e : -INFINITY;
-        float m[(kMaxGrid + 31) / 32], l[(kMaxGrid + 31) / 32], M = sk;
-#pragma unroll
-        for (int i = 0; i < (kMaxGrid + 31) / 32; ++i) {
-            const int32_t p = 32 * i + lane;
-            m[i] = p < parts ? ws.m[slot(p) * 64 + h] : -INFINITY;
-            l[i] = p < parts ? ws.l[slot(p) * 64 + h] : 0.0f;
+            z = warp_sum(z) + (sk == -INFINITY ? 0.0f : tc::ex2_approx(sk - M));
+            if (lane == 0) {
+                inv_s[warp] = z > 0.0f ? 1.0f / z : 0.0f;
+                if (a.lse && h < a.H && dim < kDims)
+                    a.lse[(int64_t)jn.t * a.H + h] = (M + tc::lg2_approx(z)) * kLn2;
+            }
         }
+        __syncthreads();
+        float o[ND][4] = {};
+#pragma unroll 1
+        for (int32_t i0 = 0; i0 < parts; i0 += kB) {
+            if (i0 > 0) fetch(i0);
 #pragma unroll
-        for (int i = 0; i < (kMaxGrid + 31) / 32; ++i) M = fmaxf(M, m[i]);
-        M = warp_max(M);
-        float z = 0.0f;
+            for (int i = 0; i < kB; ++i)
+                if (i0 + i < parts) {
+                    const float f[4] = {w_s[0][i0 + i], w_s[1][i0 + i], w_s[2][i0 + i], w_s[3][i0 + i]};
 #pragma unroll
-        for (int i = 0; i < (kMaxGrid + 31) / 32; ++i) {
-            const float f = m[i] == -INFINITY ? 0.0f : tc::ex2_approx(m[i] - M);
-            if (32 * i + lane < parts) w_s[warp][32 * i + lane] = f;
-            z = fmaf(l[i], f, z);
-        }
-        z = warp_sum(z) + (sk == -INFINITY ? 0.0f : tc::ex2_approx(sk - M));
-        if (lane == 0) {
-            inv_s[warp] = z > 0.0f ? 1.0f / z : 0.0f;
-            if (a.lse) a.lse[(int64_t)jn.t * a.H + h] = (M + tc::lg2_approx(z)) * kLn2;
-        }
-    } else if (warp < 4) {
-        for (int32_t p = lane; p < parts; p += 32) w_s[warp][p] = 0.0f;
-        if (lane == 0) inv_s[warp] = 0.0f;
-    }
-    __syncthreads();
-    float o[2][4] = {};
-    for (int32_t i0 = 0; i0 < parts; i0 += kB) {
-        if (i0 > 0) fetch(i0);
-#pragma unroll
-        for (int i = 0; i < kB; ++i)
-            if (i0 + i < parts) {
-                const float f[4] = {w_s[0][i0 + i], w_s[1][i0 + i], w_s[2][i0 + i], w_s[3][i0 + i]};
-#pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    o[y][0] = fmaf(v[i][y].x, f[0], o[y][0]);
-                    o[y][1] = fmaf(v[i][y].y, f[1], o[y][1]);
-                    o[y][2] = fmaf(v[i][y].z, f[2], o[y][2]);
-                    o[y][3] = fmaf(v[i][y].w, f[3], o[y][3]);
+                    for (int y = 0; y < ND; ++y) {
+                        o[y][0] = fmaf(v[i][y].x, f[0], o[y][0]);
+                        o[y][1] = fmaf(v[i][y].y, f[1], o[y][1]);
+                        o[y][2] = fmaf(v[i][y].z, f[2], o[y][2]);
+                        o[y][3] = fmaf(v[i][y].w, f[3], o[y][3]);
+                    }
                 }
-            }
-    }
-#pragma unroll
-    for (int x = 0; x < 4; ++x)
-        if (4 * quad + x < a.H) {
-            __nv_bfloat16 *out = a.out + ((int64_t)jn.t * a.H + 4 * quad + x) * 512 + tid;
-            out[0] = __float2bfloat16_rn(o[0][x] * inv_s[x]);
-            out[256] = __float2bfloat16_rn(o[1][x] * inv_s[x]);
         }
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+            if (4 * quad + x < a.H) {
+                __nv_bfloat16 *out = a.out + ((int64_t)jn.t * a.H + 4 * quad + x) * 512 + dim;
+                const float r = inv_s[x];
+#pragma unroll
+                for (int y = 0; y < ND; ++y) out[y * kJoinThreads] = __float2bfloat16_rn(o[y][x] * r);
+            }
+        __syncthreads();  // w_s and inv_s are read
+    }
 }
 
 }  // namespace
@@ -874,12 +893,14 @@ cudaError_t launch_sparse_mla_paged(MlaPagedArgs a, cudaStream_t stream) {
         if (e != cudaSuccess) return e;
         entered_context(pc, dev, ctx);
     }
-    CUtensorMap q_map;
-    if (!encode_bf16_3d(&q_map, a.q, 512, a.H, a.T, 64, a.H, 1)) return cudaErrorInvalidValue;
     const int grid = min(sms, kMaxGrid);
-    e = launch_early(sparse_mla_paged_kernel, dim3(grid), dim3(kThreads), kSmemBytes, stream, q_map, a);
+    e = launch_early(sparse_mla_paged_kernel, dim3(grid), dim3(kThreads), kSmemBytes, stream, a);
     if (e != cudaSuccess) return e;
-    return launch_early(sparse_mla_paged_join_kernel, dim3(grid, (a.H + 3) / 4),
+    // a block for each four heads and half of the dims while they fit at once
+    const int quads = (a.H + 3) / 4, gx = min(a.T, grid), most = kJoinBlocks * sms;
+    if (2 * quads * gx <= most)
+        return launch_early(sparse_mla_paged_join_kernel<1>, dim3(gx, 2 * quads), dim3(kJoinThreads), 0, stream, a);
+    return launch_early(sparse_mla_paged_join_kernel<2>, dim3(gx, max(1, min(quads, most / gx))),
                         dim3(kJoinThreads), 0, stream, a);
 }
 
