@@ -71,18 +71,18 @@ struct Join {
 // Join entries: one a token while there are no more tokens than CTAs, else one
 // a CTA, of the token that starts in it and goes on in others.
 
-// Workspace: Join [kMaxGrid], then m and l [2 kMaxGrid][64], then the sums
+// Workspace: Join [kMaxGrid], then (m, l) [2 kMaxGrid][64], then the sums
 // [2 kMaxGrid][ceil(H / 4)][512][4 heads]: a thread of the epilogue holds one
 // dim of 32 heads, so a warp writes 512 bytes at once.
 struct Space {
     Join *join;
-    float *m, *l, *o;
+    float2 *ml;
+    float *o;
     int32_t quads;
     __host__ __device__ Space(void *p, int32_t H) {
         join = static_cast<Join *>(p);
-        m = reinterpret_cast<float *>(join + kMaxGrid);
-        l = m + 2 * kMaxGrid * 64;
-        o = l + 2 * kMaxGrid * 64;
+        ml = reinterpret_cast<float2 *>(join + kMaxGrid);
+        o = reinterpret_cast<float *>(ml + 2 * kMaxGrid * 64);
         quads = (H + 3) / 4;
     }
     // four heads of one dim
@@ -728,8 +728,7 @@ sparse_mla_paged_kernel(const __grid_constant__ MlaPagedArgs a) {
                         if (a.lse && h < a.H)
                             a.lse[(int64_t)tt * a.H + h] = (M + tc::lg2_approx(Z)) * kLn2;
                     } else {  // all 64: the join reads them by fours
-                        ws.m[slot * 64 + h] = m;
-                        ws.l[slot * 64 + h] = l;
+                        ws.ml[slot * 64 + h] = make_float2(m, l);
                     }
                     ms->fac[h] = f;
                 }
@@ -787,70 +786,77 @@ sparse_mla_paged_kernel(const __grid_constant__ MlaPagedArgs a) {
 
 // Joins the tokens that several CTAs worked on. Block (x, y) takes token x
 // (with more tokens than CTAs: the split token whose first tile CTA x held)
-// and its heads by fours, y, y + gridDim.y and so on; ND dims a thread. Few
-// blocks, about four an SM: they start only as the first kernel's CTAs leave
-// (its registers fill the SM), and a grid of 32 blocks for each CTA, most
-// without work, took 8 us to drain. The first parts' sums are on their way
-// before their factors are known.
+// and its items y, y + gridDim.y and so on: four heads and 256 ND / P dims, ND
+// dims a thread, P groups of threads sharing the parts (ND = 1). Few blocks,
+// four an SM: they start only as the first kernel's CTAs leave (its registers
+// fill the SM), and a grid of 32 blocks for each CTA, most without work, took
+// 8 us to drain. The first parts' sums are on their way before their factors
+// are known.
 constexpr int kJoinThreads = 256;
 constexpr int kJoinBlocks = 4;  // on an SM
 
 template <int ND>
 __global__ void __launch_bounds__(kJoinThreads, kJoinBlocks)
-sparse_mla_paged_join_kernel(const __grid_constant__ MlaPagedArgs a) {
+sparse_mla_paged_join_kernel(const __grid_constant__ MlaPagedArgs a, int32_t P) {
     __shared__ float w_s[4][kMaxGrid];
     __shared__ float inv_s[4];
+    __shared__ float4 group_s[kJoinThreads];
     const Space ws(a.workspace, a.H);
     grid_dependency_wait();
     launch_dependents();
     const Join jn = ws.join[blockIdx.x];
     if (jn.first >= jn.last) return;  // one CTA had the whole token
+    if (ND > 1) P = 1;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int32_t parts = jn.last - jn.first + 1;
+    const int32_t width = kJoinThreads / P, group = tid / width, dims = ND * width, slices = 512 / dims;
     // slot of part i: the first CTA's second slot, then the others' first ones
     auto slot = [&](int32_t i) { return 2 * (jn.first + i) + (i == 0 ? 1 : 0); };
     constexpr int kB = 8 / ND;
-    constexpr int kDims = ND * kJoinThreads, kSlices = 512 / kDims;
 #pragma unroll 1
-    for (int32_t item = blockIdx.y; item < ws.quads * kSlices; item += gridDim.y) {
-        const int32_t quad = item / kSlices, dim = (item % kSlices) * kDims + tid;
+    for (int32_t item = blockIdx.y; item < ws.quads * slices; item += gridDim.y) {
+        const int32_t quad = item / slices, dim = (item % slices) * dims + (tid - group * width);
         float4 v[kB][ND];
         auto fetch = [&](int32_t i0) {
 #pragma unroll
             for (int i = 0; i < kB; ++i)
 #pragma unroll
                 for (int y = 0; y < ND; ++y)
-                    if (i0 + i < parts) v[i][y] = *ws.sums(slot(i0 + i), quad, dim + y * kJoinThreads);
+                    if (i0 + P * i < parts) v[i][y] = *ws.sums(slot(i0 + P * i), quad, dim + y * kJoinThreads);
         };
-        fetch(0);
+        fetch(group);
         const int h = 4 * quad + warp;
         if (warp < 4) {  // one warp a head: the parts' factors
             const float sk = a.sinks && h < a.H ? __ldg(a.sinks + h) * kLog2e : -INFINITY;
-            float M = sk, z = 0.0f;
-            for (int32_t p = lane; p < parts; p += 32) M = fmaxf(M, ws.m[slot(p) * 64 + h]);
+            // a lane keeps its first part's pair; with more than 32 parts it reads the others twice
+            const float2 first = lane < parts ? ws.ml[slot(lane) * 64 + h] : make_float2(-INFINITY, 0.0f);
+            float M = fmaxf(sk, first.x);
+            for (int32_t p = lane + 32; p < parts; p += 32) M = fmaxf(M, ws.ml[slot(p) * 64 + h].x);
             M = warp_max(M);
+            float z = 0.0f;
             for (int32_t p = lane; p < parts; p += 32) {
-                const float m = ws.m[slot(p) * 64 + h];
-                const float f = m == -INFINITY ? 0.0f : tc::ex2_approx(m - M);
+                const float2 ml = p == lane ? first : ws.ml[slot(p) * 64 + h];
+                const float f = ml.x == -INFINITY ? 0.0f : tc::ex2_approx(ml.x - M);
                 w_s[warp][p] = f;
-                z = fmaf(ws.l[slot(p) * 64 + h], f, z);
+                z = fmaf(ml.y, f, z);
             }
             z = warp_sum(z) + (sk == -INFINITY ? 0.0f : tc::ex2_approx(sk - M));
             if (lane == 0) {
                 inv_s[warp] = z > 0.0f ? 1.0f / z : 0.0f;
-                if (a.lse && h < a.H && dim < kDims)
+                if (a.lse && h < a.H && item % slices == 0)
                     a.lse[(int64_t)jn.t * a.H + h] = (M + tc::lg2_approx(z)) * kLn2;
             }
         }
         __syncthreads();
         float o[ND][4] = {};
 #pragma unroll 1
-        for (int32_t i0 = 0; i0 < parts; i0 += kB) {
-            if (i0 > 0) fetch(i0);
+        for (int32_t i0 = group; i0 < parts; i0 += P * kB) {
+            if (i0 != group) fetch(i0);
 #pragma unroll
-            for (int i = 0; i < kB; ++i)
-                if (i0 + i < parts) {
-                    const float f[4] = {w_s[0][i0 + i], w_s[1][i0 + i], w_s[2][i0 + i], w_s[3][i0 + i]};
+            for (int i = 0; i < kB; ++i) {
+                const int32_t p = i0 + P * i;
+                if (p < parts) {
+                    const float f[4] = {w_s[0][p], w_s[1][p], w_s[2][p], w_s[3][p]};
 #pragma unroll
                     for (int y = 0; y < ND; ++y) {
                         o[y][0] = fmaf(v[i][y].x, f[0], o[y][0]);
@@ -859,16 +865,29 @@ sparse_mla_paged_join_kernel(const __grid_constant__ MlaPagedArgs a) {
                         o[y][3] = fmaf(v[i][y].w, f[3], o[y][3]);
                     }
                 }
-        }
-#pragma unroll
-        for (int x = 0; x < 4; ++x)
-            if (4 * quad + x < a.H) {
-                __nv_bfloat16 *out = a.out + ((int64_t)jn.t * a.H + 4 * quad + x) * 512 + dim;
-                const float r = inv_s[x];
-#pragma unroll
-                for (int y = 0; y < ND; ++y) out[y * kJoinThreads] = __float2bfloat16_rn(o[y][x] * r);
             }
-        __syncthreads();  // w_s and inv_s are read
+        }
+        if (ND == 1 && P > 1) {
+            group_s[tid] = make_float4(o[0][0], o[0][1], o[0][2], o[0][3]);
+            __syncthreads();
+            for (int q = 1; q < P && group == 0; ++q) {
+                const float4 x = group_s[tid + q * width];
+                o[0][0] += x.x;
+                o[0][1] += x.y;
+                o[0][2] += x.z;
+                o[0][3] += x.w;
+            }
+        }
+        if (group == 0)
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+                if (4 * quad + x < a.H) {
+                    __nv_bfloat16 *out = a.out + ((int64_t)jn.t * a.H + 4 * quad + x) * 512 + dim;
+                    const float r = inv_s[x];
+#pragma unroll
+                    for (int y = 0; y < ND; ++y) out[y * kJoinThreads] = __float2bfloat16_rn(o[y][x] * r);
+                }
+        __syncthreads();  // w_s, inv_s and group_s are read
     }
 }
 
@@ -896,12 +915,15 @@ cudaError_t launch_sparse_mla_paged(MlaPagedArgs a, cudaStream_t stream) {
     const int grid = min(sms, kMaxGrid);
     e = launch_early(sparse_mla_paged_kernel, dim3(grid), dim3(kThreads), kSmemBytes, stream, a);
     if (e != cudaSuccess) return e;
-    // a block for each four heads and half of the dims while they fit at once
+    // Small items while they fit at once: first the parts by four groups of
+    // threads, then by two, then none, then two dims a thread.
     const int quads = (a.H + 3) / 4, gx = min(a.T, grid), most = kJoinBlocks * sms;
-    if (2 * quads * gx <= most)
-        return launch_early(sparse_mla_paged_join_kernel<1>, dim3(gx, 2 * quads), dim3(kJoinThreads), 0, stream, a);
+    for (int P = 4; P > 0; P >>= 1)
+        if (2 * quads * gx * P <= most)
+            return launch_early(sparse_mla_paged_join_kernel<1>, dim3(gx, 2 * quads * P), dim3(kJoinThreads), 0,
+                                stream, a, (int32_t)P);
     return launch_early(sparse_mla_paged_join_kernel<2>, dim3(gx, max(1, min(quads, most / gx))),
-                        dim3(kJoinThreads), 0, stream, a);
+                        dim3(kJoinThreads), 0, stream, a, 1);
 }
 
 }  // namespace csa
