@@ -482,10 +482,13 @@ def _rows(t, name, ndim):
 
 
 def _match(dev, *specs):
-    """Each (tensor or None, name, dtype, shape): on device `dev`, contiguous,
-    of that dtype and shape."""
+    """Each (tensor or None, name, dtype, shape): on device `dev` (a CUDA one),
+    contiguous, of that dtype and shape."""
     for t, name, dtype, shape in specs:
         if t is None:
+            continue
+        if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev
+                and t.shape == shape and t.is_contiguous() and dev >= 0):
             continue
         if not isinstance(t, torch.Tensor) or not t.is_cuda:
             raise TypeError(f"{name} must be a CUDA tensor")
@@ -495,8 +498,22 @@ def _match(dev, *specs):
             raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
-        if t.get_device() != dev:
-            raise ValueError(f"{name} is on cuda:{t.get_device()}, the call on cuda:{dev}")
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, the call on cuda:{dev}")
+
+
+def _scratch(workspace, dev, size, *args):
+    """A call's workspace and its bytes: the caller's (its size is checked by
+    the call), or a new one of `size(*args)` bytes."""
+    if workspace is None:
+        need = size(*args)
+        if need == 0:
+            return None, 0
+        workspace = torch.empty(need, dtype=torch.uint8, device=f"cuda:{dev}")
+    elif not isinstance(workspace, torch.Tensor) or workspace.get_device() != dev:
+        raise ValueError(f"workspace must be a tensor on cuda:{dev}")
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace, workspace.numel() * workspace.element_size()
 
 
 def _addr(t):
@@ -636,11 +653,8 @@ def csa_indexer_topk_paged(q, k_cache, w, pages, q_seq, q_pos, cmp_ratio: int, t
            (q_seq, "q_seq", torch.int32, (T,)), (q_pos, "q_pos", torch.int32, (T,)),
            (out, "out", torch.int32, (T, max(topk, 0))),
            (out_val, "out_val", torch.float32, (T, max(topk, 0))))
-    need = csa_indexer_topk_paged_workspace_size(T, max_pages * page, Hi, Di, topk) \
-        if max_pages * page < 2 ** 31 else 0
-    workspace, ws_bytes = _workspace(need, q.device, workspace)
-    if workspace is not None and workspace.get_device() != dev:
-        raise ValueError(f"workspace is on {workspace.device}, the call on cuda:{dev}")
+    workspace, ws_bytes = _scratch(workspace, dev, csa_indexer_topk_paged_workspace_size, T,
+                                   min(max_pages * page, 2 ** 31 - 1), Hi, Di, topk)
     _launch(dev, "csa_indexer_topk_paged", stream, q.data_ptr(), k_cache.data_ptr(), _addr(w),
             pages.data_ptr(), _addr(q_seq), _addr(q_pos), batch, T, Hi, Di, n_pages, page, max_pages,
             cmp_ratio, topk, out.data_ptr(), _addr(out_val), _addr(workspace), ws_bytes)
@@ -690,10 +704,7 @@ def csa_sparse_mla_paged(q, ori_cache, cmp_cache, cmp_sparse_indices, ori_pages,
            (q_seq, "q_seq", torch.int32, (T,)), (q_pos, "q_pos", torch.int32, (T,)),
            (sinks, "sinks", torch.float32, (H,)), (out, "out", torch.bfloat16, (T, H, D)),
            (lse, "lse", torch.float32, (T, H)))
-    workspace, ws_bytes = _workspace(lib().csa_sparse_mla_paged_workspace_size(T, H), q.device,
-                                     workspace)
-    if workspace is not None and workspace.get_device() != dev:
-        raise ValueError(f"workspace is on {workspace.device}, the call on cuda:{dev}")
+    workspace, ws_bytes = _scratch(workspace, dev, csa_sparse_mla_paged_workspace_size, T, H)
     _launch(dev, "csa_sparse_mla_paged", stream, q.data_ptr(), ori_cache.data_ptr(),
             _addr(cmp_cache), _addr(cmp_sparse_indices), ori_pages.data_ptr(), _addr(cmp_pages),
             _addr(q_seq), _addr(q_pos), batch, T, H, D, ori_n, ori_page, ori_max, cmp_n, cmp_page,
