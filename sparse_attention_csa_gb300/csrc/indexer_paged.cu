@@ -806,13 +806,12 @@ cudaError_t launch_indexer_topk_paged(IndexerPagedArgs a, cudaStream_t stream) {
                                        Score<64>::kSmem, stream, a);
         if (e != cudaSuccess) return e;
     }
-    // CTAs a token: enough to hold the longest row the table allows in their
-    // registers, more while the GPU has room (two CTAs fit an SM) and each
-    // keeps 2048 rows.
+    // CTAs a token: as few as hold the longest row the table allows in their
+    // registers (a cluster's barriers and words cost more than its CTAs save:
+    // one token of 32768 rows 16.6 us with four, 18.4 with eight; 64 tokens of
+    // up to 16384 rows 44 us with two, 47 with four).
     int C = 1;
-    while (C < kMaxCluster && ((int64_t)C * kSelRows < a.max_rows ||
-                               ((int64_t)a.T * 2 * C <= 2 * sms && (int64_t)C * 4096 <= a.max_rows)))
-        C *= 2;
+    while (C < kMaxCluster && (int64_t)C * kSelRows < a.max_rows) C *= 2;
     const bool held = (int64_t)C * kSelRows >= a.max_rows;
     switch (C) {
         case 1: return launch_select<1>(a, held, scored, stream);
