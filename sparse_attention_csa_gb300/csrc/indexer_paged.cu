@@ -492,17 +492,18 @@ indexer_paged_select_kernel(const __grid_constant__ IndexerPagedArgs a, int32_t 
         return;
     }
     // This CTA's rows [r0, r1), a multiple of 128 apart: chunks of kSelRows, in
-    // which warp w holds 128 kQuads rows, 128 at a time.
+    // which a thread holds 4 kQuads consecutive rows (so that one scan over the
+    // threads gives every row its place in the output).
     const int32_t share = (int32_t)((((int64_t)n + C - 1) / C + 127) / 128 * 128);
     const int32_t r0 = (int32_t)min((int64_t)rank * share, (int64_t)n);
     const int32_t r1 = (int32_t)min((int64_t)r0 + share, (int64_t)n);
     float4 held[kQuads];
-    auto row_at = [&](int32_t c0, int i) { return c0 + 128 * (kQuads * warp + i) + 4 * lane; };
+    auto row_at = [&](int32_t c0, int i) { return c0 + 4 * (kQuads * tid + i); };
     auto fetch = [&](int32_t c0) {
 #pragma unroll
         for (int i = 0; i < kQuads; ++i) {  // row_pad is a multiple of 64: whole float4 are in bounds
             const int32_t r = row_at(c0, i);
-            held[i] = r < r1 ? __ldcg(reinterpret_cast<const float4 *>(sc + r))
+            held[i] = r < r1 ? *reinterpret_cast<const float4 *>(sc + r)
                              : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         }
     };
@@ -586,9 +587,9 @@ indexer_paged_select_kernel(const __grid_constant__ IndexerPagedArgs a, int32_t 
     const uint32_t bin = sm.pick[0];
     int32_t left = K - (int32_t)sm.pick[1];  // to take of the bin's rows
     const int32_t n_bin = (int32_t)sm.pick[2];
-    // rows of the bin: those with (key & mask) above prefix are taken, those
-    // equal to it in row order while `left` lasts
-    uint32_t mask = 0u, prefix = 0u;
+    // the K-th largest key: rows with a larger one are taken, those with an
+    // equal one in row order while `left` lasts
+    uint32_t kth = 0u;
     // rows above the threshold and on it in the CTAs before this one
     uint32_t gt_before = 0, eq_before = 0;
     if (n_bin <= kCand) {
@@ -616,66 +617,62 @@ indexer_paged_select_kernel(const __grid_constant__ IndexerPagedArgs a, int32_t 
             asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // done with the peers
         }
         __syncthreads();
-        if (left < n_bin) {
-            if (tid < n_bin) {
-                const uint32_t mine = sm.all[tid];
-                int32_t gt = 0, eq = 0;
-                for (int32_t i = 0; i < n_bin; ++i) {
-                    gt += sm.all[i] > mine;
-                    eq += sm.all[i] == mine;
-                }
-                if (gt < left && left <= gt + eq) {  // all that pass hold the same key
-                    sm.pick[0] = mine;
-                    sm.pick[1] = gt;
-                }
+        if (tid < n_bin) {
+            const uint32_t mine = sm.all[tid];
+            int32_t gt = 0, eq = 0;
+            for (int32_t i = 0; i < n_bin; ++i) {
+                gt += sm.all[i] > mine;
+                eq += sm.all[i] == mine;
             }
-            __syncthreads();
-            mask = 0xffffffffu;
-            prefix = sm.pick[0];
-            left -= (int32_t)sm.pick[1];
+            if (gt < left && left <= gt + eq) {  // all that pass hold the same key
+                sm.pick[0] = mine;
+                sm.pick[1] = gt;
+            }
         }
+        __syncthreads();
+        kth = sm.pick[0];
+        left -= (int32_t)sm.pick[1];
         if (C > 1) {
             const bool in = (uint32_t)tid < start;
-            const uint32_t k = in ? sm.all[tid] & mask : 0u;
-            gt_before += __syncthreads_count(in && k > prefix);
-            eq_before = __syncthreads_count(in && k == prefix);
+            const uint32_t k = in ? sm.all[tid] : 0u;
+            gt_before += __syncthreads_count(in && k > kth);
+            eq_before = __syncthreads_count(in && k == kth);
         }
     } else {
-        if (left < n_bin) {
+        uint32_t mask = 0u;  // bits of kth that are known
 #pragma unroll 1
-            for (int pass = 0; pass < 4; ++pass) {
-                const int shift = 24 - 8 * pass;
-                uint32_t *h = sm.digit[pass & 1];
-                sweep([&](float s) {
-                    const uint32_t k = float_key(s);
-                    if (bin_of(s) == bin && (k & mask) == prefix) atomicAdd(&h[(k >> shift) & 255u], 1u);
-                });
-                if (tid < 256) sm.digit[(pass + 1) & 1][tid] = 0;  // read two passes ago
-                sync();
-                int32_t cnt = 0;
-                if (tid < 256)
+        for (int pass = 0; pass < 4; ++pass) {
+            const int shift = 24 - 8 * pass;
+            uint32_t *h = sm.digit[pass & 1];
+            sweep([&](float s) {
+                const uint32_t k = float_key(s);
+                if (bin_of(s) == bin && (k & mask) == kth) atomicAdd(&h[(k >> shift) & 255u], 1u);
+            });
+            if (tid < 256) sm.digit[(pass + 1) & 1][tid] = 0;  // read two passes ago
+            sync();
+            int32_t cnt = 0;
+            if (tid < 256)
 #pragma unroll
-                    for (int r = 0; r < C; ++r)
-                        cnt += (int32_t)(C > 1 ? peer_u32(&h[255 - tid], r) : h[255 - tid]);
-                int32_t total;
-                const int32_t above = block_exclusive_scan<kSelThreads>(cnt, sm.scan, &total);
-                if (tid < 256 && above < left && left <= above + cnt) {
-                    sm.pick[0] = 255 - tid;
-                    sm.pick[1] = above;
-                }
-                sync();  // the peers have read this pass's counts
-                prefix |= sm.pick[0] << shift;
-                mask |= 255u << shift;
-                left -= (int32_t)sm.pick[1];
-                __syncthreads();
+                for (int r = 0; r < C; ++r)
+                    cnt += (int32_t)(C > 1 ? peer_u32(&h[255 - tid], r) : h[255 - tid]);
+            int32_t total;
+            const int32_t above = block_exclusive_scan<kSelThreads>(cnt, sm.scan, &total);
+            if (tid < 256 && above < left && left <= above + cnt) {
+                sm.pick[0] = 255 - tid;
+                sm.pick[1] = above;
             }
+            sync();  // the peers have read this pass's counts
+            kth |= sm.pick[0] << shift;
+            mask |= 255u << shift;
+            left -= (int32_t)sm.pick[1];
+            __syncthreads();
         }
         if (C > 1) {
             uint32_t n_gt = 0, n_eq = 0;
             sweep([&](float s) {
-                const uint32_t b = bin_of(s), k = float_key(s) & mask;
-                n_gt += b > bin || (b == bin && k > prefix);
-                n_eq += b == bin && k == prefix;
+                const uint32_t k = float_key(s);
+                n_gt += k > kth;
+                n_eq += k == kth;
             });
             n_gt = __reduce_add_sync(0xffffffffu, n_gt);
             n_eq = __reduce_add_sync(0xffffffffu, n_eq);
@@ -690,67 +687,50 @@ indexer_paged_select_kernel(const __grid_constant__ IndexerPagedArgs a, int32_t 
             asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // done with the peers
         }
     }
-    // ---- emission in row order: 1 for a row above the threshold, 65536 for
-    // one on it
-    auto kind = [&](float s) -> uint32_t {
-        const uint32_t b = bin_of(s), k = float_key(s) & mask;
-        return b > bin || (b == bin && k > prefix) ? 1u : b == bin && k == prefix ? 65536u : 0u;
-    };
+    // ---- emission in row order
     for (int32_t c0 = r0; c0 < r1; c0 += kSelRows) {
         if (!kHeld) fetch(c0);
-        uint32_t quad[kQuads], sum = 0;  // this thread's counts
+        uint32_t up = 0, on = 0;  // this thread's rows above the K-th key and on it
 #pragma unroll
         for (int i = 0; i < kQuads; ++i) {
             const int32_t r = row_at(c0, i);
             const float v[4] = {held[i].x, held[i].y, held[i].z, held[i].w};
-            quad[i] = 0;
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (r + e < r1) quad[i] += kind(v[e]);
-            sum += quad[i];
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t k = float_key(v[e]), bit = 1u << (4 * i + e);
+                if (r + e < r1 && k > kth) up |= bit;
+                if (r + e < r1 && k == kth) on |= bit;
+            }
         }
-        // a warp's counts stay below 2^16 each (128 kQuads rows)
-        const uint32_t in_warp = __reduce_add_sync(0xffffffffu, sum);
+        // packed counts: a chunk's rows stay below 2^16
+        static_assert(kSelThreads / 32 <= 32 && kSelRows < 65536, "packed counts");
+        const uint32_t mine = (uint32_t)__popc(up) | ((uint32_t)__popc(on) << 16);
+        uint32_t x = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
         __syncthreads();
-        if (lane == 0) sm.warps[warp] = in_warp;
+        if (lane == 31) sm.warps[warp] = x;
         __syncthreads();
-        static_assert(kSelThreads / 32 <= 16 && kSelRows < 65536, "packed counts");
         const uint32_t others = lane < kSelThreads / 32 ? sm.warps[lane] : 0u;
-        const uint32_t before = __reduce_add_sync(0xffffffffu, lane < warp ? others : 0u);
+        const uint32_t before = __reduce_add_sync(0xffffffffu, lane < warp ? others : 0u) + x - mine;
         const uint32_t chunk = __reduce_add_sync(0xffffffffu, others);
-        uint32_t gt = gt_before + (before & 0xffffu), eq = eq_before + (before >> 16);
+        uint32_t g1 = gt_before + (before & 0xffffu), e1 = eq_before + (before >> 16);
         gt_before += chunk & 0xffffu;
         eq_before += chunk >> 16;
-        if (in_warp != 0) {
-#pragma unroll
-            for (int i = 0; i < kQuads; ++i) {
-                if (!__any_sync(0xffffffffu, quad[i] != 0)) continue;
-                uint32_t x = quad[i];
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
-                    if (lane >= o) x += y;
-                }
-                const uint32_t all = __shfl_sync(0xffffffffu, x, 31);
-                x -= quad[i];
-                uint32_t g1 = gt + (x & 0xffffu), e1 = eq + (x >> 16);
-                const int32_t r = row_at(c0, i);
-                const float v[4] = {held[i].x, held[i].y, held[i].z, held[i].w};
-                if (quad[i])
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const uint32_t k = r + e < r1 ? kind(v[e]) : 0u;
-                        if (k == 1u || (k && e1 < (uint32_t)left)) {
-                            const uint32_t at = g1 + min(e1, (uint32_t)left);
-                            idx[at] = r + e;
-                            if (val) val[at] = v[e];
-                        }
-                        g1 += k & 1u;
-                        e1 += k >> 16;
-                    }
-                gt += all & 0xffffu;
-                eq += all >> 16;
+        for (uint32_t todo = up | on; todo; todo &= todo - 1) {
+            const int i = __ffs(todo) - 1;
+            const bool above = (up >> i) & 1u;
+            if (above || e1 < (uint32_t)left) {
+                const uint32_t at = g1 + min(e1, (uint32_t)left);
+                const int32_t r = row_at(c0, 0) + i;
+                idx[at] = r;
+                if (val) val[at] = sc[r];
             }
+            g1 += above;
+            e1 += !above;
         }
     }
     if (C > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // peers are done with sm
