@@ -1,4 +1,5 @@
-"""One CSA / HCA attention layer forward, chaining the four C-ABI calls.
+"""One CSA / HCA attention layer: its forward over packed sequences, chaining
+the four C-ABI calls, and its step for new tokens over paged caches.
 
 Order of the path (miles PR 2038 report, the attention forward excerpt:
 compressed cu_seqlens, then the indexer, then sparse attention over the window
@@ -13,6 +14,10 @@ rows plus the selected compressed rows):
 
 Everything runs on the current CUDA stream (the window rows optionally on a
 side stream, joined before returning); nothing synchronises.
+
+``csa_layer_decode`` continues sequences whose rows are cached: the new rows go
+to their slots (rotated on the way), the indexer chooses compressed rows, the
+attention reads the paged caches.
 """
 
 from __future__ import annotations
@@ -21,8 +26,9 @@ from dataclasses import dataclass
 
 import torch
 
-from . import (csa_compress_cu_seqlens, csa_indexer_topk, csa_indexer_topk_workspace_size,
-               csa_sparse_mla_fwd, csa_window_idx)
+from . import (csa_cache_append, csa_compress_cu_seqlens, csa_indexer_topk,
+               csa_indexer_topk_paged, csa_indexer_topk_workspace_size, csa_rope,
+               csa_sparse_mla_fwd, csa_sparse_mla_paged, csa_window_idx)
 
 
 @dataclass
@@ -88,3 +94,57 @@ def csa_layer_forward(q, ori_kv, cmp_kv, cu_seqlens, sinks, softmax_scale: float
     if win_done is not None:
         main.wait_event(win_done)
     return outputs
+
+
+@dataclass
+class PagedLayerCache:
+    """One layer's paged caches. Original and compressed rows have tables of
+    their own; the indexer's rows share the compressed rows' table."""
+    ori: torch.Tensor                    # [pages, page_size, 512] bf16
+    ori_pages: torch.Tensor              # [batch, max_pages] int32
+    cmp: torch.Tensor | None = None      # [pages, page_size, 512] bf16
+    cmp_pages: torch.Tensor | None = None
+    k_idx: torch.Tensor | None = None    # [pages, page_size, Di] bf16 (INDEXER layers)
+
+
+@dataclass
+class DecodeOutputs:
+    out: torch.Tensor                 # [T, H, 512] bf16
+    lse: torch.Tensor | None          # [T, H] fp32
+    topk_idx: torch.Tensor | None     # [T, topk] int32 rows of the sequence (INDEXER layers)
+
+
+def csa_layer_decode(q, kv, cache: PagedLayerCache, q_seq, q_pos, sinks, softmax_scale: float,
+                     cmp_ratio: int, ori_win_left: int, inv_freq=None, rope_layout="interleaved",
+                     turn_back: bool = False, q_idx=None, w=None, topk: int = 0,
+                     return_softmax_lse: bool = False, indexer_workspace=None,
+                     attention_workspace=None) -> DecodeOutputs:
+    """New tokens of one layer: q [T, H, 512] and their rows kv [T, 512] at
+    positions ``q_pos`` [T] (negative: padding) of sequences ``q_seq`` [T]
+    (None: token t is sequence t's).
+
+    ``kv`` is appended to ``cache.ori`` (None: the rows are there already).
+    With ``inv_freq`` the last ``2 * inv_freq.numel()`` dims of q and kv are
+    rotated at their positions first (q into a new tensor), and with
+    ``turn_back`` those of the output are turned back at the token's own
+    position. ``q_idx``/``w``/``topk`` given -> INDEXER layer; omitted ->
+    every visible compressed row, or none without ``cache.cmp``. Compressed
+    rows that these tokens complete are the caller's to append before the call
+    (``csa_cache_append`` with the group's number as position and
+    ``pos_stride=cmp_ratio``)."""
+    if kv is not None:
+        csa_cache_append(kv, q_seq, q_pos, cache.ori_pages, cache.ori, inv_freq=inv_freq,
+                         layout=rope_layout)
+    if inv_freq is not None:
+        q = csa_rope(q, q_pos, inv_freq, layout=rope_layout)
+    idx = None
+    if q_idx is not None:
+        idx, _ = csa_indexer_topk_paged(q_idx, cache.k_idx, w, cache.cmp_pages, q_seq, q_pos,
+                                        cmp_ratio, topk, workspace=indexer_workspace)
+    out, lse = csa_sparse_mla_paged(q, cache.ori, cache.cmp, idx, cache.ori_pages,
+                                    cache.cmp_pages, q_seq, q_pos, sinks, softmax_scale, cmp_ratio,
+                                    ori_win_left, return_softmax_lse=return_softmax_lse,
+                                    workspace=attention_workspace)
+    if inv_freq is not None and turn_back:
+        csa_rope(out, q_pos, inv_freq, layout=rope_layout, inverse=True, out=out)
+    return DecodeOutputs(out, lse, idx)
