@@ -575,9 +575,10 @@ csa_status_t csa_indexer_topk_paged(const csa_bf16_t *q, const csa_bf16_t *k_cac
  * sizes < 1, max_pages * page_size above INT32_MAX, topk < 1 with
  * cmp_sparse_indices, q_seq NULL with total_tokens > batch -> CSA_ERR_SHAPE;
  * head_dim != 512, heads > 64, ori_win_right != 0, cmp_ratio < 2 while
- * cmp_cache is used, q/ori_cache/cmp_cache/out not 16-byte aligned ->
- * CSA_ERR_UNSUPPORTED; a short or misaligned workspace -> CSA_ERR_WORKSPACE.
- * total_tokens == 0 launches nothing.
+ * cmp_cache is used, a window or a list of more than 2^27 rows (or a compressed
+ * table of more, without a list), q/ori_cache/cmp_cache/out not 16-byte
+ * aligned -> CSA_ERR_UNSUPPORTED; a short or misaligned workspace ->
+ * CSA_ERR_WORKSPACE. total_tokens == 0 launches nothing.
  */
 size_t csa_sparse_mla_paged_workspace_size(int32_t total_tokens, int32_t heads);
 

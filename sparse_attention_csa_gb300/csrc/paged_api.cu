@@ -20,6 +20,7 @@ bool known(csa_dtype_t d) { return d == CSA_BF16 || d == CSA_F32; }
 bool known(csa_rope_layout_t l) { return l == CSA_ROPE_INTERLEAVED || l == CSA_ROPE_HALF; }
 
 constexpr int32_t kMaxRopeDim = 1024;
+constexpr int32_t kMaxKeys = 1 << 27;  // of a token in either cache: tile counts of many tokens stay in 32 bits
 
 // Do [a, a + rows of `len` bytes every `sa`] and the same at b share a byte?
 // Rows of two column ranges of one wider matrix (equal strides) do not.
@@ -237,6 +238,9 @@ csa_status_t csa_sparse_mla_paged(
     }
     if (head_dim != 512 || heads > 64 || ori_win_right != 0) return CSA_ERR_UNSUPPORTED;
     if (use_cmp && cmp_ratio < 2) return CSA_ERR_UNSUPPORTED;
+    if (ori_win_left >= kMaxKeys ||
+        (use_cmp && (cmp_sparse_indices ? topk : cmp_max_pages * cmp_page_size) > kMaxKeys))
+        return CSA_ERR_UNSUPPORTED;
     if (misaligned(q, 16) || misaligned(ori_cache, 16) || misaligned(out, 16) ||
         (use_cmp && misaligned(cmp_cache, 16)))
         return CSA_ERR_UNSUPPORTED;
@@ -265,7 +269,7 @@ csa_status_t csa_sparse_mla_paged(
     a.batch = batch;
     a.topk = a.idx ? topk : 0;
     a.cmp_ratio = use_cmp ? cmp_ratio : 1;
-    a.window = ori_win_left < INT32_MAX ? ori_win_left + 1 : INT32_MAX;
+    a.window = ori_win_left + 1;
     a.softmax_scale = softmax_scale;
     a.wait_ns = csa::pipeline_wait_limit_ns();
     return from_cuda(csa::launch_sparse_mla_paged(a, (cudaStream_t)stream));

@@ -6,14 +6,16 @@
 //     l_i = scale q.kv_i ; Z = sum e^(l_i - m) + e^(sink - m)
 //     out = sum e^(l_i - m) kv_i / Z ; lse = m + ln Z
 //
-// Work split. A token's keys form tiles of 64 slots; the tiles of all tokens,
-// one after the other, are dealt to the CTAs in equal runs, so a long row is
-// spread over many CTAs and short ones share one, whatever the lengths are. A
-// run covers the end of one token, whole tokens, and the start of one more;
-// whole tokens are finished in place, and a CTA's one or two pieces of tokens
-// go to its two slots of the workspace (fp32 sums with their running maximum),
-// which the CTA that holds a token's first tile describes and a second kernel
-// joins. The split depends on the sizes alone, so results repeat bit by bit.
+// Work split. A token's keys form tiles of 64 slots. With no more tokens than
+// CTAs, each token gets as many CTAs as its tiles need at the least number of
+// tiles a CTA with which all parts fit the grid: long rows are spread over many
+// CTAs and no CTA meets two tokens. With more, the tiles of all tokens, one
+// after the other, are dealt to the CTAs in equal runs: a run covers the end of
+// one token, whole tokens, and the start of one more. Whole tokens are finished
+// in place; a CTA's one or two pieces of tokens go to its two slots of the
+// workspace (fp32 sums with their running maximum), which the CTA that holds a
+// token's first tile describes and a second kernel joins. The split follows
+// from sizes and positions alone, so results repeat bit by bit.
 //
 // A tile. All heads share a row, which is both key and value, so a tile is
 // loaded once for two products:
@@ -181,6 +183,7 @@ struct Misc {
     int64_t done;          // tiles up to the end of the batch
     int32_t run_t;         // token holding the CTA's next tile
     int32_t n_pieces;
+    int32_t tiles[kMaxGrid];  // of each token, with no more tokens than CTAs
     int32_t scan[kThreads / 32 + 1];
     uint32_t valid[kStages][2];  // per stage and loader warp: 32 slot bits
     Piece piece[kPieces];
@@ -298,7 +301,7 @@ sparse_mla_paged_kernel(const __grid_constant__ MlaPagedArgs a) {
     // everything above is local: wait for the kernels before this one
     grid_dependency_wait();
     launch_dependents();
-    const bool by_token = a.T <= (int32_t)gridDim.x;
+    const bool by_token = a.T <= (int32_t)gridDim.x;  // at most kMaxGrid, and a thread for each
     if (tid == 0 && !by_token) ws.join[c] = {-1, 0, 0, 0};
     // The lists and tables, when a line each for the grid's threads covers
     // them, are on their way to L2 while the runs are worked out.
@@ -316,35 +319,102 @@ sparse_mla_paged_kernel(const __grid_constant__ MlaPagedArgs a) {
     tc::fence_proxy_async_smem();
     tc::tc_fence_before();
 
-    // ------------------------------------------------ this CTA's run of tiles
-    // Tokens are scanned kThreads at a time; with no more than that, one scan
-    // both counts the tiles and places them.
-    const bool one_scan = a.T <= kThreads;
+    // ---------------------------------------------- this CTA's share of tiles
     Keys k = {-1, 0, 0, 0, 0};
-    int32_t n = 0, total = 0;
-    int64_t N = 0, b = 0;
-    for (int32_t t0 = 0; t0 < a.T; t0 += kThreads) {
-        const int32_t t = t0 + tid;
-        n = 0;
-        if (t < a.T) {
-            k = token_keys(a, t, c == 0);
+    int32_t n = 0;
+    int64_t s = 0, e = 1;  // by token: one piece, below; else this CTA's run of tiles
+    int64_t per = 0;
+    if (by_token) {
+        if (tid < a.T) {
+            k = token_keys(a, tid, c == 0);
             n = k.tiles();
+            ms->tiles[tid] = n;
         }
-        b = block_exclusive_scan<kThreads>(n, ms->scan, &total);
-        N += total;
-    }
-    tc::tc_fence_after();
-    const uint32_t tmem = ms->tmem_base;
-    const int64_t per = div64(N + gridDim.x - 1, gridDim.x);  // tiles of a run
-    const int64_t s = min(c * per, N), e = min(s + per, N);
-    if (s == e) {  // no run left for this CTA
         __syncthreads();
-        if (warp == kMmaWarp) tc::tmem_dealloc(tmem, kTmemCols);
-        return;
-    }
-    if (one_scan) {
-        if (b <= s && s < b + n) ms->run_t = tid;
-    } else {  // the token holding tile s
+        tc::tc_fence_after();
+        // Every warp finds the least number of tiles a CTA may get so that the
+        // tokens' parts fit the grid, and with it this CTA's token and part.
+        constexpr int kW = (kMaxGrid + 31) / 32;
+        int32_t v[kW], most = 1;
+        uint32_t low = 0, high = 0;
+#pragma unroll
+        for (int i = 0; i < kW; ++i) {
+            v[i] = 32 * i + lane < a.T ? ms->tiles[32 * i + lane] : 0;
+            most = max(most, v[i]);
+            low += (uint32_t)v[i] & 0xffffu;
+            high += (uint32_t)v[i] >> 16;
+        }
+        most = __reduce_max_sync(0xffffffffu, most);
+        const int64_t N = ((int64_t)__reduce_add_sync(0xffffffffu, high) << 16) +
+                          __reduce_add_sync(0xffffffffu, low);
+        const int32_t G = gridDim.x;
+        auto parts_of = [&](int32_t x, int32_t q) { return ((uint32_t)x + (uint32_t)q - 1u) / (uint32_t)q; };
+        int32_t lo = (int32_t)div64(N + G - 1, G), up = most;  // N / q + T <= G suffices
+        if (G > a.T) up = (int32_t)min((int64_t)most, div64(N, G - a.T) + 1);
+        while (lo < up) {
+            const int32_t q = lo + (up - lo) / 2;
+            uint32_t parts = 0;
+#pragma unroll
+            for (int i = 0; i < kW; ++i) parts += parts_of(v[i], q);
+            if (__reduce_add_sync(0xffffffffu, parts) <= (uint32_t)G) up = q;
+            else lo = q + 1;
+        }
+        int32_t mine_t = -1, mine_first = 0, mine_parts = 0, before = 0;
+#pragma unroll
+        for (int i = 0; i < kW; ++i) {
+            const int32_t p = (int32_t)parts_of(v[i], lo);
+            int32_t x = p;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int32_t y = __shfl_up_sync(0xffffffffu, x, o);
+                if (lane >= o) x += y;
+            }
+            const int32_t first = before + x - p;
+            if (first <= c && c < first + p) {
+                mine_t = 32 * i + lane;
+                mine_first = first;
+                mine_parts = p;
+            }
+            before += __shfl_sync(0xffffffffu, x, 31);
+        }
+        const uint32_t who = __ballot_sync(0xffffffffu, mine_t >= 0);
+        if (who == 0) {  // no part left for this CTA
+            __syncthreads();
+            if (warp == kMmaWarp) tc::tmem_dealloc(ms->tmem_base, kTmemCols);
+            return;
+        }
+        const int src = __ffs(who) - 1;
+        const int32_t t = __shfl_sync(0xffffffffu, mine_t, src);
+        const int32_t first = __shfl_sync(0xffffffffu, mine_first, src);
+        const int32_t parts = __shfl_sync(0xffffffffu, mine_parts, src);
+        if (tid == t) {
+            const uint32_t part = (uint32_t)(c - first);
+            ms->piece[0] = {t, (int32_t)(part * (uint32_t)n / (uint32_t)parts),
+                            (int32_t)((part + 1u) * (uint32_t)n / (uint32_t)parts),
+                            parts == 1 ? -1 : 2 * c + (part == 0 ? 1 : 0), k};
+            if (part == 0) ws.join[t] = {t, first, first + parts - 1, 0};
+            ms->n_pieces = 1;
+            ms->done = 1;
+        }
+    } else {
+        // Equal runs. Tokens are scanned kThreads at a time: once to count the
+        // tiles, once for the token that holds the run's first one.
+        int64_t N = 0;
+        int32_t total;
+        for (int32_t t0 = 0; t0 < a.T; t0 += kThreads) {
+            const int32_t t = t0 + tid;
+            block_exclusive_scan<kThreads>(t < a.T ? token_keys(a, t, c == 0).tiles() : 0, ms->scan, &total);
+            N += total;
+        }
+        tc::tc_fence_after();
+        per = div64(N + gridDim.x - 1, gridDim.x);
+        s = min(c * per, N);
+        e = min(s + per, N);
+        if (s == e) {  // no run left for this CTA
+            __syncthreads();
+            if (warp == kMmaWarp) tc::tmem_dealloc(ms->tmem_base, kTmemCols);
+            return;
+        }
         int64_t base = 0;
         for (int32_t t0 = 0; t0 < a.T && base <= s; t0 += kThreads) {
             const int32_t t = t0 + tid, nt = t < a.T ? token_keys(a, t, false).tiles() : 0;
@@ -357,6 +427,7 @@ sparse_mla_paged_kernel(const __grid_constant__ MlaPagedArgs a) {
         }
     }
     __syncthreads();
+    const uint32_t tmem = ms->tmem_base;
 
     // counters of each role, kept across batches of pieces
     uint32_t g = 0, np = 0;
@@ -364,44 +435,39 @@ sparse_mla_paged_kernel(const __grid_constant__ MlaPagedArgs a) {
     int64_t done = s;
     while (done < e) {
         // ------------------------------------------------- a batch of pieces
-        const int32_t t_first = ms->run_t;
-        int32_t t = tid;
-        int x = tid - t_first;  // place in the batch
-        if (!one_scan) {
+        if (!by_token) {
+            const int32_t t_first = ms->run_t, t = t_first + tid;
             const int64_t base = ms->run_base;
-            t = t_first + tid;
-            x = tid;
+            int32_t total;
             n = 0;
             if (tid < kPieces && t < a.T) {
                 k = token_keys(a, t, false);
                 n = k.tiles();
             }
-            b = base + block_exclusive_scan<kThreads>(n, ms->scan, &total);
-        }
-        if (x >= 0 && x < kPieces && n > 0 && b < e) {
-            Piece p;
-            p.t = t;
-            p.j0 = (int32_t)max(s - b, (int64_t)0);
-            p.j1 = (int32_t)min(e - b, (int64_t)n);
-            p.slot = p.j0 == 0 && p.j1 == n ? -1 : 2 * c + (p.j0 == 0 ? 1 : 0);
-            p.k = k;
-            ms->piece[x] = p;
-            if (by_token && p.j0 == 0)
-                ws.join[t] = {t, c, p.slot < 0 ? c : (int32_t)div64(b + n - 1, per), 0};
-            else if (p.slot == 2 * c + 1)  // starts here, goes on in other CTAs
-                ws.join[c] = {t, c, (int32_t)div64(b + n - 1, per), 0};
-            if (x == kPieces - 1 || t + 1 == a.T || b + n >= e) {
-                ms->n_pieces = x + 1;
-                ms->done = min(e, b + n);
+            const int64_t b = base + block_exclusive_scan<kThreads>(n, ms->scan, &total);
+            if (n > 0 && b < e) {
+                Piece p;
+                p.t = t;
+                p.j0 = (int32_t)max(s - b, (int64_t)0);
+                p.j1 = (int32_t)min(e - b, (int64_t)n);
+                p.slot = p.j0 == 0 && p.j1 == n ? -1 : 2 * c + (p.j0 == 0 ? 1 : 0);
+                p.k = k;
+                ms->piece[tid] = p;
+                if (p.slot == 2 * c + 1)  // starts here, goes on in other CTAs
+                    ws.join[c] = {t, c, (int32_t)div64(b + n - 1, per), 0};
+                if (tid == kPieces - 1 || t + 1 == a.T || b + n >= e) {
+                    ms->n_pieces = tid + 1;
+                    ms->done = min(e, b + n);
+                }
+            }
+            if (tid == 0) {
+                ms->run_t = t_first + kPieces;
+                ms->run_base = base + total;
             }
         }
         __syncthreads();
         done = ms->done;
         const int32_t n_pieces = ms->n_pieces;
-        if (tid == 0) {
-            ms->run_t = t_first + kPieces;
-            if (!one_scan) ms->run_base += total;
-        }
 
         if (warp == kMmaWarp) {
             // ===================================================== MMA warp
@@ -793,10 +859,10 @@ sparse_mla_paged_kernel(const __grid_constant__ MlaPagedArgs a) {
 // 8 us to drain. The first parts' sums are on their way before their factors
 // are known.
 constexpr int kJoinThreads = 256;
-constexpr int kJoinBlocks = 4;  // on an SM
+constexpr int join_blocks(int nd) { return nd == 1 ? 3 : 4; }  // on an SM, by registers
 
 template <int ND>
-__global__ void __launch_bounds__(kJoinThreads, kJoinBlocks)
+__global__ void __launch_bounds__(kJoinThreads, join_blocks(ND))
 sparse_mla_paged_join_kernel(const __grid_constant__ MlaPagedArgs a, int32_t P) {
     __shared__ float w_s[4][kMaxGrid];
     __shared__ float inv_s[4];
@@ -917,12 +983,12 @@ cudaError_t launch_sparse_mla_paged(MlaPagedArgs a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     // Small items while they fit at once: first the parts by four groups of
     // threads, then by two, then none, then two dims a thread.
-    const int quads = (a.H + 3) / 4, gx = min(a.T, grid), most = kJoinBlocks * sms;
+    const int quads = (a.H + 3) / 4, gx = min(a.T, grid);
     for (int P = 4; P > 0; P >>= 1)
-        if (2 * quads * gx * P <= most)
+        if (2 * quads * gx * P <= join_blocks(1) * sms)
             return launch_early(sparse_mla_paged_join_kernel<1>, dim3(gx, 2 * quads * P), dim3(kJoinThreads), 0,
                                 stream, a, (int32_t)P);
-    return launch_early(sparse_mla_paged_join_kernel<2>, dim3(gx, max(1, min(quads, most / gx))),
+    return launch_early(sparse_mla_paged_join_kernel<2>, dim3(gx, max(1, min(quads, join_blocks(2) * sms / gx))),
                         dim3(kJoinThreads), 0, stream, a, 1);
 }
 

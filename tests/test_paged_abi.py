@@ -102,6 +102,7 @@ def test_mla_rejects(L):
     assert call(om=2 ** 20, ops=2 ** 12) == call(cm=2 ** 20, cps=2 ** 12) == 2
     assert call(seq=NUL) == 2
     assert call(D=576) == call(H=65) == call(wr=1) == call(r=1) == 3
+    assert call(wl=2 ** 27) == call(topk=2 ** 27 + 1) == call(idx=NUL, cm=2 ** 14, cps=2 ** 14) == 3
     for k in ("q", "ori", "cmp", "out"):
         assert call(**{k: C.c_void_p(0x10008)}) == 3, k
     assert call(ws=NUL) == call(wsb=need - 1) == call(ws=C.c_void_p(0x10010)) == 4
