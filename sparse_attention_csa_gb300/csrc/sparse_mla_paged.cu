@@ -334,35 +334,37 @@ sparse_mla_paged_kernel(const __grid_constant__ MlaPagedArgs a) {
         tc::tc_fence_after();
         // Every warp finds the least number of tiles a CTA may get so that the
         // tokens' parts fit the grid, and with it this CTA's token and part.
-        constexpr int kW = (kMaxGrid + 31) / 32;
-        int32_t v[kW], most = 1;
-        uint32_t low = 0, high = 0;
-#pragma unroll
-        for (int i = 0; i < kW; ++i) {
-            v[i] = 32 * i + lane < a.T ? ms->tiles[32 * i + lane] : 0;
-            most = max(most, v[i]);
-            low += (uint32_t)v[i] & 0xffffu;
-            high += (uint32_t)v[i] >> 16;
+        // (Loops over rows of 32 tokens, not unrolled: code that runs once costs
+        // more to fetch than to execute.)
+        const int rows = (a.T + 31) >> 5;
+        auto tiles_at = [&](int i) { return 32 * i + lane < a.T ? ms->tiles[32 * i + lane] : 0; };
+        auto parts_of = [&](int32_t x, int32_t q) { return ((uint32_t)x + (uint32_t)q - 1u) / (uint32_t)q; };
+        int32_t most = 1;
+        int64_t N = 0;
+#pragma unroll 1
+        for (int i = 0; i < rows; ++i) {
+            const int32_t x = tiles_at(i);
+            most = max(most, x);
+            N += ((int64_t)__reduce_add_sync(0xffffffffu, (uint32_t)x >> 16) << 16) +
+                 __reduce_add_sync(0xffffffffu, (uint32_t)x & 0xffffu);
         }
         most = __reduce_max_sync(0xffffffffu, most);
-        const int64_t N = ((int64_t)__reduce_add_sync(0xffffffffu, high) << 16) +
-                          __reduce_add_sync(0xffffffffu, low);
         const int32_t G = gridDim.x;
-        auto parts_of = [&](int32_t x, int32_t q) { return ((uint32_t)x + (uint32_t)q - 1u) / (uint32_t)q; };
         int32_t lo = (int32_t)div64(N + G - 1, G), up = most;  // N / q + T <= G suffices
         if (G > a.T) up = (int32_t)min((int64_t)most, div64(N, G - a.T) + 1);
+#pragma unroll 1
         while (lo < up) {
             const int32_t q = lo + (up - lo) / 2;
             uint32_t parts = 0;
-#pragma unroll
-            for (int i = 0; i < kW; ++i) parts += parts_of(v[i], q);
+#pragma unroll 1
+            for (int i = 0; i < rows; ++i) parts += parts_of(tiles_at(i), q);
             if (__reduce_add_sync(0xffffffffu, parts) <= (uint32_t)G) up = q;
             else lo = q + 1;
         }
         int32_t mine_t = -1, mine_first = 0, mine_parts = 0, before = 0;
-#pragma unroll
-        for (int i = 0; i < kW; ++i) {
-            const int32_t p = (int32_t)parts_of(v[i], lo);
+#pragma unroll 1
+        for (int i = 0; i < rows && before <= c; ++i) {
+            const int32_t p = (int32_t)parts_of(tiles_at(i), lo);
             int32_t x = p;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
