@@ -501,14 +501,21 @@ def _match(dev, *specs):
         raise ValueError(f"{name} is on cuda:{t.get_device()}, the call on cuda:{dev}")
 
 
-def _scratch(workspace, dev, size, *args):
+def _scratch(workspace, dev, stream, size, *args):
     """A call's workspace and its bytes: the caller's (its size is checked by
-    the call), or a new one of `size(*args)` bytes."""
+    the call), or a new one of `size(*args)` bytes, made on the call's stream
+    (the allocator then keeps it from other streams while the call runs)."""
     if workspace is None:
         need = size(*args)
         if need == 0:
             return None, 0
-        workspace = torch.empty(need, dtype=torch.uint8, device=f"cuda:{dev}")
+        if stream is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=f"cuda:{dev}")
+        else:
+            if not isinstance(stream, torch.cuda.Stream):
+                stream = torch.cuda.ExternalStream(int(stream), device=dev)
+            with torch.cuda.stream(stream):
+                workspace = torch.empty(need, dtype=torch.uint8, device=f"cuda:{dev}")
     elif not isinstance(workspace, torch.Tensor) or workspace.get_device() != dev:
         raise ValueError(f"workspace must be a tensor on cuda:{dev}")
     elif not workspace.is_contiguous():
@@ -653,7 +660,8 @@ def csa_indexer_topk_paged(q, k_cache, w, pages, q_seq, q_pos, cmp_ratio: int, t
            (q_seq, "q_seq", torch.int32, (T,)), (q_pos, "q_pos", torch.int32, (T,)),
            (out, "out", torch.int32, (T, max(topk, 0))),
            (out_val, "out_val", torch.float32, (T, max(topk, 0))))
-    workspace, ws_bytes = _scratch(workspace, dev, csa_indexer_topk_paged_workspace_size, T,
+    workspace, ws_bytes = _scratch(workspace, dev, stream,
+                                   csa_indexer_topk_paged_workspace_size, T,
                                    min(max_pages * page, 2 ** 31 - 1), Hi, Di, topk)
     _launch(dev, "csa_indexer_topk_paged", stream, q.data_ptr(), k_cache.data_ptr(), _addr(w),
             pages.data_ptr(), _addr(q_seq), _addr(q_pos), batch, T, Hi, Di, n_pages, page, max_pages,
@@ -704,7 +712,8 @@ def csa_sparse_mla_paged(q, ori_cache, cmp_cache, cmp_sparse_indices, ori_pages,
            (q_seq, "q_seq", torch.int32, (T,)), (q_pos, "q_pos", torch.int32, (T,)),
            (sinks, "sinks", torch.float32, (H,)), (out, "out", torch.bfloat16, (T, H, D)),
            (lse, "lse", torch.float32, (T, H)))
-    workspace, ws_bytes = _scratch(workspace, dev, csa_sparse_mla_paged_workspace_size, T, H)
+    workspace, ws_bytes = _scratch(workspace, dev, stream,
+                                   csa_sparse_mla_paged_workspace_size, T, H)
     _launch(dev, "csa_sparse_mla_paged", stream, q.data_ptr(), ori_cache.data_ptr(),
             _addr(cmp_cache), _addr(cmp_sparse_indices), ori_pages.data_ptr(), _addr(cmp_pages),
             _addr(q_seq), _addr(q_pos), batch, T, H, D, ori_n, ori_page, ori_max, cmp_n, cmp_page,

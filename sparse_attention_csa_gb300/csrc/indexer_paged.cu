@@ -90,34 +90,6 @@ struct Score {
     static_assert(kSmem <= 232448, "shared memory budget");
 };
 
-template <class Misc>
-struct Ctx {
-    Misc *m;
-    int32_t *err;
-    uint64_t limit;  // pipeline waits give up after this long
-    __device__ __forceinline__ bool aborted() const {
-        return *reinterpret_cast<volatile int32_t *>(&m->abort) != 0;
-    }
-    __device__ __forceinline__ void fail(int site) const {
-        *reinterpret_cast<volatile int32_t *>(&m->abort) = 1;
-        report_error(err, kErrTimeout, kKerIndexerPaged, site);
-    }
-    __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, int site) const {
-        if (aborted()) return false;
-        if (tc::mbar_wait(bar, parity, limit)) return true;
-        fail(site);
-        return false;
-    }
-};
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32_t bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(tc::smem_u32(bar))
-                 : "memory");
-}
-
 template <int DI>
 __global__ void __launch_bounds__(kThreads, 1)
 indexer_paged_score_kernel(const __grid_constant__ IndexerPagedArgs a) {
@@ -128,7 +100,7 @@ indexer_paged_score_kernel(const __grid_constant__ IndexerPagedArgs a) {
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     Misc *ms = reinterpret_cast<Misc *>(smem + S::kOffMisc);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const Ctx<Misc> cx{ms, a.err, a.wait_ns};
+    const PipeWaits<Misc, kKerIndexerPaged> cx{ms, a.err, a.wait_ns};
     const int32_t c = blockIdx.x;
 
     if (tid == 0) {

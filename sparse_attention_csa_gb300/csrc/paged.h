@@ -8,7 +8,9 @@
 
 #include <atomic>
 
+#include "common.cuh"
 #include "csa.h"
+#include "tc_ptx.cuh"
 #include "tmap.h"
 
 namespace csa {
@@ -145,6 +147,41 @@ __device__ __forceinline__ int32_t paged_seq(const int32_t *q_seq, int32_t batch
     const int32_t b = q_seq ? __ldg(q_seq + t) : t;  // not behind the position's load
     if (pos < 0) return -1;
     return (uint32_t)b < (uint32_t)batch ? b : -2;
+}
+
+// A kernel's waits on its own pipeline barriers: bounded, and none begins once
+// one has given up (recorded in the device error word; M::abort tells the CTA).
+template <class M, int32_t kKernel>
+struct PipeWaits {
+    M *m;
+    int32_t *err;
+    uint64_t limit;  // a wait gives up after this long
+    __device__ __forceinline__ bool aborted() const {
+        return *reinterpret_cast<volatile int32_t *>(&m->abort) != 0;
+    }
+    __device__ __forceinline__ void fail(int site) const {
+        *reinterpret_cast<volatile int32_t *>(&m->abort) = 1;
+        report_error(err, kErrTimeout, kKernel, site);
+    }
+    // false on timeout or when already aborted
+    __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, int site) const {
+        if (aborted()) return false;
+        if (tc::mbar_wait(bar, parity, limit)) return true;
+        fail(site);
+        return false;
+    }
+};
+
+// 16 bytes global -> shared; `bytes` 0 writes zeros (nothing is read then).
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
+// The mbarrier counts one arrival (already included in its expected count)
+// once every cp.async this thread issued so far has landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(tc::smem_u32(bar))
+                 : "memory");
 }
 
 // a / b, by a 32-bit division when both fit.

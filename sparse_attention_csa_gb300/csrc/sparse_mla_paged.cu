@@ -194,25 +194,7 @@ struct Misc {
 constexpr size_t kSmemBytes = kOffMisc + sizeof(Misc) + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 
-struct Ctx {
-    Misc *m;
-    int32_t *err;
-    uint64_t limit;  // pipeline waits give up after this long
-    __device__ __forceinline__ bool aborted() const {
-        return *reinterpret_cast<volatile int32_t *>(&m->abort) != 0;
-    }
-    __device__ __forceinline__ void fail(int site) const {
-        *reinterpret_cast<volatile int32_t *>(&m->abort) = 1;
-        report_error(err, kErrTimeout, kKerMlaPaged, site);
-    }
-    // bounded wait; false (and abort) on timeout or when already aborted
-    __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, int site) const {
-        if (aborted()) return false;
-        if (tc::mbar_wait(bar, parity, limit)) return true;
-        fail(site);
-        return false;
-    }
-};
+using Ctx = PipeWaits<Misc, kKerMlaPaged>;
 
 // AND / OR of v over the 256 softmax threads.
 __device__ __forceinline__ bool all_of(bool v) {
@@ -250,18 +232,6 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint4 (&v)[8]) {
         f[4 * i + 3] = __uint_as_float(v[i].w);
     }
     tc::tmem_st32(taddr, f);  // the bits as they are
-}
-
-// 16 bytes global -> shared; `bytes` 0 writes zeros (nothing is read then).
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32_t bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-
-// The mbarrier counts one arrival (already included in its expected count)
-// once every cp.async this thread issued so far has landed.
-__device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(tc::smem_u32(bar))
-                 : "memory");
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
