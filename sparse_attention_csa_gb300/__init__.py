@@ -461,9 +461,10 @@ def _dims(t, name, ndim):
     """The shape of a tensor argument with `ndim` axes."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dim() != ndim:
-        raise ValueError(f"{name} must have {ndim} dims, got {tuple(t.shape)}")
-    return t.shape
+    shape = t.shape
+    if len(shape) != ndim:
+        raise ValueError(f"{name} must have {ndim} dims, got {tuple(shape)}")
+    return shape
 
 
 def _rows(t, name, ndim):
@@ -487,9 +488,12 @@ def _match(dev, *specs):
     for t, name, dtype, shape in specs:
         if t is None:
             continue
-        if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev
-                and t.shape == shape and t.is_contiguous() and dev >= 0):
-            continue
+        try:
+            if (t.dtype is dtype and t.shape == shape and t.get_device() == dev >= 0
+                    and t.is_contiguous()):
+                continue
+        except AttributeError:
+            pass
         if not isinstance(t, torch.Tensor) or not t.is_cuda:
             raise TypeError(f"{name} must be a CUDA tensor")
         if t.dtype is not dtype:
