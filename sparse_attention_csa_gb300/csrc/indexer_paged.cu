@@ -23,7 +23,11 @@
 // never fall lower) nearly always leaves a handful of candidates in the bin of
 // the topk-th; they are ranked directly. More than kCand of them (outliers,
 // equal scores, infinities) go through radix passes over that bin's keys. The
-// rows are emitted in order by counts over lanes, warps and CTAs.
+// rows are emitted in order by counts over lanes, warps and CTAs. Bound by the
+// latency of its steps: 2 MB read.
+//
+// Both together: one token over 32768 rows 14.2 us; 64 tokens over 0.57 million
+// rows, 146 MB, 39.3 us, the scores alone at 4.5 TB/s under a profiler.
 #include "common.cuh"
 #include "internal.h"
 #include "paged.h"
@@ -760,8 +764,8 @@ cudaError_t launch_indexer_topk_paged(IndexerPagedArgs a, cudaStream_t stream) {
     }
     // CTAs a token: as few as hold the longest row the table allows in their
     // registers (a cluster's barriers and words cost more than its CTAs save:
-    // one token of 32768 rows 16.6 us with four, 18.4 with eight; 64 tokens of
-    // up to 16384 rows 44 us with two, 47 with four).
+    // whole calls of one token over 32768 rows 14.2 us, 16.0 with twice the
+    // CTAs; of 64 tokens over up to 16384 rows 39.4 us, 41.0 with twice).
     int C = 1;
     while (C < kMaxCluster && (int64_t)C * kSelRows < a.max_rows) C *= 2;
     const bool held = (int64_t)C * kSelRows >= a.max_rows;
