@@ -428,7 +428,7 @@ struct Sel {
 // reads it again.
 template <int C, bool kHeld>
 __global__ void __launch_bounds__(kSelThreads, 2)
-indexer_paged_select_kernel(const __grid_constant__ IndexerPagedArgs a, int32_t after_scores) {
+indexer_paged_select_kernel(const __grid_constant__ IndexerPagedArgs a) {
     __shared__ Sel sm;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = C > 1 ? cluster_rank() : 0;
@@ -450,13 +450,10 @@ indexer_paged_select_kernel(const __grid_constant__ IndexerPagedArgs a, int32_t 
         sm.range[0] = 0xffffffffu;
         sm.range[1] = 0u;
     }
-    // The score kernel lets this one start only after its own wait for the
-    // kernels before it: behind it, the positions are there already.
-    if (!after_scores) grid_dependency_wait();
+    grid_dependency_wait();
+    launch_dependents();
     int32_t seq;
     const int32_t n = visible_rows(a, t, &seq, tid == 0 && rank == 0);
-    if (after_scores) grid_dependency_wait();
-    launch_dependents();
     const float *sc = a.scores + (int64_t)t * a.row_pad;
     int32_t *idx = a.topk_idx + (int64_t)t * K;
     float *val = a.topk_val ? a.topk_val + (int64_t)t * K : nullptr;
@@ -713,7 +710,7 @@ indexer_paged_select_kernel(const __grid_constant__ IndexerPagedArgs a, int32_t 
 }
 
 template <int C>
-cudaError_t launch_select(const IndexerPagedArgs &a, bool held, bool after_scores, cudaStream_t stream) {
+cudaError_t launch_select(const IndexerPagedArgs &a, bool held, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)a.T * C);
     cfg.blockDim = dim3(kSelThreads);
@@ -726,8 +723,8 @@ cudaError_t launch_select(const IndexerPagedArgs &a, bool held, bool after_score
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = C > 1 ? 2 : 1;
-    return held ? cudaLaunchKernelEx(&cfg, indexer_paged_select_kernel<C, true>, a, (int32_t)after_scores)
-                : cudaLaunchKernelEx(&cfg, indexer_paged_select_kernel<C, false>, a, (int32_t)after_scores);
+    return held ? cudaLaunchKernelEx(&cfg, indexer_paged_select_kernel<C, true>, a)
+                : cudaLaunchKernelEx(&cfg, indexer_paged_select_kernel<C, false>, a);
 }
 
 template <int DI>
@@ -770,10 +767,10 @@ cudaError_t launch_indexer_topk_paged(IndexerPagedArgs a, cudaStream_t stream) {
     while (C < kMaxCluster && (int64_t)C * kSelRows < a.max_rows) C *= 2;
     const bool held = (int64_t)C * kSelRows >= a.max_rows;
     switch (C) {
-        case 1: return launch_select<1>(a, held, scored, stream);
-        case 2: return launch_select<2>(a, held, scored, stream);
-        case 4: return launch_select<4>(a, held, scored, stream);
-        default: return launch_select<8>(a, held, scored, stream);
+        case 1: return launch_select<1>(a, held, stream);
+        case 2: return launch_select<2>(a, held, stream);
+        case 4: return launch_select<4>(a, held, stream);
+        default: return launch_select<8>(a, held, stream);
     }
 }
 

@@ -1,0 +1,84 @@
+"""GPU tests of the order of the paged calls against the work around them:
+inputs written right before a call, results on other streams."""
+
+import numpy as np
+import pytest
+import torch
+
+import sparse_attention_csa_gb300 as csa
+from tests import _paged_ref as R
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def clean_error_word():
+    yield
+    torch.cuda.synchronize()
+    assert csa.csa_device_error() == (0, 0)
+
+
+def i32(x):
+    return torch.as_tensor(np.asarray(x, dtype=np.int32)).cuda()
+
+
+class Rows:
+    """Three sequences' indexer rows, and tokens that move over them."""
+
+    def __init__(self, n, topk=32, seed=0):
+        gen = torch.Generator().manual_seed(seed)
+        table, total = R.pool_rows([n, n, n], 64, seed=seed)
+        self.table, self.topk = i32(table), topk
+        self.cache = R.grid(gen, (total, 64, 64), 0.5, torch.bfloat16).cuda()
+        self.q = R.grid(gen, (3, 8, 64), 0.5, torch.bfloat16).cuda()
+        self.w = R.grid(gen, (3, 8), 0.125, torch.float32).cuda()
+
+    def call(self, seq, pos, **kw):
+        return csa.csa_indexer_topk_paged(self.q, self.cache, self.w, self.table, seq, pos, 4, self.topk, **kw)
+
+
+@pytest.mark.parametrize("n", [300, 12000, 40000])
+def test_indexer_sees_positions_written_right_before(n):
+    """Positions and sequence numbers changed by a kernel between calls, also in
+    a graph: each call answers for what stands there when its turn comes."""
+    c = Rows(n)
+    steps = 24
+    rng = np.random.default_rng(n)
+    all_seq = i32(rng.integers(0, 3, (steps, 3)))
+    all_pos = i32(rng.integers(-1, 4 * n, (steps, 3)))
+    want = []
+    for k in range(steps):
+        torch.cuda.synchronize()
+        want.append(c.call(all_seq[k].clone(), all_pos[k].clone(), return_value=True))
+        torch.cuda.synchronize()
+    seq, pos = torch.zeros_like(all_seq[0]), torch.zeros_like(all_pos[0])
+    ws = torch.empty(csa.csa_indexer_topk_paged_workspace_size(3, c.table.shape[1] * 64, 8, 64, c.topk),
+                     dtype=torch.uint8, device="cuda")
+    outs = [(torch.empty((3, c.topk), dtype=torch.int32, device="cuda"),
+             torch.empty((3, c.topk), device="cuda")) for _ in range(steps)]
+
+    def run():
+        for k in range(steps):
+            seq.copy_(all_seq[k])
+            pos.copy_(all_pos[k])
+            c.call(seq, pos, return_value=True, workspace=ws, out=outs[k][0], out_val=outs[k][1])
+
+    def same():
+        torch.cuda.synchronize()
+        return all(torch.equal(a, b) and torch.equal(x, y) for (a, x), (b, y) in zip(want, outs))
+
+    run()
+    assert same()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run()
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run()
+    for a, x in outs:
+        a.zero_()
+        x.zero_()
+    g.replay()
+    assert same()
