@@ -318,19 +318,21 @@ indexer_paged_score_kernel(const __grid_constant__ IndexerPagedArgs a) {
             }
         } else {
             // =============================================== epilogue warps
+            // Every wait's result is the warp's, not a lane's: what follows is
+            // collective, and lanes that gave up must not part from the others.
             const uint32_t lane_addr = tmem + ((uint32_t)(32 * warp) << 16);
             bool ok = true;
             for (int32_t i = 0; i < n_pieces && ok; ++i) {
                 const Piece p = ms->piece[i];
                 if (p.j0 >= p.j1) continue;
-                ok = cx.wait(&ms->q_full[np & 1], (np >> 1) & 1, 30);
+                ok = __all_sync(0xffffffffu, cx.wait(&ms->q_full[np & 1], (np >> 1) & 1, 30));
+                if (!ok) break;
                 const float4 *w4 = reinterpret_cast<const float4 *>(ms->w[np & 1]);
                 float *out = a.scores + (int64_t)p.t * a.row_pad;
-                for (int32_t j = p.j0; j < p.j1 && ok; ++j, ++g) {
+                for (int32_t j = p.j0; j < p.j1; ++j, ++g) {
                     const uint32_t st = g % S::kStages, acc = g % kAcc;
-                    ok = cx.wait(&ms->k_full[st], (g / S::kStages) & 1, 31) &&
-                         cx.wait(&ms->acc_full[acc], (g / kAcc) & 1, 32);
-                    ok = __all_sync(0xffffffffu, ok);
+                    ok = __all_sync(0xffffffffu, cx.wait(&ms->k_full[st], (g / S::kStages) & 1, 31) &&
+                                                     cx.wait(&ms->acc_full[acc], (g / kAcc) & 1, 32));
                     if (!ok) break;
                     tc::tc_fence_after();
                     const bool there = (ms->present[st][warp] >> lane) & 1u;

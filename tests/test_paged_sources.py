@@ -44,3 +44,21 @@ def test_nothing_is_read_before_the_wait(name, expected):
         for touch in ("__ldg", "visible_rows(", "token_keys(", "paged_seq(", "paged_row(", "report_error("):
             assert touch not in ahead, f"{kernel}: {touch} before the wait"
         assert "launch_dependents();" not in ahead, f"{kernel}: lets others start before its own wait"
+
+
+def statements(body):
+    return [" ".join(x.split()) for x in re.split(r"[;{}]", body) if x.strip()]
+
+
+def test_waits_of_whole_warps_are_voted():
+    """Where a whole warp waits in the score kernel, one lane's wait may give up
+    while another's ends well. The lanes have to go on alike: a vote or a
+    warp-wide load that part of a warp skips never ends. (The MMA role is one
+    lane and needs no vote.)"""
+    body = kernels("indexer_paged.cu")["indexer_paged_score_kernel"]
+    one_lane = body[body.index("if (warp == kMmaWarp) {\n            \n"):body.index("__syncwarp();")]
+    assert "if (lane == 0) {" in one_lane and "cx.wait(" in one_lane
+    waits = [x for x in statements(body.replace(one_lane, "")) if "cx.wait(" in x]
+    assert len(waits) == 4
+    for x in waits:
+        assert "__all_sync(0xffffffffu, cx.wait(" in x, x
