@@ -11,6 +11,13 @@ call fails loudly when the library has not been built.
 PyTorch supplies device memory and the current CUDA stream. All tensors are
 CUDA tensors in THD layout, contiguous, with the dtypes ``include/csa.h``
 states (bf16 activations, fp32 weights/sinks/outputs, int32 indices).
+
+The rotation and the paged calls make results and workspaces that they are not
+given from the memory of the call's ``stream``: used on another stream, such a
+result needs what any tensor of that stream needs (an event, and
+``record_stream`` where it may be freed early). The other calls make theirs
+from the current stream's; given a ``stream`` that is not the current one, pass
+them their outputs.
 """
 
 from __future__ import annotations
@@ -505,21 +512,26 @@ def _match(dev, *specs):
         raise ValueError(f"{name} is on cuda:{t.get_device()}, the call on cuda:{dev}")
 
 
+def _new(shape, dtype, dev, stream):
+    """A new tensor on device `dev` from the memory of the call's stream (None:
+    that device's current one). Another stream's block may still be in use by
+    work queued there, which the call's stream does not wait for."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
 def _scratch(workspace, dev, stream, size, *args):
     """A call's workspace and its bytes: the caller's (its size is checked by
-    the call), or a new one of `size(*args)` bytes, made on the call's stream
-    (the allocator then keeps it from other streams while the call runs)."""
+    the call), or a new one of `size(*args)` bytes."""
     if workspace is None:
         need = size(*args)
         if need == 0:
             return None, 0
-        if stream is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=f"cuda:{dev}")
-        else:
-            if not isinstance(stream, torch.cuda.Stream):
-                stream = torch.cuda.ExternalStream(int(stream), device=dev)
-            with torch.cuda.stream(stream):
-                workspace = torch.empty(need, dtype=torch.uint8, device=f"cuda:{dev}")
+        workspace = _new((need,), torch.uint8, dev, stream)
     elif not isinstance(workspace, torch.Tensor) or workspace.get_device() != dev:
         raise ValueError(f"workspace must be a tensor on cuda:{dev}")
     elif not workspace.is_contiguous():
@@ -562,10 +574,17 @@ def csa_rope_freqs(rope_dim: int, theta: float = 10000.0, factor: float = 1.0,
     positions for longer contexts: all pairs (``original_len`` 0) or the slow
     ones, by parts."""
     rope_dim = int(rope_dim)
+    half = max(rope_dim, 0) // 2
     if out is None:
-        out = torch.empty((max(rope_dim, 0) // 2,), dtype=torch.float64, device=device or "cuda")
-    dev = out.get_device()
-    _match(dev, (out, "out", torch.float64, (max(rope_dim, 0) // 2,)))
+        device = torch.device(device or "cuda")
+        if device.type != "cuda":
+            raise TypeError(f"device must be a CUDA device, got {device}")
+        dev = torch.cuda.current_device() if device.index is None else device.index
+        out = _new((half,), torch.float64, dev, stream)
+    else:
+        _dims(out, "out", 1)
+        dev = out.get_device()
+        _match(dev, (out, "out", torch.float64, (half,)))
     _launch(dev, "csa_rope_freqs", stream, rope_dim, theta, factor, int(original_len), beta_fast,
             beta_slow, out.data_ptr())
     return out
@@ -585,9 +604,7 @@ def csa_rope(x, positions, inv_freq, rope_offset=None, layout: str = "interleave
     dev, shape = x.get_device(), x.shape
     T, D = shape[0], shape[-1]
     H = shape[1] if len(shape) == 3 else 1
-    if out is None:
-        out = torch.empty(shape, dtype=x.dtype, device=x.device)
-    elif out is not x:
+    if out is not None and out is not x:
         if _rows(out, "out", (2, 3)) != code:
             raise TypeError(f"out must be {x.dtype}, got {out.dtype}")
         if out.shape != shape or out.get_device() != dev:
@@ -598,9 +615,12 @@ def csa_rope(x, positions, inv_freq, rope_offset=None, layout: str = "interleave
     _match(dev, (positions, "positions", torch.int32, (T,)),
            (inv_freq, "inv_freq", torch.float64, (half,)),
            (cu_seqlens, "cu_seqlens", torch.int32, (batch + 1,)))
+    code_layout = _layout(layout)
+    if out is None:
+        out = _new(shape, x.dtype, dev, stream)
     _launch(dev, "csa_rope", stream, x.data_ptr(), code, x.stride(0), _addr(positions),
             _addr(cu_seqlens), batch, pos_stride, _addr(inv_freq), T, H, D,
-            D - 2 * half if rope_offset is None else rope_offset, 2 * half, _layout(layout), mscale,
+            D - 2 * half if rope_offset is None else rope_offset, 2 * half, code_layout, mscale,
             1 if inverse else 0, out.data_ptr(), out.stride(0))
     return out
 
@@ -652,18 +672,18 @@ def csa_indexer_topk_paged(q, k_cache, w, pages, q_seq, q_pos, cmp_ratio: int, t
     batch, max_pages = _dims(pages, "pages", 2)
     dev = q.get_device()
     topk = int(topk)
-    if out is None:
-        out = torch.empty((T, max(topk, 0)), dtype=torch.int32, device=q.device)
+    shape = (T, max(topk, 0))
     if not return_value:
         out_val = None
-    elif out_val is None:
-        out_val = torch.empty((T, max(topk, 0)), dtype=torch.float32, device=q.device)
     _match(dev, (q, "q", torch.bfloat16, (T, Hi, Di)),
            (k_cache, "k_cache", torch.bfloat16, (n_pages, page, Di)),
            (w, "w", torch.float32, (T, Hi)), (pages, "pages", torch.int32, (batch, max_pages)),
            (q_seq, "q_seq", torch.int32, (T,)), (q_pos, "q_pos", torch.int32, (T,)),
-           (out, "out", torch.int32, (T, max(topk, 0))),
-           (out_val, "out_val", torch.float32, (T, max(topk, 0))))
+           (out, "out", torch.int32, shape), (out_val, "out_val", torch.float32, shape))
+    if out is None:
+        out = _new(shape, torch.int32, dev, stream)
+    if return_value and out_val is None:
+        out_val = _new(shape, torch.float32, dev, stream)
     workspace, ws_bytes = _scratch(workspace, dev, stream,
                                    csa_indexer_topk_paged_workspace_size, T,
                                    min(max_pages * page, 2 ** 31 - 1), Hi, Di, topk)
@@ -701,12 +721,8 @@ def csa_sparse_mla_paged(q, ori_cache, cmp_cache, cmp_sparse_indices, ori_pages,
         cmp_max = _dims(cmp_pages, "cmp_pages", 2)[1]
         if cmp_sparse_indices is not None:
             topk = _dims(cmp_sparse_indices, "cmp_sparse_indices", 2)[1]
-    if out is None:
-        out = torch.empty_like(q)
     if not return_softmax_lse:
         lse = None
-    elif lse is None:
-        lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
     _match(dev, (q, "q", torch.bfloat16, (T, H, D)),
            (ori_cache, "ori_cache", torch.bfloat16, (ori_n, ori_page, D)),
            (cmp_cache, "cmp_cache", torch.bfloat16, (cmp_n, cmp_page, D)),
@@ -716,6 +732,10 @@ def csa_sparse_mla_paged(q, ori_cache, cmp_cache, cmp_sparse_indices, ori_pages,
            (q_seq, "q_seq", torch.int32, (T,)), (q_pos, "q_pos", torch.int32, (T,)),
            (sinks, "sinks", torch.float32, (H,)), (out, "out", torch.bfloat16, (T, H, D)),
            (lse, "lse", torch.float32, (T, H)))
+    if out is None:
+        out = _new((T, H, D), torch.bfloat16, dev, stream)
+    if return_softmax_lse and lse is None:
+        lse = _new((T, H), torch.float32, dev, stream)
     workspace, ws_bytes = _scratch(workspace, dev, stream,
                                    csa_sparse_mla_paged_workspace_size, T, H)
     _launch(dev, "csa_sparse_mla_paged", stream, q.data_ptr(), ori_cache.data_ptr(),

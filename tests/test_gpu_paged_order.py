@@ -82,3 +82,49 @@ def test_indexer_sees_positions_written_right_before(n):
         x.zero_()
     g.replay()
     assert same()
+
+
+def busy_blocks(shapes_dtypes, value):
+    """Frees blocks of these sizes that the current stream goes on writing for
+    a while: what the allocator would hand out next to the current stream."""
+    blocks = [torch.empty(s, dtype=d, device="cuda") for s, d in shapes_dtypes]
+    torch.cuda._sleep(200_000_000)
+    for b in blocks:
+        b.fill_(value)
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_results_belong_to_the_calls_stream(raw):
+    """With `stream=` naming a stream that is not the current one, results that
+    the call makes itself are not memory which work pending on the current
+    stream still writes."""
+    side = torch.cuda.Stream()
+    stream = side.cuda_stream if raw else side
+    gen = torch.Generator().manual_seed(3)
+    c = Rows(3000)
+    seq, pos = i32([0, 1, 2]), i32([11999, 5000, 700])
+    x = torch.randn((64, 8, 512), generator=gen).bfloat16().cuda()
+    xpos, inv = torch.arange(64, dtype=torch.int32).cuda(), csa.csa_rope_freqs(64)
+    ori = torch.randn((40, 64, 512), generator=gen).bfloat16().cuda()
+    table, none, late = i32(np.arange(40)[None]), torch.zeros_like(xpos), xpos + 2000
+    calls = [
+        (lambda **k: (csa.csa_rope(x, xpos, inv, **k),), [((64, 8, 512), torch.bfloat16)]),
+        (lambda **k: (csa.csa_rope_freqs(4096, 5e5, **k),), [((2048,), torch.float64)]),
+        (lambda **k: c.call(seq, pos, return_value=True, **k),
+         [((3, 32), torch.int32), ((3, 32), torch.float32)]),
+        (lambda **k: csa.csa_sparse_mla_paged(x, ori, None, None, table, None, none, late, None, 0.04, 1, 127,
+                                              return_softmax_lse=True, **k),
+         [((64, 8, 512), torch.bfloat16), ((64, 8), torch.float32)]),
+    ]
+    for call, made in calls:
+        want = [w.clone() for w in call() if w is not None]
+        torch.cuda.synchronize()
+        torch.cuda.empty_cache()
+        busy_blocks(made, 7)
+        got = call(stream=stream)
+        side.synchronize()
+        with torch.cuda.stream(side):
+            early = [g.clone() for g in got]
+        torch.cuda.synchronize()
+        for w, e, g in zip(want, early, got):
+            assert torch.equal(w, e) and torch.equal(w, g)
