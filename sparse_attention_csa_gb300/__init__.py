@@ -539,6 +539,13 @@ def _scratch(workspace, dev, stream, size, *args):
     return workspace, workspace.numel() * workspace.element_size()
 
 
+def _written(*tensors):
+    """Tells autograd that the call wrote these tensors of the caller's (None:
+    not given), as PyTorch's own in-place calls do: a graph that saved one of
+    them then refuses its backward instead of using the new values."""
+    torch._C._increment_version([t for t in tensors if t is not None])
+
+
 def _addr(t):
     return None if t is None else t.data_ptr()
 
@@ -556,7 +563,7 @@ def _launch(dev, where, stream, *args):
         stream = torch._C._cuda_getCurrentRawStream(dev)
     elif hasattr(stream, "cuda_stream"):
         stream = stream.cuda_stream
-    fn = getattr(lib(), where)
+    fn = getattr(_lib or lib(), where)
     if torch._C._cuda_getDevice() == dev:
         rc = fn(*args, stream)
     else:
@@ -574,7 +581,7 @@ def csa_rope_freqs(rope_dim: int, theta: float = 10000.0, factor: float = 1.0,
     positions for longer contexts: all pairs (``original_len`` 0) or the slow
     ones, by parts."""
     rope_dim = int(rope_dim)
-    half = max(rope_dim, 0) // 2
+    half, given = max(rope_dim, 0) // 2, out
     if out is None:
         device = torch.device(device or "cuda")
         if device.type != "cuda":
@@ -587,6 +594,7 @@ def csa_rope_freqs(rope_dim: int, theta: float = 10000.0, factor: float = 1.0,
         _match(dev, (out, "out", torch.float64, (half,)))
     _launch(dev, "csa_rope_freqs", stream, rope_dim, theta, factor, int(original_len), beta_fast,
             beta_slow, out.data_ptr())
+    _written(given)
     return out
 
 
@@ -599,7 +607,12 @@ def csa_rope(x, positions, inv_freq, rope_offset=None, layout: str = "interleave
 
     ``positions`` [T] int32, or None with ``cu_seqlens`` [batch+1]: the place
     in the packed sequence; both times ``pos_stride``. ``inverse`` turns back,
-    which is also the backward. ``out`` may be ``x``. Returns out."""
+    which is also the backward. ``out`` may be ``x``. Returns out.
+
+    As with every call here, nothing is recorded for autograd: the result of an
+    ``x`` that requires a gradient does not require one, and the caller turns
+    the gradient back with ``inverse``. Tensors of the caller's that are written
+    (``out``, the caches) count as changed in place, though."""
     code = _rows(x, "x", (2, 3))
     dev, shape = x.get_device(), x.shape
     T, D = shape[0], shape[-1]
@@ -615,13 +628,14 @@ def csa_rope(x, positions, inv_freq, rope_offset=None, layout: str = "interleave
     _match(dev, (positions, "positions", torch.int32, (T,)),
            (inv_freq, "inv_freq", torch.float64, (half,)),
            (cu_seqlens, "cu_seqlens", torch.int32, (batch + 1,)))
-    code_layout = _layout(layout)
+    code_layout, given = _layout(layout), out
     if out is None:
         out = _new(shape, x.dtype, dev, stream)
     _launch(dev, "csa_rope", stream, x.data_ptr(), code, x.stride(0), _addr(positions),
             _addr(cu_seqlens), batch, pos_stride, _addr(inv_freq), T, H, D,
             D - 2 * half if rope_offset is None else rope_offset, 2 * half, code_layout, mscale,
             1 if inverse else 0, out.data_ptr(), out.stride(0))
+    _written(given)
     return out
 
 
@@ -648,6 +662,7 @@ def csa_cache_append(rows, row_seq, row_pos, pages, cache, inv_freq=None, rope_o
             _addr(row_pos), pages.data_ptr(), batch, max_pages, n_pages, page, T, width,
             _addr(inv_freq), width - 2 * half if rope_offset is None else rope_offset, 2 * half,
             _layout(layout), mscale, pos_stride, cache.data_ptr())
+    _written(cache)
     return cache
 
 
@@ -680,6 +695,7 @@ def csa_indexer_topk_paged(q, k_cache, w, pages, q_seq, q_pos, cmp_ratio: int, t
            (w, "w", torch.float32, (T, Hi)), (pages, "pages", torch.int32, (batch, max_pages)),
            (q_seq, "q_seq", torch.int32, (T,)), (q_pos, "q_pos", torch.int32, (T,)),
            (out, "out", torch.int32, shape), (out_val, "out_val", torch.float32, shape))
+    given = out, out_val
     if out is None:
         out = _new(shape, torch.int32, dev, stream)
     if return_value and out_val is None:
@@ -690,6 +706,7 @@ def csa_indexer_topk_paged(q, k_cache, w, pages, q_seq, q_pos, cmp_ratio: int, t
     _launch(dev, "csa_indexer_topk_paged", stream, q.data_ptr(), k_cache.data_ptr(), _addr(w),
             pages.data_ptr(), _addr(q_seq), _addr(q_pos), batch, T, Hi, Di, n_pages, page, max_pages,
             cmp_ratio, topk, out.data_ptr(), _addr(out_val), _addr(workspace), ws_bytes)
+    _written(*given)
     return out, out_val
 
 
@@ -732,6 +749,7 @@ def csa_sparse_mla_paged(q, ori_cache, cmp_cache, cmp_sparse_indices, ori_pages,
            (q_seq, "q_seq", torch.int32, (T,)), (q_pos, "q_pos", torch.int32, (T,)),
            (sinks, "sinks", torch.float32, (H,)), (out, "out", torch.bfloat16, (T, H, D)),
            (lse, "lse", torch.float32, (T, H)))
+    given = out, lse
     if out is None:
         out = _new((T, H, D), torch.bfloat16, dev, stream)
     if return_softmax_lse and lse is None:
@@ -743,6 +761,7 @@ def csa_sparse_mla_paged(q, ori_cache, cmp_cache, cmp_sparse_indices, ori_pages,
             _addr(q_seq), _addr(q_pos), batch, T, H, D, ori_n, ori_page, ori_max, cmp_n, cmp_page,
             cmp_max, topk, _addr(sinks), softmax_scale, cmp_ratio, ori_win_left, ori_win_right,
             out.data_ptr(), _addr(lse), 1 if return_softmax_lse else 0, _addr(workspace), ws_bytes)
+    _written(*given)
     return out, lse
 
 
