@@ -562,7 +562,9 @@ csa_status_t csa_indexer_topk_paged(const csa_bf16_t *q, const csa_bf16_t *k_cac
  * may be absent (a server releases them as the window moves on); a page that
  * is needed and absent is recorded and its rows are left out. A token left
  * without any row gets out = 0 and lse = its sink (-inf without sinks); a
- * padding slot out = 0 and lse = -inf.
+ * padding slot out = 0 and lse = -inf. A NaN in a head's query or sink, or in a
+ * row that a token sees, makes that head's (that token's) out and lse NaN, and
+ * so does a sink of +inf; rows that no token sees may hold anything.
  * The keys of all tokens are split evenly over the GPU whatever their lengths
  * and joined through the workspace; the split follows from the sizes and
  * positions alone, so equal calls give equal bits.

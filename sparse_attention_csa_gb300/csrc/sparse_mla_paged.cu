@@ -703,7 +703,8 @@ sparse_mla_paged_kernel(const __grid_constant__ MlaPagedArgs a) {
                         }
                         l *= al;
 #pragma unroll
-                        for (int x = 0; x < 16; ++x) v[x] = m == -INFINITY ? -INFINITY : v[x] - m;
+                        for (int x = 0; x < 16; ++x)
+                            v[x] = m == -INFINITY ? v[x] : v[x] - m;  // no maximum yet: -inf or NaN
                         if (j > 0) {
                             if (wg == 0 && !hi) ms->fac[h] = al;
                             if (any_of(al != 1.0f)) {
@@ -766,7 +767,7 @@ sparse_mla_paged_kernel(const __grid_constant__ MlaPagedArgs a) {
                         const float M = fmaxf(m, sk);
                         const float w = m == -INFINITY ? 0.0f : tc::ex2_approx(m - M);
                         const float Z = fmaf(l, w, sk == -INFINITY ? 0.0f : tc::ex2_approx(sk - M));
-                        f = Z > 0.0f ? w / Z : 0.0f;
+                        f = Z == 0.0f ? 0.0f : w / Z;  // no key and no sink: 0; a NaN stays one
                         if (a.lse && h < a.H)
                             a.lse[(int64_t)tt * a.H + h] = (M + tc::lg2_approx(Z)) * kLn2;
                     } else {  // all 64: the join reads them by fours
@@ -884,7 +885,7 @@ sparse_mla_paged_join_kernel(const __grid_constant__ MlaPagedArgs a, int32_t P) 
             }
             z = warp_sum(z) + (sk == -INFINITY ? 0.0f : tc::ex2_approx(sk - M));
             if (lane == 0) {
-                inv_s[warp] = z > 0.0f ? 1.0f / z : 0.0f;
+                inv_s[warp] = z == 0.0f ? 0.0f : 1.0f / z;  // a NaN stays one
                 if (a.lse && h < a.H && item % slices == 0)
                     a.lse[(int64_t)jn.t * a.H + h] = (M + tc::lg2_approx(z)) * kLn2;
             }
