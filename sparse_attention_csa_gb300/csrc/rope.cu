@@ -266,6 +266,9 @@ bool aligned(const void *p, int64_t stride_bytes) {
     return ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)stride_bytes) & 15u) == 0;
 }
 
+// Blocks of `each` for n things, n up to 2^31 - 1.
+unsigned blocks(int32_t n, int each) { return (unsigned)(((int64_t)n + each - 1) / each); }
+
 }  // namespace
 
 cudaError_t launch_rope_freqs(const RopeFreqsArgs &a, cudaStream_t stream) {
@@ -285,7 +288,7 @@ cudaError_t launch_rope(const RopeArgs &a, cudaStream_t stream) {
     rows = min(rows, max((int64_t)1, (int64_t)a.T * a.H / 304));
     const int hb = (int)min((int64_t)a.H, rows);
     const int tb = (int)max((int64_t)1, min(min(rows / hb, (int64_t)kMaxRows), (int64_t)(kTable / (a.n / 2))));
-    const dim3 grid((a.T + tb - 1) / tb, (a.H + hb - 1) / hb);
+    const dim3 grid(blocks(a.T, tb), blocks(a.H, hb));
 #define CSA_ROPE(T, VV)                                                          \
     do {                                                                         \
         if (a.half)                                                              \
@@ -309,7 +312,7 @@ cudaError_t launch_cache_append(const AppendArgs &a, cudaStream_t stream) {
     rows = min(rows, max(1, a.T / 304));
     int tb = min(rows, kMaxRows);
     if (a.n > 0) tb = max(1, min(tb, kTable / (a.n / 2)));
-    const dim3 grid((a.T + tb - 1) / tb);
+    const dim3 grid(blocks(a.T, tb));
 #define CSA_APPEND(T, VV)                                                          \
     do {                                                                           \
         if (a.half)                                                                \
