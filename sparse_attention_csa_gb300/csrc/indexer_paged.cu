@@ -747,7 +747,8 @@ cudaError_t launch_indexer_topk_paged(IndexerPagedArgs a, cudaStream_t stream) {
     int sms, dev;
     bool first;
     unsigned long long ctx;
-    cudaError_t e = enter_context(pc, &sms, &first, &ctx, &dev);
+    cudaError_t e = enter_context(pc, &first, &ctx, &dev);
+    if (e == cudaSuccess) e = sm_count(&sms);
     if (e != cudaSuccess) return e;
     if (first) {
         if ((e = allow_smem<64>()) != cudaSuccess || (e = allow_smem<128>()) != cudaSuccess) return e;

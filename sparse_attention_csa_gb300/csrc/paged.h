@@ -15,16 +15,14 @@
 
 namespace csa {
 
-// Number of SMs of the current device, and whether this is the first call of
-// this place (a static of the caller's) in the device's present context: a
-// kernel's attributes are set once for each.
+// Whether this is the first call of this place (a static of the caller's) in
+// the current device's present context: a kernel's attributes are set once for
+// each.
 constexpr int kPagedDevices = 64;
 struct PerContext {
     std::atomic<unsigned long long> seen[kPagedDevices];
-    std::atomic<int> sms[kPagedDevices];
 };
-inline cudaError_t enter_context(PerContext &pc, int *sms, bool *first, unsigned long long *ctx,
-                                 int *device) {
+inline cudaError_t enter_context(PerContext &pc, bool *first, unsigned long long *ctx, int *device) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -32,16 +30,26 @@ inline cudaError_t enter_context(PerContext &pc, int *sms, bool *first, unsigned
     *device = dev;
     *ctx = current_context_id();
     *first = *ctx == 0 || pc.seen[dev].load(std::memory_order_acquire) != *ctx;
-    *sms = pc.sms[dev].load(std::memory_order_relaxed);
-    if (*sms == 0) {
-        e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
-        if (e != cudaSuccess) return e;
-        pc.sms[dev].store(*sms, std::memory_order_relaxed);
-    }
     return cudaSuccess;
 }
 inline void entered_context(PerContext &pc, int device, unsigned long long ctx) {
     pc.seen[device].store(ctx, std::memory_order_release);
+}
+
+// SMs of the current device, looked up once.
+inline cudaError_t sm_count(int *sms) {
+    static std::atomic<int> known[kPagedDevices];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kPagedDevices) return cudaErrorInvalidDevice;
+    *sms = known[dev].load(std::memory_order_relaxed);
+    if (*sms == 0) {
+        e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+        if (e != cudaSuccess) return e;
+        known[dev].store(*sms, std::memory_order_relaxed);
+    }
+    return cudaSuccess;
 }
 
 struct RopeFreqsArgs {

@@ -282,10 +282,13 @@ cudaError_t launch_rope(const RopeArgs &a, cudaStream_t stream) {
     const bool vec = aligned(a.x, a.x_stride * es) && aligned(a.out, a.out_stride * es) &&
                      a.D % V == 0 && a.off % V == 0 && a.n % (2 * V) == 0;
     const int units = (a.x == a.out ? a.n : a.D) / (vec ? V : 1);
+    int sms;
+    const cudaError_t e = sm_count(&sms);
+    if (e != cudaSuccess) return e;
     // rows (token, head) per block: about sixteen units a thread, fewer while
-    // that leaves SMs without a block
+    // that leaves an SM with less than two blocks
     int64_t rows = max(1, 16 * kThreads / max(units, 1));
-    rows = min(rows, max((int64_t)1, (int64_t)a.T * a.H / 304));
+    rows = min(rows, max((int64_t)1, (int64_t)a.T * a.H / (2 * sms)));
     const int hb = (int)min((int64_t)a.H, rows);
     const int tb = (int)max((int64_t)1, min(min(rows / hb, (int64_t)kMaxRows), (int64_t)(kTable / (a.n / 2))));
     const dim3 grid(blocks(a.T, tb), blocks(a.H, hb));
@@ -308,8 +311,13 @@ cudaError_t launch_cache_append(const AppendArgs &a, cudaStream_t stream) {
     const bool vec = aligned(a.rows, a.row_stride * es) && aligned(a.cache, a.D * 2) &&
                      a.D % 8 == 0 && a.off % 8 == 0 && a.n % 16 == 0;
     const int units = a.D / (vec ? 8 : 1);
+    int sms;
+    const cudaError_t e = sm_count(&sms);
+    if (e != cudaSuccess) return e;
+    // rows per block: kPieces units a thread, fewer while that leaves an SM
+    // with less than two blocks
     int rows = max(1, kPieces * kThreads / max(units, 1));
-    rows = min(rows, max(1, a.T / 304));
+    rows = min(rows, max(1, a.T / (2 * sms)));
     int tb = min(rows, kMaxRows);
     if (a.n > 0) tb = max(1, min(tb, kTable / (a.n / 2)));
     const dim3 grid(blocks(a.T, tb));

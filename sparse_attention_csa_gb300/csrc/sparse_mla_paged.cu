@@ -947,7 +947,8 @@ cudaError_t launch_sparse_mla_paged(MlaPagedArgs a, cudaStream_t stream) {
     int sms, dev;
     bool first;
     unsigned long long ctx;
-    cudaError_t e = enter_context(pc, &sms, &first, &ctx, &dev);
+    cudaError_t e = enter_context(pc, &first, &ctx, &dev);
+    if (e == cudaSuccess) e = sm_count(&sms);
     if (e != cudaSuccess) return e;
     if (first) {
         e = cudaFuncSetAttribute(sparse_mla_paged_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
