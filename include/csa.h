@@ -467,8 +467,10 @@ csa_status_t csa_rope_freqs(int32_t rope_dim, double theta, double factor, int32
  *     out_b = mscale (x_b cos theta_i + x_a sin theta_i)
  * inverse != 0 turns by -theta_i: the transpose of the forward map, so that it
  * takes the gradient of out to the gradient of x (and turns an attention
- * output back when the rows it sums were rotated). Computed in fp32 from
- * angles reduced in fp64, rounded once.
+ * output back when the rows it sums were rotated). Angles are reduced as
+ * 64-bit fixed-point fractions of a turn (off by the frequency's rounding in
+ * 64 bits, times p), the factors and the products are fp32, the result is
+ * rounded once.
  * x, out: dtype (CSA_BF16 or CSA_F32); token t starts x_stride (out_stride)
  * elements after token t - 1 and holds [heads, head_dim] contiguously. out may
  * be x itself (with the same stride): only the rotary dims are touched then.

@@ -18,10 +18,14 @@
 // radians), but 64-bit floating point is slow here. So a block turns each
 // frequency once into a fraction of a turn per position in fixed point, in
 // units of 2^-64 turns; p times that, modulo 2^64, is the angle without its
-// whole turns: three integer multiplications, exact but for the frequency's
-// own rounding (2^-65 turns, times p). Its upper 32 bits, as a signed
-// fraction, are half a turn at most and exact to 2^-25 turns as a float, and
-// sincospif gives the factors.
+// whole turns: three integer multiplications that add no error to the
+// frequency's (f / 2 pi is a product in 64 bits with a rounded constant: 2^-52
+// of it, times p, so 2^-34 turns at p = 2^20 and f = 1). Its upper 32 bits, as
+// a signed fraction, are half a turn at most: 24 of them go through sincospif
+// as a float, exactly, and the other 8 turn its result by their own angle,
+// below 2^-22 radians (a float of all 32 would be off by 2^-23.3 radians, as
+// much as sincospif itself: factors up to 2^20 positions were off by up to
+// 1.16e-7, and are by 8.0e-8; no case got slower).
 #include "common.cuh"
 #include "internal.h"
 #include "paged.h"
@@ -44,10 +48,12 @@ __device__ __forceinline__ uint64_t fixed_turns(double f) {
 }
 
 __device__ __forceinline__ float2 cos_sin(int64_t p, uint64_t turns, float sign, float m) {
-    const int32_t frac = (int32_t)(((uint64_t)p * turns) >> 32);
+    const uint32_t frac = (uint32_t)(((uint64_t)p * turns) >> 32);  // of a turn, modulo 1
+    const uint32_t upper = (frac + 128u) & ~255u;
     float s, c;
-    sincospif((float)frac * 0x1p-31f, &s, &c);
-    return make_float2(m * c, m * sign * s);
+    sincospif((float)(int32_t)upper * 0x1p-31f, &s, &c);
+    const float rest = (float)(int32_t)(frac - upper) * (0x1p-31f * 3.14159265f);  // radians
+    return make_float2(m * fmaf(-rest, s, c), m * sign * fmaf(rest, c, s));
 }
 
 // V consecutive elements <-> fp32
