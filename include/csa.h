@@ -531,6 +531,8 @@ csa_status_t csa_cache_append(const void *rows, csa_dtype_t dtype, int64_t row_s
  * that the table holds no page for are recorded and rank last (-inf) where a
  * token is scored; one that sees at most topk rows is not, unless the values
  * are asked for, and selects them all.
+ * As in csa_indexer_topk a product that is NaN counts as 0; a score that is
+ * NaN ranks above all others.
  * csa_indexer_topk_paged_workspace_size: bytes for the scores, 4 for every
  * token and row the table can hold (max_rows = max_pages * page_size).
  * Errors: as csa_indexer_topk (q and k_cache 16-byte aligned, index_dim 64 or

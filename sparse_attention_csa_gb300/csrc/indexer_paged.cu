@@ -355,7 +355,7 @@ indexer_paged_score_kernel(const __grid_constant__ IndexerPagedArgs a) {
                     tc::tc_fence_before();
                     tc::mbar_arrive(&ms->acc_empty[acc]);
                     const int64_t r = (int64_t)j * kTileRows + 32 * warp + lane;
-                    if (r < p.n) out[r] = there ? sum[0] + sum[1] : -INFINITY;
+                    if (r < p.n) out[r] = there ? (sum[0] + sum[1]) + 0.0f : -INFINITY;  // no -0
                 }
                 if (ok) tc::mbar_arrive(&ms->q_empty[np & 1]);
                 ++np;
@@ -411,6 +411,17 @@ __device__ __forceinline__ uint4 peer_u128(const void *p, uint32_t rank) {
                  : "r"(peer_addr(p, rank))
                  : "memory");
     return v;
+}
+
+// A score's rank as an unsigned number, from its bits alone (the score kernel
+// writes no -0, so equal scores have equal keys). A NaN lies at an end of the
+// order, above +inf as the score kernel writes it, and so is the smallest or the
+// largest key: there are no bins then. (float_key adds 0 first, and what the
+// compiler makes of that ranks a NaN below zero, where linear bins would count
+// it among the lowest: more rows written than counted.)
+__device__ __forceinline__ uint32_t row_key(float s) {
+    const uint32_t u = __float_as_uint(s);
+    return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
 
 struct Sel {
@@ -508,7 +519,7 @@ indexer_paged_select_kernel(const __grid_constant__ IndexerPagedArgs a) {
     {
         uint32_t lo = 0xffffffffu, hi = 0u;
         sweep([&](float s) {
-            const uint32_t k = float_key(s);
+            const uint32_t k = row_key(s);
             lo = min(lo, k);
             hi = max(hi, k);
         });
@@ -524,7 +535,8 @@ indexer_paged_select_kernel(const __grid_constant__ IndexerPagedArgs a) {
     const uint32_t hi = __reduce_max_sync(0xffffffffu, gather(&sm.range[1], 0u));
     auto key_float = [](uint32_t k) { return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k); };
     const float fl = key_float(lo), span = key_float(hi) - fl;
-    // no bins without a finite, positive span: all rows are candidates of bin 0
+    // no bins without a finite, positive span (a NaN among the scores makes it
+    // one): all rows are candidates of bin 0
     const float scale = span > 0.0f && span < INFINITY ? (float)(kBins - 1) / span : 0.0f;
     const bool binned = scale > 0.0f && scale < INFINITY;
     auto bin_of = [&](float s) -> uint32_t {
@@ -572,7 +584,7 @@ indexer_paged_select_kernel(const __grid_constant__ IndexerPagedArgs a) {
         sweep([&](float s) {
             const uint32_t b = bin_of(s);
             n_gt += b > bin;
-            if (b == bin) sm.cand[atomicAdd(&sm.n_cand, 1u)] = float_key(s);
+            if (b == bin) sm.cand[atomicAdd(&sm.n_cand, 1u)] = row_key(s);
         });
         n_gt = __reduce_add_sync(0xffffffffu, n_gt);
         if (C > 1 && lane == 0) atomicAdd(&sm.counts[0], n_gt);
@@ -620,7 +632,7 @@ indexer_paged_select_kernel(const __grid_constant__ IndexerPagedArgs a) {
             const int shift = 24 - 8 * pass;
             uint32_t *h = sm.digit[pass & 1];
             sweep([&](float s) {
-                const uint32_t k = float_key(s);
+                const uint32_t k = row_key(s);
                 if (bin_of(s) == bin && (k & mask) == kth) atomicAdd(&h[(k >> shift) & 255u], 1u);
             });
             if (tid < 256) sm.digit[(pass + 1) & 1][tid] = 0;  // read two passes ago
@@ -645,7 +657,7 @@ indexer_paged_select_kernel(const __grid_constant__ IndexerPagedArgs a) {
         if (C > 1) {
             uint32_t n_gt = 0, n_eq = 0;
             sweep([&](float s) {
-                const uint32_t k = float_key(s);
+                const uint32_t k = row_key(s);
                 n_gt += k > kth;
                 n_eq += k == kth;
             });
@@ -672,7 +684,7 @@ indexer_paged_select_kernel(const __grid_constant__ IndexerPagedArgs a) {
             const float v[4] = {held[i].x, held[i].y, held[i].z, held[i].w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const uint32_t k = float_key(v[e]), bit = 1u << (4 * i + e);
+                const uint32_t k = row_key(v[e]), bit = 1u << (4 * i + e);
                 if (r + e < r1 && k > kth) up |= bit;
                 if (r + e < r1 && k == kth) on |= bit;
             }

@@ -62,3 +62,11 @@ def test_waits_of_whole_warps_are_voted():
     assert len(waits) == 4
     for x in waits:
         assert "__all_sync(0xffffffffu, cx.wait(" in x, x
+
+
+def test_selection_ranks_nan_like_it_counts_it():
+    """The selection writes the rows whose key lies above the border's and
+    counts them by linear bins: a NaN has one place in both (its own key, no
+    bins). float_key alone ranks it below zero."""
+    body = kernels("indexer_paged.cu")["indexer_paged_select_kernel"]
+    assert "row_key(" in body and "float_key(" not in body
