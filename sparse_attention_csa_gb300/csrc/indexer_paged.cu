@@ -26,8 +26,13 @@
 // rows are emitted in order by counts over lanes, warps and CTAs. Bound by the
 // latency of its steps: 2 MB read.
 //
-// Both together: one token over 32768 rows 14.2 us; 64 tokens over 0.57 million
-// rows, 146 MB, 39.3 us, the scores alone at 4.5 TB/s under a profiler.
+// The number of CTAs a token, whether they hold their rows, and the workspace
+// follow from what the page table can hold, not from what a token sees: a table
+// much wider than its sequences costs CTAs without rows and, past 65536 rows,
+// sweeps that read the scores again.
+//
+// Both together: one token over 32768 rows 14.4 us; 64 tokens over 0.57 million
+// rows, 146 MB, 39.8 us, the scores alone at 4.5 TB/s under a profiler.
 #include "common.cuh"
 #include "internal.h"
 #include "paged.h"
@@ -635,7 +640,7 @@ indexer_paged_select_kernel(const __grid_constant__ IndexerPagedArgs a) {
                 const uint32_t k = row_key(s);
                 if (bin_of(s) == bin && (k & mask) == kth) atomicAdd(&h[(k >> shift) & 255u], 1u);
             });
-            if (tid < 256) sm.digit[(pass + 1) & 1][tid] = 0;  // read two passes ago
+            if (tid < 256) sm.digit[(pass + 1) & 1][tid] = 0;  // by all, in the pass before
             sync();
             int32_t cnt = 0;
             if (tid < 256)

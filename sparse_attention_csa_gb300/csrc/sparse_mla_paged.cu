@@ -22,22 +22,29 @@
 //     S = Q K^T: heads x keys, K = 512. 64 heads fill half of M = 128, which
 //          costs the tensor core as much as all of it, so the other half of M
 //          takes the heads' dims 256-511 and N = 128 the keys' low and high
-//          dims: 16 MMAs (64 cycles each) in place of 32 (58 each). Of the
-//          four blocks of the result the two matching ones are added; rows of
-//          the low and the high half alternate in groups of 8, so a head's
-//          two partial scores sit 8 lanes apart in one warp. Q is the operand
+//          dims: 16 MMAs in place of 32. Of the four blocks of the result the
+//          two matching ones are added; rows of the low and the high half
+//          alternate in groups of 8, so a head's two partial scores sit 8
+//          lanes apart in one warp. Q is the operand
 //          in tensor memory (128 columns), which leaves shared memory to
 //          three tiles; a token's Q comes through the tiles' stages like one.
 //     O^T += V^T P^T: 4 slabs of 128 dims x 64 heads, K = 64 keys; V is the
-//          K tile's bytes read MN-major.
+//          K tile's bytes read MN-major. P is rounded to bf16, V's type, as in
+//          the packed forward; its sums stay fp32. The output is then off by
+//          up to 2.15e-3 (norm of the error over the norm, normal inputs, 640
+//          keys a token), where rounding the output alone gives 1.66e-3. With
+//          the rounded-off part of P as a second bf16 operand it was 1.66e-3
+//          too, but the products of a tile take half as long again: one token
+//          12.8 -> 13.5 us, 64 tokens 26.4 -> 28.8, 81 drafted 33.2 -> 37.0,
+//          long rows 59.9 -> 70.9. Rounding was kept.
 // Shared memory holds three tiles (192 KB) and two P (16 KB); tensor memory Q
 // (128 columns), S (128) and O^T (256). The scores of the next tile are
 // computed while this one's softmax runs. Rows are gathered by cp.async; their
 // pages are found some tiles ahead by a warp of its own.
 //
 // Bound by HBM with long rows, by the latency of its steps with few tiles a
-// CTA. With 64 heads, join included: one token of 640 keys 13.0 us, 64 of them
-// 26.5 us, six long rows (225 MB read) 60 us or 3.7 TB/s.
+// CTA. With 64 heads, join included: one token of 640 keys 12.8 us, 64 of them
+// 26.4 us, six long rows (225 MB read) 59.9 us or 3.8 TB/s.
 #include "common.cuh"
 #include "internal.h"
 #include "paged.h"
@@ -831,9 +838,9 @@ sparse_mla_paged_kernel(const __grid_constant__ MlaPagedArgs a) {
 // (with more tokens than CTAs: the split token whose first tile CTA x held)
 // and its items y, y + gridDim.y and so on: four heads and 256 ND / P dims, ND
 // dims a thread, P groups of threads sharing the parts (ND = 1). Few blocks,
-// four an SM: they start only as the first kernel's CTAs leave (its registers
-// fill the SM), and a grid of 32 blocks for each CTA, most without work, took
-// 8 us to drain. The first parts' sums are on their way before their factors
+// three (ND = 1) or four an SM: they start only as the first kernel's CTAs
+// leave (its registers fill the SM), and a grid of 32 blocks for each CTA, most
+// without work, took 8 us to drain. The first parts' sums are on their way before their factors
 // are known.
 constexpr int kJoinThreads = 256;
 constexpr int join_blocks(int nd) { return nd == 1 ? 3 : 4; }  // on an SM, by registers
