@@ -504,7 +504,7 @@ csa_status_t csa_rope(const void *x, csa_dtype_t dtype, int64_t x_stride, const 
  * rows [total_rows, width], dtype; row t starts row_stride elements after row
  * t - 1. Padding slots (row_pos < 0) write nothing. No other slot of the cache
  * is touched. Slots named by several rows of one call hold a mixture of them
- * afterwards: keep them distinct.
+ * afterwards: keep them distinct, and rows apart from the cache.
  * Errors: negative sizes, width < 1, page_size < 1, rope_dim negative or odd
  * or outside the row, row_stride < width (with more than one row), row_seq
  * NULL with total_rows > batch -> CSA_ERR_SHAPE; an unknown dtype or layout,

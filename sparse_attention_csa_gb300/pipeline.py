@@ -128,10 +128,16 @@ def csa_layer_decode(q, kv, cache: PagedLayerCache, q_seq, q_pos, sinks, softmax
     rotated at their positions first (q into a new tensor), and with
     ``turn_back`` those of the output are turned back at the token's own
     position. ``q_idx``/``w``/``topk`` given -> INDEXER layer; omitted ->
-    every visible compressed row, or none without ``cache.cmp``. Compressed
-    rows that these tokens complete are the caller's to append before the call
-    (``csa_cache_append`` with the group's number as position and
-    ``pos_stride=cmp_ratio``)."""
+    every visible compressed row, or none without ``cache.cmp``.
+
+    Left to the caller: compressed rows that these tokens complete, appended
+    before the call (``csa_cache_append`` with the group's number as position
+    and ``pos_stride=cmp_ratio``), and with them the raw projections of the
+    unfinished group, and of the one before it for overlapping layers, that
+    ``csa_compress_thd`` makes a row from; the rotation of the indexer's
+    queries and rows (``q_idx`` comes as the indexer takes it); an ``mscale``
+    other than 1 (rotate by ``csa_rope`` and ``csa_cache_append``, and leave
+    ``inv_freq`` and ``kv`` out)."""
     if kv is not None:
         csa_cache_append(kv, q_seq, q_pos, cache.ori_pages, cache.ori, inv_freq=inv_freq,
                          layout=rope_layout)
