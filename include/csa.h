@@ -536,7 +536,9 @@ csa_status_t csa_cache_append(const void *rows, csa_dtype_t dtype, int64_t row_s
  * csa_indexer_topk_paged_workspace_size: bytes for the scores, 4 for every
  * token and row the table can hold (max_rows = max_pages * page_size): 64 MB
  * for 64 tokens and a table of 262144 rows, 8.6 GB for 8192 of them. A long
- * chunk of a prompt is better sent in several calls.
+ * chunk of a prompt is better sent in several calls. Its contents do not matter
+ * before the call and mean nothing after it; calls that may overlap on the GPU
+ * (captured graphs replayed at once, too) need workspaces of their own.
  * Errors: as csa_indexer_topk (q and k_cache 16-byte aligned, index_dim 64 or
  * 128, 1 to 64 heads, cmp_ratio >= 2, topk >= 1), plus page_size < 1,
  * max_pages * page_size above INT32_MAX, q_seq NULL with total_tokens > batch

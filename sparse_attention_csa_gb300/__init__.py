@@ -583,7 +583,7 @@ def csa_rope_freqs(rope_dim: int, theta: float = 10000.0, factor: float = 1.0,
     rope_dim = int(rope_dim)
     half, given = max(rope_dim, 0) // 2, out
     if out is None:
-        device = torch.device(device or "cuda")
+        device = torch.device("cuda" if device is None else device)
         if device.type != "cuda":
             raise TypeError(f"device must be a CUDA device, got {device}")
         dev = torch.cuda.current_device() if device.index is None else device.index

@@ -128,3 +128,20 @@ def test_results_belong_to_the_calls_stream(raw):
         torch.cuda.synchronize()
         for w, e, g in zip(want, early, got):
             assert torch.equal(w, e) and torch.equal(w, g)
+
+
+def test_ways_to_name_a_stream_and_a_device():
+    """The default stream by its handle 0, as an object, or left out; a device
+    by its number."""
+    want = csa.csa_rope_freqs(64)
+    for stream in (0, torch.cuda.default_stream(), torch.cuda.current_stream().cuda_stream, None):
+        for device in (None, 0, "cuda", torch.device("cuda:0")):
+            got = csa.csa_rope_freqs(64, device=device, stream=stream)
+            torch.cuda.synchronize()
+            assert got.device == want.device and torch.equal(got, want)
+    with pytest.raises(TypeError):
+        csa.csa_rope_freqs(64, device="cpu")
+    c, seq, pos = Rows(300), i32([0, 1, 2]), i32([1199, 5, 700])
+    idx = [c.call(seq, pos, stream=s)[0] for s in (None, 0, torch.cuda.default_stream())]
+    torch.cuda.synchronize()
+    assert torch.equal(idx[0], idx[1]) and torch.equal(idx[0], idx[2])
