@@ -31,12 +31,12 @@
 //     O^T += V^T P^T: 4 slabs of 128 dims x 64 heads, K = 64 keys; V is the
 //          K tile's bytes read MN-major. P is rounded to bf16, V's type, as in
 //          the packed forward; its sums stay fp32. The output is then off by
-//          up to 2.15e-3 (norm of the error over the norm, normal inputs, 640
-//          keys a token), where rounding the output alone gives 1.66e-3. With
-//          the rounded-off part of P as a second bf16 operand it was 1.66e-3
-//          too, but the products of a tile take half as long again: one token
-//          12.8 -> 13.5 us, 64 tokens 26.4 -> 28.8, 81 drafted 33.2 -> 37.0,
-//          long rows 59.9 -> 70.9. Rounding was kept.
+//          up to 2.15e-3 (norm of the error over the norm, normal inputs),
+//          where rounding the output alone gives 1.66e-3. With the rounded-off
+//          part of P as a second bf16 operand it was 1.66e-3 too, but that
+//          takes 16 more MMAs a tile: one token 12.8 -> 13.5 us, 64 tokens
+//          26.4 -> 28.8, 81 drafted 33.2 -> 37.0, long rows 59.9 -> 70.9 (68.9
+//          by the MMAs alone). Rounding was kept.
 // Shared memory holds three tiles (192 KB) and two P (16 KB); tensor memory Q
 // (128 columns), S (128) and O^T (256). The scores of the next tile are
 // computed while this one's softmax runs. Rows are gathered by cp.async; their
