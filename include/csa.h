@@ -424,7 +424,9 @@ csa_status_t csa_indexer_topk_noalloc(const csa_bf16_t *q, const csa_bf16_t *k, 
  * r % page_size of pool page pages[b, r / page_size]. Pages may have any size
  * and order, and sequences may share pages they only read. Entries outside
  * [0, num_pages) stand for absent pages: a call that needs one skips its rows
- * and records it in the device error word.
+ * and records it in the device error word. CSA_PAGE_EVICTED stands for a page
+ * given back on purpose (csa_cache_evict writes it): calls that read rows skip
+ * its rows and record nothing.
  *
  * New tokens are rows t of the call's tensors: q_pos[t] (or row_pos[t]) is the
  * token's position in its sequence, from 0, itself included in what it sees,
@@ -436,6 +438,7 @@ csa_status_t csa_indexer_topk_noalloc(const csa_bf16_t *q, const csa_bf16_t *k, 
  */
 typedef enum { CSA_BF16 = 0, CSA_F32 = 1 } csa_dtype_t;
 typedef enum { CSA_ROPE_INTERLEAVED = 0, CSA_ROPE_HALF = 1 } csa_rope_layout_t;
+#define CSA_PAGE_EVICTED INT32_MIN
 
 /*
  * Rotation frequencies in radians per position, inv_freq [rope_dim / 2] fp64:
@@ -603,6 +606,139 @@ csa_status_t csa_sparse_mla_paged(
     const float *sinks, float softmax_scale, int32_t cmp_ratio, int32_t ori_win_left,
     int32_t ori_win_right, csa_bf16_t *out, float *softmax_lse, int32_t return_softmax_lse,
     void *workspace, size_t workspace_bytes, csa_stream_t stream);
+
+/*
+ * Compressed rows held in 4 bits. A row of 512 dims takes 384 bytes in place
+ * of 1024; a 4-bit cache is a pool of pages [num_pages, page_size, 384] with a
+ * table as above. Format of a row:
+ *   bytes   0-223  dims 0-447, 4 bits each: sign (bit 3) and a magnitude code
+ *                  0-7 for 0, 0.5, 1, 1.5, 2, 3, 4, 6. Eight dims make a
+ *                  little-endian 32-bit word: its low half holds dims 0, 2, 4,
+ *                  6 from the lowest bits up, its high half dims 1, 3, 5, 7
+ *   bytes 224-251  an e4m3 scale for each group of 16 dims
+ *   byte  252      e + 127: a power of two 2^e for the whole row (27 to 227)
+ *   bytes 253-255  zero
+ *   bytes 256-383  dims 448-511, the rotary ones, in bf16
+ * A held value is code * scale * 2^e, exact in bf16.
+ *
+ * csa_cache_append_q4 is csa_cache_append into such a cache. Rotary dims have
+ * to lie within the last 64. For a row x, with top_g the largest finite
+ * magnitude of group g:
+ *     e = floor(log2(max_g top_g / 6)) - 7, within [-100, 100]
+ *     scale_g = top_g / 6 / 2^e to e4m3, at most 448 (nearest, ties to even)
+ *     code_d = |x_d| / (scale_g 2^e) to the nearest code, ties to the even one
+ * (top_g / 6 in fp32; everything else as if exact). Equal rows are held in
+ * equal bytes. Groups below 2^-17 of the row's largest vanish; magnitudes above
+ * 2^111 saturate. A group with a value that is not finite reads as NaN.
+ * Errors: as csa_cache_append, and width != 512, rotary dims below 448, cache
+ * not 16-byte aligned -> CSA_ERR_UNSUPPORTED. An evicted page is absent to it.
+ *
+ * csa_cache_read_q4: the held rows row_pos[t] of sequences row_seq[t] (NULL:
+ * row t is sequence t's) as bf16, out [total_rows, 512]. Padding slots
+ * (row_pos < 0) and rows without a page read as zeros; the latter are recorded
+ * unless evicted.
+ * Errors: negative sizes, page_size < 1, row_seq NULL with total_rows > batch
+ * -> CSA_ERR_SHAPE; NULL cache/pages/row_pos/out -> CSA_ERR_NULL; cache or out
+ * not 16-byte aligned -> CSA_ERR_UNSUPPORTED. total_rows == 0 launches nothing.
+ */
+csa_status_t csa_cache_append_q4(const void *rows, csa_dtype_t dtype, int64_t row_stride,
+                                 const int32_t *row_seq, const int32_t *row_pos,
+                                 const int32_t *pages, int32_t batch, int32_t max_pages,
+                                 int32_t num_pages, int32_t page_size, int32_t total_rows,
+                                 int32_t width, const double *inv_freq, int32_t rope_offset,
+                                 int32_t rope_dim, csa_rope_layout_t layout, float mscale,
+                                 int32_t pos_stride, uint8_t *cache, csa_stream_t stream);
+
+csa_status_t csa_cache_read_q4(const uint8_t *cache, const int32_t *pages, const int32_t *row_seq,
+                               const int32_t *row_pos, int32_t batch, int32_t max_pages,
+                               int32_t num_pages, int32_t page_size, int32_t total_rows,
+                               csa_bf16_t *out, csa_stream_t stream);
+
+/*
+ * csa_sparse_mla_paged with the compressed rows held in 4 bits: cmp_cache
+ * [cmp_num_pages, cmp_page_size, 384]. The window rows stay bf16. The attention
+ * is that over the held values; arguments, workspace and errors are the same.
+ */
+csa_status_t csa_sparse_mla_paged_q4(
+    const csa_bf16_t *q, const csa_bf16_t *ori_cache, const uint8_t *cmp_cache,
+    const int32_t *cmp_sparse_indices, const int32_t *ori_pages, const int32_t *cmp_pages,
+    const int32_t *q_seq, const int32_t *q_pos, int32_t batch, int32_t total_tokens, int32_t heads,
+    int32_t head_dim, int32_t ori_num_pages, int32_t ori_page_size, int32_t ori_max_pages,
+    int32_t cmp_num_pages, int32_t cmp_page_size, int32_t cmp_max_pages, int32_t topk,
+    const float *sinks, float softmax_scale, int32_t cmp_ratio, int32_t ori_win_left,
+    int32_t ori_win_right, csa_bf16_t *out, float *softmax_lse, int32_t return_softmax_lse,
+    void *workspace, size_t workspace_bytes, csa_stream_t stream);
+
+/*
+ * The attention weight that cached compressed rows received, added up:
+ *     out[b, j] = mass[b, j] + sum over the tokens t of sequence b that attend
+ *         compressed row j, and their heads h, of e^(scale q[t,h].k_j - lse[t,h])
+ * with q, lists, tables and softmax_lse [T, H] those of the attention call
+ * (csa_sparse_mla_paged, csa_sparse_mla_paged_q4) and cmp_cache in `format`.
+ * Rows are those of the sequence: mass, out [batch, max_pages * page_size]
+ * fp32; mass NULL counts as zeros, out may be mass itself. Rows that received
+ * nothing keep mass's bits. A row listed twice counts twice; entries that are
+ * negative or not visible count nothing, and neither do rows without a page
+ * (recorded unless evicted) and heads whose lse is -inf. A row's weight from
+ * one token that is NaN counts as 0, one above the number of heads (an lse
+ * that is not this attention's) as that number. Sums do not depend on the
+ * order of the tokens' work: equal calls give equal bits.
+ * workspace: csa_attn_mass_paged_workspace_size(total_tokens, topk with
+ * cmp_sparse_indices, else max_pages * page_size) bytes, 256-byte aligned; its
+ * contents do not matter before the call and mean nothing after it, and calls
+ * that may overlap on the GPU need workspaces of their own.
+ * Errors: negative sizes, heads < 1, page_size < 1, max_pages * page_size
+ * above INT32_MAX, topk < 1 with cmp_sparse_indices, q_seq NULL with
+ * total_tokens > batch -> CSA_ERR_SHAPE; head_dim != 512, heads > 64,
+ * cmp_ratio < 2, total_tokens or batch > 65535, an unknown format, a list (or,
+ * without one, a table) of more than 2^27 rows, q or cmp_cache not 16-byte
+ * aligned, out overlapping mass without being mass -> CSA_ERR_UNSUPPORTED;
+ * NULL out, or with tokens q/softmax_lse/cmp_cache/cmp_pages/q_pos ->
+ * CSA_ERR_NULL; a short or misaligned workspace -> CSA_ERR_WORKSPACE. No
+ * sequence or no page launches nothing; without tokens out receives mass.
+ */
+typedef enum { CSA_ROWS_BF16 = 0, CSA_ROWS_Q4 = 1 } csa_rows_t;
+
+size_t csa_attn_mass_paged_workspace_size(int32_t total_tokens, int32_t slots);
+
+csa_status_t csa_attn_mass_paged(const csa_bf16_t *q, const float *softmax_lse,
+                                 const void *cmp_cache, csa_rows_t format,
+                                 const int32_t *cmp_sparse_indices, const int32_t *cmp_pages,
+                                 const int32_t *q_seq, const int32_t *q_pos, int32_t batch,
+                                 int32_t total_tokens, int32_t heads, int32_t head_dim,
+                                 int32_t num_pages, int32_t page_size, int32_t max_pages,
+                                 int32_t topk, float softmax_scale, int32_t cmp_ratio,
+                                 const float *mass, float *out, void *workspace,
+                                 size_t workspace_bytes, csa_stream_t stream);
+
+/*
+ * Pages of cached rows to give back, by the weight their rows received. Of
+ * sequence b, rows [0, rows[b]) are in use (a negative number: none). The pages
+ * it holds of them (table entries >= 0) that contain one of the first
+ * keep_first or the last keep_last rows, and a last page that is not full yet,
+ * stay. Of the others those with the largest sum of mass over their rows in
+ * use stay, the lower page among equal sums, until keep_pages pages are held
+ * with the former; the rest are given back: pages_out has CSA_PAGE_EVICTED in
+ * their place, freed[b] lists their pool pages in the table's order (-1 padded)
+ * and n_freed[b] is their number. Other entries are copied. Sums are formed in
+ * 64 bits; one that is NaN ranks above all.
+ * mass [batch, max_pages * page_size] fp32 (csa_attn_mass_paged), pages,
+ * pages_out, freed [batch, max_pages], rows, n_freed [batch] int32; pages_out
+ * may be pages itself, freed and n_freed may be NULL. A page that several
+ * sequences share is listed by each that gives it back: counting who still
+ * holds it is the caller's. The indexer ranks an evicted page's rows last, the
+ * attention skips them.
+ * Errors: negative sizes, page_size < 1, max_pages * page_size above INT32_MAX
+ * -> CSA_ERR_SHAPE; max_pages > 24576, mass not aligned to its element,
+ * pages_out overlapping pages without being pages, freed overlapping either ->
+ * CSA_ERR_UNSUPPORTED; NULL mass/pages/rows/pages_out -> CSA_ERR_NULL. rows[b]
+ * beyond the table is cut to it and recorded. batch == 0 launches nothing.
+ */
+csa_status_t csa_cache_evict(const float *mass, const int32_t *pages, const int32_t *rows,
+                             int32_t batch, int32_t max_pages, int32_t page_size,
+                             int32_t keep_pages, int32_t keep_first, int32_t keep_last,
+                             int32_t *pages_out, int32_t *freed, int32_t *n_freed,
+                             csa_stream_t stream);
 
 /*
  * Synchronises `stream`, then returns and clears the device error word of the

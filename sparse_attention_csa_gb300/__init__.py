@@ -35,7 +35,9 @@ __all__ = [
     "csa_bsnd_indexer_workspace_size", "csa_indexer_topk_bsnd", "csa_compress_thd",
     "csa_rope_freqs", "csa_rope", "csa_cache_append", "csa_indexer_topk_paged_workspace_size",
     "csa_indexer_topk_paged", "csa_sparse_mla_paged_workspace_size", "csa_sparse_mla_paged",
-    "csa_set_wait_limit_ns", "csa_set_pair_select_rows", "EXPORTED_SYMBOLS",
+    "csa_cache_append_q4", "csa_cache_read_q4", "csa_sparse_mla_paged_q4",
+    "csa_attn_mass_paged_workspace_size", "csa_attn_mass_paged", "csa_cache_evict",
+    "CSA_PAGE_EVICTED", "csa_set_wait_limit_ns", "csa_set_pair_select_rows", "EXPORTED_SYMBOLS",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -50,8 +52,13 @@ EXPORTED_SYMBOLS = (
     "csa_bsnd_indexer_workspace_size", "csa_indexer_topk_bsnd", "csa_compress_thd",
     "csa_rope_freqs", "csa_rope", "csa_cache_append", "csa_indexer_topk_paged_workspace_size",
     "csa_indexer_topk_paged", "csa_sparse_mla_paged_workspace_size", "csa_sparse_mla_paged",
+    "csa_cache_append_q4", "csa_cache_read_q4", "csa_sparse_mla_paged_q4",
+    "csa_attn_mass_paged_workspace_size", "csa_attn_mass_paged", "csa_cache_evict",
     "csa_set_wait_limit_ns", "csa_set_pair_select_rows",
 )
+
+# A page table's entry for a page given back on purpose (csa_cache_evict).
+CSA_PAGE_EVICTED = -2 ** 31
 
 _STATUS = {0: "CSA_OK", 1: "CSA_ERR_NULL", 2: "CSA_ERR_SHAPE", 3: "CSA_ERR_UNSUPPORTED",
            4: "CSA_ERR_WORKSPACE", 5: "CSA_ERR_CUDA", 6: "CSA_ERR_DEVICE_CHECK",
@@ -121,6 +128,14 @@ def lib():
         L.csa_sparse_mla_paged_workspace_size.argtypes = [_i32, _i32]
         L.csa_sparse_mla_paged.argtypes = [_vp] * 8 + [_i32] * 11 + [_vp, _f32, _i32, _i32, _i32,
                                                                      _vp, _vp, _i32, _vp, _sz, _vp]
+        L.csa_cache_append_q4.argtypes = L.csa_cache_append.argtypes
+        L.csa_cache_read_q4.argtypes = [_vp] * 4 + [_i32] * 5 + [_vp, _vp]
+        L.csa_sparse_mla_paged_q4.argtypes = L.csa_sparse_mla_paged.argtypes
+        L.csa_attn_mass_paged_workspace_size.restype = _sz
+        L.csa_attn_mass_paged_workspace_size.argtypes = [_i32, _i32]
+        L.csa_attn_mass_paged.argtypes = [_vp, _vp, _vp, C.c_int] + [_vp] * 4 + [_i32] * 8 + [
+            _f32, _i32, _vp, _vp, _vp, _sz, _vp]
+        L.csa_cache_evict.argtypes = [_vp] * 3 + [_i32] * 6 + [_vp] * 4
         L.csa_set_wait_limit_ns.argtypes = [C.c_uint64]
         L.csa_set_pair_select_rows.argtypes = [_i32]
         for name in ("csa_compress_cu_seqlens", "csa_window_idx", "csa_indexer_topk",
@@ -128,7 +143,9 @@ def lib():
                      "csa_indexer_topk_noalloc", "csa_indexer_kl_loss_grad",
                      "csa_sparse_mla_fwd_bsnd", "csa_indexer_topk_bsnd", "csa_compress_thd",
                      "csa_rope_freqs", "csa_rope", "csa_cache_append", "csa_indexer_topk_paged",
-                     "csa_sparse_mla_paged", "csa_set_wait_limit_ns", "csa_set_pair_select_rows"):
+                     "csa_sparse_mla_paged", "csa_cache_append_q4", "csa_cache_read_q4",
+                     "csa_sparse_mla_paged_q4", "csa_attn_mass_paged", "csa_cache_evict",
+                     "csa_set_wait_limit_ns", "csa_set_pair_select_rows"):
             getattr(L, name).restype = C.c_int
         _lib = L
     return _lib
@@ -714,18 +731,11 @@ def csa_sparse_mla_paged_workspace_size(total_tokens, heads) -> int:
     return lib().csa_sparse_mla_paged_workspace_size(int(total_tokens), int(heads))
 
 
-def csa_sparse_mla_paged(q, ori_cache, cmp_cache, cmp_sparse_indices, ori_pages, cmp_pages, q_seq,
-                         q_pos, sinks, softmax_scale: float, cmp_ratio: int, ori_win_left: int,
-                         ori_win_right: int = 0, return_softmax_lse: bool = False,
-                         workspace=None, out=None, lse=None, stream=None):
-    """Sparse MLA attention of new tokens q [T, H, 512] at positions ``q_pos``
-    [T] (negative: padding) of sequences ``q_seq`` [T] (None: token t is
-    sequence t's) over the window rows of ``ori_cache`` [pages, page_size,
-    512] and the rows of ``cmp_cache`` listed in ``cmp_sparse_indices`` [T,
-    topk] (rows of the sequence; None: every visible row), each with its page
-    table [batch, max_pages]. ``cmp_cache`` None: window only.
-
-    Returns ``(out [T, H, 512], lse [T, H] or None)``."""
+def _mla_paged(where, row_dtype, row_width, q, ori_cache, cmp_cache, cmp_sparse_indices, ori_pages,
+               cmp_pages, q_seq, q_pos, sinks, softmax_scale, cmp_ratio, ori_win_left, ori_win_right,
+               return_softmax_lse, workspace, out, lse, stream):
+    """The calls of both forms of compressed rows, `row_width` elements of
+    `row_dtype` each."""
     T, H, D = _dims(q, "q", 3)
     ori_n, ori_page, _ = _dims(ori_cache, "ori_cache", 3)
     batch, ori_max = _dims(ori_pages, "ori_pages", 2)
@@ -742,7 +752,7 @@ def csa_sparse_mla_paged(q, ori_cache, cmp_cache, cmp_sparse_indices, ori_pages,
         lse = None
     _match(dev, (q, "q", torch.bfloat16, (T, H, D)),
            (ori_cache, "ori_cache", torch.bfloat16, (ori_n, ori_page, D)),
-           (cmp_cache, "cmp_cache", torch.bfloat16, (cmp_n, cmp_page, D)),
+           (cmp_cache, "cmp_cache", row_dtype, (cmp_n, cmp_page, row_width or D)),
            (cmp_sparse_indices, "cmp_sparse_indices", torch.int32, (T, topk)),
            (ori_pages, "ori_pages", torch.int32, (batch, ori_max)),
            (cmp_pages, "cmp_pages", torch.int32, (batch, cmp_max)),
@@ -756,13 +766,169 @@ def csa_sparse_mla_paged(q, ori_cache, cmp_cache, cmp_sparse_indices, ori_pages,
         lse = _new((T, H), torch.float32, dev, stream)
     workspace, ws_bytes = _scratch(workspace, dev, stream,
                                    csa_sparse_mla_paged_workspace_size, T, H)
-    _launch(dev, "csa_sparse_mla_paged", stream, q.data_ptr(), ori_cache.data_ptr(),
+    _launch(dev, where, stream, q.data_ptr(), ori_cache.data_ptr(),
             _addr(cmp_cache), _addr(cmp_sparse_indices), ori_pages.data_ptr(), _addr(cmp_pages),
             _addr(q_seq), _addr(q_pos), batch, T, H, D, ori_n, ori_page, ori_max, cmp_n, cmp_page,
             cmp_max, topk, _addr(sinks), softmax_scale, cmp_ratio, ori_win_left, ori_win_right,
             out.data_ptr(), _addr(lse), 1 if return_softmax_lse else 0, _addr(workspace), ws_bytes)
     _written(*given)
     return out, lse
+
+
+def csa_sparse_mla_paged(q, ori_cache, cmp_cache, cmp_sparse_indices, ori_pages, cmp_pages, q_seq,
+                         q_pos, sinks, softmax_scale: float, cmp_ratio: int, ori_win_left: int,
+                         ori_win_right: int = 0, return_softmax_lse: bool = False,
+                         workspace=None, out=None, lse=None, stream=None):
+    """Sparse MLA attention of new tokens q [T, H, 512] at positions ``q_pos``
+    [T] (negative: padding) of sequences ``q_seq`` [T] (None: token t is
+    sequence t's) over the window rows of ``ori_cache`` [pages, page_size,
+    512] and the rows of ``cmp_cache`` listed in ``cmp_sparse_indices`` [T,
+    topk] (rows of the sequence; None: every visible row), each with its page
+    table [batch, max_pages]. ``cmp_cache`` None: window only.
+
+    Returns ``(out [T, H, 512], lse [T, H] or None)``."""
+    return _mla_paged("csa_sparse_mla_paged", torch.bfloat16, None, q, ori_cache, cmp_cache,
+                      cmp_sparse_indices, ori_pages, cmp_pages, q_seq, q_pos, sinks, softmax_scale,
+                      cmp_ratio, ori_win_left, ori_win_right, return_softmax_lse, workspace, out,
+                      lse, stream)
+
+
+def csa_sparse_mla_paged_q4(q, ori_cache, cmp_cache, cmp_sparse_indices, ori_pages, cmp_pages,
+                            q_seq, q_pos, sinks, softmax_scale: float, cmp_ratio: int,
+                            ori_win_left: int, ori_win_right: int = 0,
+                            return_softmax_lse: bool = False, workspace=None, out=None, lse=None,
+                            stream=None):
+    """As :func:`csa_sparse_mla_paged`, the compressed rows held in 4 bits:
+    ``cmp_cache`` [pages, page_size, 384] uint8, as :func:`csa_cache_append_q4`
+    leaves it. The window rows ``ori_cache`` stay bf16.
+
+    Returns ``(out [T, H, 512], lse [T, H] or None)``."""
+    return _mla_paged("csa_sparse_mla_paged_q4", torch.uint8, 384, q, ori_cache, cmp_cache,
+                      cmp_sparse_indices, ori_pages, cmp_pages, q_seq, q_pos, sinks, softmax_scale,
+                      cmp_ratio, ori_win_left, ori_win_right, return_softmax_lse, workspace, out,
+                      lse, stream)
+
+
+def csa_cache_append_q4(rows, row_seq, row_pos, pages, cache, inv_freq=None, rope_offset=None,
+                        layout: str = "interleaved", mscale: float = 1.0, pos_stride: int = 1,
+                        stream=None):
+    """:func:`csa_cache_append` of 512-wide rows into a cache that holds them in
+    4 bits: ``cache`` [num_pages, page_size, 384] uint8. Dims 0-447 are held as
+    4-bit codes with a scale for each 16, the last 64 in bf16; the rotary dims
+    have to lie within these. Returns cache."""
+    code = _rows(rows, "rows", (2,))
+    dev = rows.get_device()
+    T, width = rows.shape
+    n_pages, page, _ = _dims(cache, "cache", 3)
+    batch, max_pages = _dims(pages, "pages", 2)
+    half = 0 if inv_freq is None else _dims(inv_freq, "inv_freq", 1)[0]
+    _match(dev, (row_seq, "row_seq", torch.int32, (T,)), (row_pos, "row_pos", torch.int32, (T,)),
+           (pages, "pages", torch.int32, (batch, max_pages)),
+           (cache, "cache", torch.uint8, (n_pages, page, 384)),
+           (inv_freq, "inv_freq", torch.float64, (half,)))
+    _launch(dev, "csa_cache_append_q4", stream, rows.data_ptr(), code, rows.stride(0),
+            _addr(row_seq), _addr(row_pos), pages.data_ptr(), batch, max_pages, n_pages, page, T,
+            width, _addr(inv_freq), width - 2 * half if rope_offset is None else rope_offset,
+            2 * half, _layout(layout), mscale, pos_stride, cache.data_ptr())
+    _written(cache)
+    return cache
+
+
+def csa_cache_read_q4(cache, pages, row_seq, row_pos, out=None, stream=None):
+    """The rows at positions ``row_pos`` [T] of sequences ``row_seq`` [T] (None:
+    row t is sequence t's) of a 4-bit ``cache`` with table ``pages``, as bf16
+    [T, 512]. A negative position, and a row without a page, reads as zeros."""
+    n_pages, page, _ = _dims(cache, "cache", 3)
+    batch, max_pages = _dims(pages, "pages", 2)
+    T = _dims(row_pos, "row_pos", 1)[0]
+    dev = cache.get_device()
+    _match(dev, (cache, "cache", torch.uint8, (n_pages, page, 384)),
+           (pages, "pages", torch.int32, (batch, max_pages)), (row_seq, "row_seq", torch.int32, (T,)),
+           (row_pos, "row_pos", torch.int32, (T,)), (out, "out", torch.bfloat16, (T, 512)))
+    given = out
+    if out is None:
+        out = _new((T, 512), torch.bfloat16, dev, stream)
+    _launch(dev, "csa_cache_read_q4", stream, cache.data_ptr(), pages.data_ptr(), _addr(row_seq),
+            row_pos.data_ptr(), batch, max_pages, n_pages, page, T, out.data_ptr())
+    _written(given)
+    return out
+
+
+def csa_attn_mass_paged_workspace_size(total_tokens, slots) -> int:
+    return lib().csa_attn_mass_paged_workspace_size(int(total_tokens), int(slots))
+
+
+def csa_attn_mass_paged(q, softmax_lse, cmp_cache, cmp_sparse_indices, cmp_pages, q_seq, q_pos,
+                        mass, softmax_scale: float, cmp_ratio: int, out=None, workspace=None,
+                        stream=None):
+    """The attention weight that the compressed rows of each sequence received
+    from new tokens, heads summed, added to ``mass`` [batch, max_pages *
+    page_size] fp32 (None: zeros). q [T, H, 512], lists, table and ``softmax_lse``
+    [T, H] are those of the attention call; ``cmp_cache`` is its cache, bf16
+    [pages, page_size, 512] or 4-bit [pages, page_size, 384] uint8.
+
+    ``out`` may be ``mass`` (None: a new tensor). Returns out."""
+    T, H, D = _dims(q, "q", 3)
+    n_pages, page, width = _dims(cmp_cache, "cmp_cache", 3)
+    batch, max_pages = _dims(cmp_pages, "cmp_pages", 2)
+    dev = q.get_device()
+    q4 = cmp_cache.dtype is torch.uint8
+    topk = 0 if cmp_sparse_indices is None else _dims(cmp_sparse_indices, "cmp_sparse_indices", 2)[1]
+    shape = (batch, max_pages * page)
+    _match(dev, (q, "q", torch.bfloat16, (T, H, D)),
+           (softmax_lse, "softmax_lse", torch.float32, (T, H)),
+           (cmp_cache, "cmp_cache", torch.uint8 if q4 else torch.bfloat16,
+            (n_pages, page, 384 if q4 else D)),
+           (cmp_sparse_indices, "cmp_sparse_indices", torch.int32, (T, topk)),
+           (cmp_pages, "cmp_pages", torch.int32, (batch, max_pages)),
+           (q_seq, "q_seq", torch.int32, (T,)), (q_pos, "q_pos", torch.int32, (T,)),
+           (mass, "mass", torch.float32, shape), (out, "out", torch.float32, shape))
+    given = out
+    if out is None:
+        out = _new(shape, torch.float32, dev, stream)
+    workspace, ws_bytes = _scratch(workspace, dev, stream, csa_attn_mass_paged_workspace_size, T,
+                                   min(max_pages * page if cmp_sparse_indices is None else topk,
+                                       2 ** 31 - 1))
+    _launch(dev, "csa_attn_mass_paged", stream, q.data_ptr(), _addr(softmax_lse),
+            cmp_cache.data_ptr(), 1 if q4 else 0, _addr(cmp_sparse_indices), cmp_pages.data_ptr(),
+            _addr(q_seq), _addr(q_pos), batch, T, H, D, n_pages, page, max_pages, topk,
+            softmax_scale, cmp_ratio, _addr(mass), out.data_ptr(), _addr(workspace), ws_bytes)
+    _written(given)
+    return out
+
+
+def csa_cache_evict(mass, pages, rows, keep_pages: int, keep_first: int = 0, keep_last: int = 0,
+                    out=None, freed=None, n_freed=None, stream=None):
+    """Pages to give back: of the pages that hold rows [0, ``rows[b]``) of
+    sequence b (``rows`` [batch] int32), those with the first ``keep_first`` or
+    the last ``keep_last`` rows or room for more stay, and of the others the
+    ones with the largest sums of ``mass`` [batch, max_pages * page_size], up to
+    ``keep_pages`` in all.
+
+    Returns ``(out [batch, max_pages] the table with CSA_PAGE_EVICTED for pages
+    given back, freed [batch, max_pages] their pool pages, -1 padded, n_freed
+    [batch])``; ``out`` may be ``pages``."""
+    batch, max_pages = _dims(pages, "pages", 2)
+    max_rows = _dims(mass, "mass", 2)[1]
+    dev = pages.get_device()
+    page = max_rows // max_pages if max_pages else 1
+    shape = (batch, max_pages)
+    _match(dev, (pages, "pages", torch.int32, shape),
+           (mass, "mass", torch.float32, (batch, max_pages * page)),
+           (rows, "rows", torch.int32, (batch,)), (out, "out", torch.int32, shape),
+           (freed, "freed", torch.int32, shape), (n_freed, "n_freed", torch.int32, (batch,)))
+    given = out, freed, n_freed
+    if out is None:
+        out = _new(shape, torch.int32, dev, stream)
+    if freed is None:
+        freed = _new(shape, torch.int32, dev, stream)
+    if n_freed is None:
+        n_freed = _new((batch,), torch.int32, dev, stream)
+    _launch(dev, "csa_cache_evict", stream, mass.data_ptr(), pages.data_ptr(), _addr(rows), batch,
+            max_pages, page, keep_pages, keep_first, keep_last, out.data_ptr(), freed.data_ptr(),
+            n_freed.data_ptr())
+    _written(*given)
+    return out, freed, n_freed
 
 
 def csa_device_error(stream=None):

@@ -31,6 +31,9 @@ enum KernelId : int32_t {
     kKerAppend = 10,
     kKerIndexerPaged = 11,
     kKerMlaPaged = 12,
+    kKerCacheQ4 = 13,
+    kKerMass = 14,
+    kKerEvict = 15,
 };
 
 __device__ __forceinline__ void report_error(int32_t *err, int32_t kind, int32_t kernel,

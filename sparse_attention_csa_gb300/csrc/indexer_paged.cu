@@ -294,7 +294,7 @@ indexer_paged_score_kernel(const __grid_constant__ IndexerPagedArgs a) {
                     if (in >= 0) {
                         if ((uint32_t)page < (uint32_t)a.k.num_pages)
                             mine = a.k.base + ((int64_t)page * a.k.page_size + in) * DI;
-                        else
+                        else if (page != CSA_PAGE_EVICTED)
                             report_error(a.err, kErrCheck, kKerIndexerPaged, 3);
                     }
                     const uint32_t m = __ballot_sync(0xffffffffu, mine != nullptr);

@@ -136,6 +136,66 @@ struct MlaPagedArgs {
 
 size_t mla_paged_workspace_bytes(int32_t T, int32_t H);
 cudaError_t launch_sparse_mla_paged(MlaPagedArgs a, cudaStream_t stream);
+// cmp.base then points at rows of 384 bytes (q4.cuh)
+cudaError_t launch_sparse_mla_paged_q4(MlaPagedArgs a, cudaStream_t stream);
+
+constexpr int32_t kQ4Dims = 448;  // dims of a 512-wide row held in 4 bits (q4.cuh)
+
+struct Q4RowsArgs {
+    const void *rows;        // append: [T, 512], row stride row_stride
+    __nv_bfloat16 *out;      // read: [T, 512]
+    const int32_t *row_seq;  // [T] or nullptr (row t belongs to sequence t)
+    const int32_t *row_pos;  // [T], negative: skipped (read: zeros)
+    const int32_t *pages;    // [batch, max_pages]
+    const double *inv_freq;  // [n / 2] or nullptr (n = 0)
+    uint8_t *cache;          // [num_pages, page_size, 384]
+    int32_t *err;
+    int64_t row_stride;
+    int32_t T, off, n, pos_stride;  // rotary dims [off, off + n), within the last 64
+    int32_t batch, max_pages, num_pages, page_size;
+    int32_t f32, half;
+    float mscale;
+};
+
+cudaError_t launch_cache_append_q4(const Q4RowsArgs &a, cudaStream_t stream);
+cudaError_t launch_cache_read_q4(const Q4RowsArgs &a, cudaStream_t stream);
+
+struct MassArgs {
+    const __nv_bfloat16 *q;  // [T, H, 512]
+    const float *lse;        // [T, H]
+    PagedRows cmp;           // 512 wide, or (q4) 384 bytes a row
+    const int32_t *idx;      // [T, topk] or nullptr (every visible row)
+    const int32_t *q_seq;    // [T] or nullptr
+    const int32_t *q_pos;    // [T]
+    const float *mass;       // [batch, max_rows] or nullptr (zeros)
+    float *out;              // [batch, max_rows], may be mass
+    float *weights;          // workspace: [T, slot_pad]
+    int32_t *err;
+    int64_t slot_pad;
+    int32_t T, H, batch, topk, cmp_ratio, max_rows, q4;
+    float softmax_scale;
+    float fixed;             // fixed-point units of a weight of 1: a power of two
+    uint64_t wait_ns;
+};
+
+int64_t mass_slot_pad(int64_t slots);
+size_t mass_workspace_bytes(int32_t T, int64_t slots);
+cudaError_t launch_attn_mass(MassArgs a, cudaStream_t stream);
+
+constexpr int32_t kEvictMaxPages = 24576;  // a sequence's sums in shared memory
+
+struct EvictArgs {
+    const float *mass;     // [batch, max_pages * page_size]
+    const int32_t *pages;  // [batch, max_pages]
+    const int32_t *rows;   // [batch] rows in use
+    int32_t *out;          // [batch, max_pages], may be pages
+    int32_t *freed;        // [batch, max_pages] or nullptr
+    int32_t *n_freed;      // [batch] or nullptr
+    int32_t *err;
+    int32_t batch, max_pages, page_size, keep_pages, keep_first, keep_last;
+};
+
+cudaError_t launch_cache_evict(const EvictArgs &a, cudaStream_t stream);
 
 #ifdef __CUDACC__
 // Row of the pool (in rows) holding logical row r of sequence b, or -1 when

@@ -1,0 +1,87 @@
+// Rows of 512 dims held in 384 bytes: the format and its arithmetic.
+//
+//   bytes   0-223  dims 0-447, 4 bits each: sign, two exponent bits, one bit
+//                  of mantissa (magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6)
+//   bytes 224-251  an e4m3 scale for each group of 16 dims
+//   byte  252      a power of two for the whole row, exponent + 127 (27 to 227)
+//   bytes 253-255  zero
+//   bytes 256-383  dims 448-511, the rotary ones, in bf16
+//
+// Eight dims make a 32-bit word: its low half holds dims 0, 2, 4, 6 from the
+// lowest bits up, its high half dims 1, 3, 5, 7, so that one shift brings two
+// neighbours to the same place of both halves, where bf16 has its bits.
+//
+// A held value is code x scale x 2^e: two, four and one significant bits, so
+// it is exact in bf16 (and the products below are). The row's power of two puts
+// its largest scale between 128 and 256 of e4m3's 448; groups down to 2^-17 of
+// the largest keep a scale of their own. A code of 0 to 3 and a sign alone are
+// a bf16 number 2^126 below the code's value, subnormal ones (0.5) included,
+// and one multiplication brings it up.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace csa {
+namespace q4 {
+
+constexpr int kRow = 384;       // bytes
+constexpr int kDims = 448;      // in 4 bits
+constexpr int kGroup = 16;
+constexpr int kScales = 224;    // first byte of the scales
+constexpr int kExp = 252;
+constexpr int kTail = 256;      // first byte of dims 448-511
+constexpr int kMinExp = -100, kMaxExp = 100;
+
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+// Scale of a group as both halves of a bf16 pair; `unit` is the row's power of two.
+__device__ __forceinline__ __nv_bfloat162 scale_pair(float scale, float unit) {
+    return __float2bfloat162_rn(scale * unit);
+}
+
+// Two e4m3 scales (of neighbouring groups) as floats.
+__device__ __forceinline__ float2 scales2(uint16_t two) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(two, __NV_E4M3);
+    return __half22float2(*reinterpret_cast<const __half2 *>(&h));
+}
+
+// Eight codes times their group's scale: four pairs of neighbouring dims.
+__device__ __forceinline__ uint4 eight(uint32_t w, __nv_bfloat162 scale) {
+    const uint32_t bits[4] = {
+        ((w << 6) & 0x01c001c0u) | ((w << 12) & 0x80008000u),
+        ((w << 2) & 0x01c001c0u) | ((w << 8) & 0x80008000u),
+        ((w >> 2) & 0x01c001c0u) | ((w << 4) & 0x80008000u),
+        ((w >> 6) & 0x01c001c0u) | (w & 0x80008000u)};
+    uint32_t out[4];
+    const uint32_t up = 0x7e807e80u;  // 2^126 twice
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 v = __hmul2(__hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&bits[i]),
+                                                 *reinterpret_cast<const __nv_bfloat162 *>(&up)),
+                                         scale);
+        out[i] = *reinterpret_cast<const uint32_t *>(&v);
+    }
+    return make_uint4(out[0], out[1], out[2], out[3]);
+}
+
+// Dims 16 i .. 16 i + 15 of a row (i of 32) as bf16 pairs.
+__device__ __forceinline__ void sixteen(const uint8_t *row, int i, uint4 (&v)[2]) {
+    if (i < kDims / kGroup) {
+        const uint2 w = __ldg(reinterpret_cast<const uint2 *>(row) + i);
+        const float unit = pow2((int)__ldg(row + kExp) - 127);
+        const __nv_bfloat162 s = scale_pair(scales2(__ldg(row + kScales + i)).x, unit);
+        v[0] = eight(w.x, s);
+        v[1] = eight(w.y, s);
+    } else {
+        const uint4 *p = reinterpret_cast<const uint4 *>(row + kTail) + 2 * (i - kDims / kGroup);
+        v[0] = __ldg(p);
+        v[1] = __ldg(p + 1);
+    }
+}
+
+}  // namespace q4
+}  // namespace csa
