@@ -48,6 +48,7 @@
 #include "common.cuh"
 #include "internal.h"
 #include "paged.h"
+#include "q4.cuh"
 #include "tc_ptx.cuh"
 
 namespace csa {
@@ -56,10 +57,6 @@ namespace {
 
 constexpr int kTile = 64;
 constexpr int kMaxGrid = 160;     // CTAs of the persistent grid (sizes the workspace)
-constexpr int kThreads = 384;     // 8 softmax and epilogue warps, 2 loaders, 1 MMA, 1 look-up
-constexpr int kLoaders = 64;
-constexpr int kMmaWarp = 10;
-constexpr int kFindWarp = 11;
 constexpr int kRing = 4;          // tiles whose rows are found ahead of the loaders
 constexpr int kPieces = 64;       // pieces of a run described in shared memory at a time
 constexpr float kLazyMax = 8.0f;  // base-2 units
@@ -67,10 +64,25 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
 // shared memory map (offsets from a 1024-byte aligned base)
-constexpr int kStages = 3;
 constexpr uint32_t kStage = 65536;  // 4 dim groups x 8 x [low, high] x [8 keys x 128 B]
-constexpr uint32_t kOffP = kStages * kStage;  // 2 x [64 heads x 64 keys] bf16, K-major
-constexpr uint32_t kOffMisc = kOffP + 16384;
+constexpr uint32_t kRawTile = kTile * q4::kRow;  // rows as they are, each line of 128 bytes swizzled
+
+constexpr int kLoaders = 64;
+constexpr int kMmaWarp = 10;
+constexpr int kFindWarp = 11;
+
+// Both forms of compressed rows: Q4 false, bf16; true, 4 bits.
+template <bool Q4>
+struct Form {
+    // 8 softmax and epilogue warps, 2 loaders, 1 MMA, 1 look-up, and 8 that turn 4-bit rows into bf16
+    static constexpr int kSpreadWarps = Q4 ? 8 : 0;
+    static constexpr int kThreads = 384 + 32 * kSpreadWarps;
+    static constexpr int kStages = Q4 ? 2 : 3;  // tiles in bf16
+    static constexpr int kRaw = Q4 ? 3 : 0;     // tiles of 4-bit rows on their way
+    static constexpr uint32_t kOffP = kStages * kStage;  // 2 x [64 heads x 64 keys] bf16, K-major
+    static constexpr uint32_t kOffRaw = kOffP + 16384;
+    static constexpr uint32_t kOffMisc = kOffRaw + kRaw * kRawTile;
+};
 
 // tensor memory columns
 constexpr uint32_t kColQ = 0;    // [low, high] heads x 256 dims, two a column
@@ -107,14 +119,16 @@ struct Space {
 // Key slots of a token, from its position alone.
 struct Keys {
     int32_t seq, win_start, n_win, vis, n_cmp;
-    __device__ __forceinline__ uint32_t slots() const { return (uint32_t)n_win + (uint32_t)n_cmp; }
+    int32_t win_slots;  // of n_win rows: with 4-bit rows whole tiles, so that a tile is of one kind
+    __device__ __forceinline__ uint32_t slots() const { return (uint32_t)win_slots + (uint32_t)n_cmp; }
     __device__ __forceinline__ int32_t tiles() const {  // a token without keys has one, empty
-        return max(1, (int32_t)(((uint32_t)n_win + (uint32_t)n_cmp + kTile - 1) / kTile));
+        return max(1, (int32_t)((slots() + kTile - 1) / kTile));
     }
 };
 
+template <bool Q4>
 __device__ __forceinline__ Keys token_keys(const MlaPagedArgs &a, int32_t t, bool report) {
-    Keys k = {-1, 0, 0, 0, 0};
+    Keys k = {-1, 0, 0, 0, 0, 0};
     const int32_t pos = __ldg(a.q_pos + t);
     const int32_t b = paged_seq(a.q_seq, a.batch, t, pos);
     if (b < 0) {
@@ -124,6 +138,7 @@ __device__ __forceinline__ Keys token_keys(const MlaPagedArgs &a, int32_t t, boo
     k.seq = b;
     k.win_start = max(pos - a.window + 1, 0);
     k.n_win = pos - k.win_start + 1;
+    k.win_slots = Q4 ? (k.n_win + kTile - 1) / kTile * kTile : k.n_win;
     if (a.cmp.base) {
         const int32_t cap = a.cmp.max_pages * a.cmp.page_size;
         k.vis = (int32_t)(((uint32_t)pos + 1u) / (uint32_t)a.cmp_ratio);
@@ -149,13 +164,13 @@ struct Slot {
 // not checked yet.
 __device__ __forceinline__ int32_t slot_row(const MlaPagedArgs &a, const Keys &k, int32_t t, uint32_t i) {
     if (i < (uint32_t)k.n_win) return k.win_start + (int32_t)i;
-    if (i >= k.slots()) return -1;
-    const int32_t e = (int32_t)(i - (uint32_t)k.n_win);
+    if (i < (uint32_t)k.win_slots || i >= k.slots()) return -1;
+    const int32_t e = (int32_t)(i - (uint32_t)k.win_slots);
     return a.idx ? __ldg(a.idx + (int64_t)t * a.topk + e) : e;
 }
 
 __device__ __forceinline__ Slot slot_page(const MlaPagedArgs &a, const Keys &k, uint32_t i, int32_t row) {
-    const bool win = i < (uint32_t)k.n_win;
+    const bool win = i < (uint32_t)k.win_slots;
     if (row < 0 || (!win && row >= k.vis)) return {-1, -1, win};
     const PagedRows &p = win ? a.ori : a.cmp;
     const uint32_t pg = (uint32_t)row / (uint32_t)p.page_size;
@@ -163,7 +178,9 @@ __device__ __forceinline__ Slot slot_page(const MlaPagedArgs &a, const Keys &k, 
     return {in, pg < (uint32_t)p.max_pages ? __ldg(p.pages + (int64_t)k.seq * p.max_pages + pg) : -1, win};
 }
 
-// nullptr: no key, or its page is evicted or absent (recorded)
+// nullptr: no key, or its page is evicted or absent (recorded). Rows of the
+// compressed cache may be of 384 bytes: the caller knows the slot's kind.
+template <bool Q4>
 __device__ __forceinline__ const __nv_bfloat16 *slot_ptr(const MlaPagedArgs &a, const Slot &s) {
     if (s.in < 0) return nullptr;
     const PagedRows &p = s.win ? a.ori : a.cmp;
@@ -171,7 +188,8 @@ __device__ __forceinline__ const __nv_bfloat16 *slot_ptr(const MlaPagedArgs &a, 
         if (s.phys != CSA_PAGE_EVICTED) report_error(a.err, kErrCheck, kKerMlaPaged, 3);
         return nullptr;
     }
-    return p.base + ((int64_t)s.phys * p.page_size + s.in) * 512;
+    const int64_t row = (int64_t)s.phys * p.page_size + s.in;
+    return p.base + row * (Q4 && !s.win ? q4::kRow / 2 : 512);
 }
 
 // A stretch of tiles [j0, j1) of one token, worked by one CTA.
@@ -181,31 +199,39 @@ struct Piece {
     Keys k;
 };
 
+template <bool Q4>
 struct Misc {
+    static constexpr int kStages = Form<Q4>::kStages;
     uint64_t q_full;
     uint64_t kv_full[kStages], kv_empty[kStages];
+    uint64_t raw_full[Q4 ? 3 : 1], raw_empty[Q4 ? 3 : 1];
     uint64_t s_full, s_empty, p_full[2];
     uint64_t o_full, o_empty, drain;
     uint64_t ring_full[kRing], ring_empty[kRing];
     const __nv_bfloat16 *ring[kRing][kTile];  // pool rows of a tile's slots, nullptr: no key
     uint32_t tmem_base;
     int32_t abort;
+    int64_t run_s, run_e;  // the CTA's run of tiles, of `per` each
+    int64_t per;
     int64_t run_base;      // tiles before token run_t
     int64_t done;          // tiles up to the end of the batch
     int32_t run_t;         // token holding the CTA's next tile
     int32_t n_pieces;
     int32_t tiles[kMaxGrid];  // of each token, with no more tokens than CTAs
-    int32_t scan[kThreads / 32 + 1];
+    int32_t scan[Form<Q4>::kThreads / 32 + 1];
     uint32_t valid[kStages][2];  // per stage and loader warp: 32 slot bits
+    uint32_t raw_valid[Q4 ? 3 : 1][2];
     Piece piece[kPieces];
     float red[2][2][64];       // [tile parity][warpgroup][head]
     alignas(16) float fac[64];  // a rescaling's or the epilogue's factor
 };
 
-constexpr size_t kSmemBytes = kOffMisc + sizeof(Misc) + 1024;
-static_assert(kSmemBytes <= 232448, "shared memory budget");
-
-using Ctx = PipeWaits<Misc, kKerMlaPaged>;
+template <bool Q4>
+constexpr size_t smem_bytes() {
+    return Form<Q4>::kOffMisc + sizeof(Misc<Q4>) + 1024;
+}
+static_assert(smem_bytes<false>() <= 232448 && smem_bytes<true>() <= 232448, "shared memory budget");
+static_assert(Form<true>::kRaw == 3, "barriers of the raw tiles");
 
 // AND / OR of v over the 256 softmax threads.
 __device__ __forceinline__ bool all_of(bool v) {
@@ -233,24 +259,80 @@ __device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, ui
         : "memory");
 }
 
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint4 (&v)[8]) {
-    float f[32];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        f[4 * i] = __uint_as_float(v[i].x);
-        f[4 * i + 1] = __uint_as_float(v[i].y);
-        f[4 * i + 2] = __uint_as_float(v[i].z);
-        f[4 * i + 3] = __uint_as_float(v[i].w);
-    }
-    tc::tmem_st32(taddr, f);  // the bits as they are
+// N columns (16 or 32) of tensor memory.
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[N]) {
+    if constexpr (N == 16) tc::tmem_ld16(taddr, v);
+    else tc::tmem_ld32(taddr, v);
+}
+template <int N>
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const float (&v)[N]) {
+    if constexpr (N == 16) tc::tmem_st16(taddr, v);
+    else tc::tmem_st32(taddr, v);
 }
 
-__global__ void __launch_bounds__(kThreads, 1)
+// Of a piece's tiles, Q being the first, the number of the first with 4-bit rows.
+__device__ __forceinline__ int32_t first_coded(const Piece &p) {
+    return 1 + max(p.k.win_slots / kTile - p.j0, 0);
+}
+
+__device__ __forceinline__ void mbar_arrive_n(uint64_t *bar, uint32_t n) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(tc::smem_u32(bar)), "r"(n) : "memory");
+}
+
+// A warp's eight rows of a raw tile, to bf16 in a stage. Lane: row `lane % 8`
+// and of its 14 pieces of 32 codes (16 bytes) every fourth; in the
+// last round half the lanes copy the rotary dims. Eight lanes read and write
+// eight rows, at eight places of a swizzled line: no bank conflicts. A row of
+// zeros (no key) gives zeros. The loops stay loops: every role runs its own code
+// on the same SM, and its instructions have to be fetched.
+__device__ __forceinline__ void spread_rows(const unsigned char *raw, unsigned char *stage, int w, int lane) {
+    const int r = lane & 7, k = lane >> 3;
+    raw += (8 * w + r) * q4::kRow;
+    stage += w * 2048 + r * 128;
+    const float unit = q4::pow2((int)raw[q4::kExp ^ (r << 4)] - 127);
+    auto put = [&](int piece, const uint4 &c) {  // 32 dims
+        const float2 f =
+            q4::scales2(*reinterpret_cast<const uint16_t *>(raw + ((q4::kScales + 2 * piece) ^ (r << 4))));
+        const __nv_bfloat162 s0 = q4::scale_pair(f.x, unit), s1 = q4::scale_pair(f.y, unit);
+        unsigned char *line = stage + ((piece & 7) >> 1) * 16384 + (piece >> 3) * 1024;
+        const uint32_t word[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+            *reinterpret_cast<uint4 *>(line + (((4 * (piece & 1) + x) ^ r) << 4)) =
+                q4::eight(word[x], x < 2 ? s0 : s1);
+    };
+    uint4 c = *reinterpret_cast<const uint4 *>(raw + ((16 * k) ^ (r << 4)));
+#pragma unroll 1
+    for (int piece = k; piece < 12; piece += 4) {
+        const uint4 now = c;
+        c = *reinterpret_cast<const uint4 *>(raw + ((16 * (piece + 4)) ^ (r << 4)));
+        put(piece, now);
+    }
+    if (k < 2) {
+        put(12 + k, c);
+    } else {
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+            *reinterpret_cast<uint4 *>(stage + 3 * 16384 + 1024 + (((4 * (k - 2) + x) ^ r) << 4)) =
+                *reinterpret_cast<const uint4 *>(raw + ((q4::kTail + 64 * (k - 2) + 16 * x) ^ (r << 4)));
+    }
+}
+
+template <bool Q4>
+__global__ void __launch_bounds__(Form<Q4>::kThreads, 1)
 sparse_mla_paged_kernel(const __grid_constant__ MlaPagedArgs a) {
+    using F = Form<Q4>;
+    constexpr int kThreads = F::kThreads, kStages = F::kStages, kSpreadWarps = F::kSpreadWarps;
+    constexpr int kRaw = Q4 ? F::kRaw : 1;
+    constexpr uint32_t kOffP = F::kOffP;
+    constexpr int kCols = Q4 ? 16 : 32;  // tensor memory columns a thread takes at a time: its registers
+    using Misc = Misc<Q4>;
+    using Ctx = PipeWaits<Misc, kKerMlaPaged>;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem = reinterpret_cast<unsigned char *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    Misc *ms = reinterpret_cast<Misc *>(smem + kOffMisc);
+    Misc *ms = reinterpret_cast<Misc *>(smem + F::kOffMisc);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const Space ws(a.workspace, a.H);
     const Ctx cx{ms, a.err, a.wait_ns};
@@ -259,7 +341,7 @@ sparse_mla_paged_kernel(const __grid_constant__ MlaPagedArgs a) {
     if (tid == 0) {
         tc::mbar_init(&ms->q_full, 256);
         for (int i = 0; i < kStages; ++i) {
-            tc::mbar_init(&ms->kv_full[i], kLoaders + 2);
+            tc::mbar_init(&ms->kv_full[i], Q4 ? 33 * kSpreadWarps : kLoaders + 2);
             tc::mbar_init(&ms->kv_empty[i], 1);
         }
         tc::mbar_init(&ms->s_full, 1);
@@ -270,7 +352,11 @@ sparse_mla_paged_kernel(const __grid_constant__ MlaPagedArgs a) {
         tc::mbar_init(&ms->drain, 1);
         for (int i = 0; i < kRing; ++i) {
             tc::mbar_init(&ms->ring_full[i], 32);
-            tc::mbar_init(&ms->ring_empty[i], kLoaders);
+            tc::mbar_init(&ms->ring_empty[i], kLoaders + 32 * kSpreadWarps);
+        }
+        for (int i = 0; Q4 && i < kRaw; ++i) {
+            tc::mbar_init(&ms->raw_full[i], kLoaders + 2);
+            tc::mbar_init(&ms->raw_empty[i], kSpreadWarps);
         }
         ms->abort = 0;
         tc::fence_mbar_init();
@@ -301,13 +387,13 @@ sparse_mla_paged_kernel(const __grid_constant__ MlaPagedArgs a) {
     tc::tc_fence_before();
 
     // ---------------------------------------------- this CTA's share of tiles
-    Keys k = {-1, 0, 0, 0, 0};
-    int32_t n = 0;
-    int64_t s = 0, e = 1;  // by token: one piece, below; else this CTA's run of tiles
-    int64_t per = 0;
+    // (What only the batches below need waits in shared memory: every role's
+    // code would carry it in registers.)
     if (by_token) {
+        Keys k = {-1, 0, 0, 0, 0, 0};
+        int32_t n = 0;
         if (tid < a.T) {
-            k = token_keys(a, tid, c == 0);
+            k = token_keys<Q4>(a, tid, c == 0);
             n = k.tiles();
             ms->tiles[tid] = n;
         }
@@ -377,7 +463,7 @@ sparse_mla_paged_kernel(const __grid_constant__ MlaPagedArgs a) {
                             parts == 1 ? -1 : 2 * c + (part == 0 ? 1 : 0), k};
             if (part == 0) ws.join[t] = {t, first, first + parts - 1, 0};
             ms->n_pieces = 1;
-            ms->done = 1;
+            ms->done = ms->run_e = 1;
         }
     } else {
         // Equal runs. Tokens are scanned kThreads at a time: once to count the
@@ -386,13 +472,17 @@ sparse_mla_paged_kernel(const __grid_constant__ MlaPagedArgs a) {
         int32_t total;
         for (int32_t t0 = 0; t0 < a.T; t0 += kThreads) {
             const int32_t t = t0 + tid;
-            block_exclusive_scan<kThreads>(t < a.T ? token_keys(a, t, c == 0).tiles() : 0, ms->scan, &total);
+            block_exclusive_scan<kThreads>(t < a.T ? token_keys<Q4>(a, t, c == 0).tiles() : 0, ms->scan, &total);
             N += total;
         }
         tc::tc_fence_after();
-        per = div64(N + gridDim.x - 1, gridDim.x);
-        s = min(c * per, N);
-        e = min(s + per, N);
+        const int64_t per = div64(N + gridDim.x - 1, gridDim.x);
+        const int64_t s = min(c * per, N), e = min(s + per, N);
+        if (tid == 0) {
+            ms->run_s = s;
+            ms->run_e = e;
+            ms->per = per;
+        }
         if (s == e) {  // no run left for this CTA
             __syncthreads();
             if (warp == kMmaWarp) tc::tmem_dealloc(ms->tmem_base, kTmemCols);
@@ -400,7 +490,7 @@ sparse_mla_paged_kernel(const __grid_constant__ MlaPagedArgs a) {
         }
         int64_t base = 0;
         for (int32_t t0 = 0; t0 < a.T && base <= s; t0 += kThreads) {
-            const int32_t t = t0 + tid, nt = t < a.T ? token_keys(a, t, false).tiles() : 0;
+            const int32_t t = t0 + tid, nt = t < a.T ? token_keys<Q4>(a, t, false).tiles() : 0;
             const int64_t bt = base + block_exclusive_scan<kThreads>(nt, ms->scan, &total);
             if (bt <= s && s < bt + nt) {
                 ms->run_t = t;
@@ -414,17 +504,17 @@ sparse_mla_paged_kernel(const __grid_constant__ MlaPagedArgs a) {
 
     // counters of each role, kept across batches of pieces
     uint32_t g = 0, np = 0;
+    uint32_t rc = 0;  // raw tiles so far
     bool issued = false;
-    int64_t done = s;
-    while (done < e) {
+    do {
         // ------------------------------------------------- a batch of pieces
         if (!by_token) {
             const int32_t t_first = ms->run_t, t = t_first + tid;
-            const int64_t base = ms->run_base;
-            int32_t total;
-            n = 0;
+            const int64_t base = ms->run_base, s = ms->run_s, e = ms->run_e;
+            int32_t total, n = 0;
+            Keys k = {-1, 0, 0, 0, 0, 0};
             if (tid < kPieces && t < a.T) {
-                k = token_keys(a, t, false);
+                k = token_keys<Q4>(a, t, false);
                 n = k.tiles();
             }
             const int64_t b = base + block_exclusive_scan<kThreads>(n, ms->scan, &total);
@@ -437,7 +527,7 @@ sparse_mla_paged_kernel(const __grid_constant__ MlaPagedArgs a) {
                 p.k = k;
                 ms->piece[tid] = p;
                 if (p.slot == 2 * c + 1)  // starts here, goes on in other CTAs
-                    ws.join[c] = {t, c, (int32_t)div64(b + n - 1, per), 0};
+                    ws.join[c] = {t, c, (int32_t)div64(b + n - 1, ms->per), 0};
                 if (tid == kPieces - 1 || t + 1 == a.T || b + n >= e) {
                     ms->n_pieces = tid + 1;
                     ms->done = min(e, b + n);
@@ -449,7 +539,6 @@ sparse_mla_paged_kernel(const __grid_constant__ MlaPagedArgs a) {
             }
         }
         __syncthreads();
-        done = ms->done;
         const int32_t n_pieces = ms->n_pieces;
 
         if (warp == kMmaWarp) {
@@ -531,6 +620,7 @@ sparse_mla_paged_kernel(const __grid_constant__ MlaPagedArgs a) {
             bool ok = true;
             for (int32_t i = 0; i < n_pieces && ok; ++i) {
                 const int32_t nt = 1 + ms->piece[i].j1 - ms->piece[i].j0;  // Q, then the keys
+                const int32_t coded = Q4 ? first_coded(ms->piece[i]) : nt;
                 for (int32_t j = 0; j < nt; ++j, ++g) {
                     ok = __all_sync(0xffffffffu,
                                     cx.wait(&ms->ring_full[g % kRing], (g / kRing) & 1, 40));
@@ -538,6 +628,37 @@ sparse_mla_paged_kernel(const __grid_constant__ MlaPagedArgs a) {
                     const __nv_bfloat16 *mine = ms->ring[g % kRing][32 * w + lane];
                     tc::mbar_arrive(&ms->ring_empty[g % kRing]);
                     const uint32_t m = __ballot_sync(0xffffffffu, mine != nullptr), st = g % kStages;
+                    if constexpr (Q4) {
+                        // Tiles in bf16 are the spread warps', which follow the
+                        // stages one by one. Four rows of 384 bytes are three
+                        // instructions. (A bulk copy a row took 65 clocks to
+                        // issue, 4200 a tile.)
+                        if (j < coded) continue;
+                        const uint32_t rs = rc % kRaw;
+                        ok = __all_sync(0xffffffffu, cx.wait(&ms->raw_empty[rs], ((rc / kRaw) & 1) ^ 1, 42));
+                        if (!ok) break;
+                        ++rc;
+                        const uint32_t raw = tc::smem_u32(smem + F::kOffRaw + rs * kRawTile) + 32 * w * q4::kRow;
+#pragma unroll 1
+                        for (int x = 0; x < 3; ++x) {
+                            const int sub = (32 * x + lane) / 24, piece = (32 * x + lane) % 24;
+#pragma unroll
+                            for (int r = 0; r < 32; r += 4) {
+                                const unsigned char *src = reinterpret_cast<const unsigned char *>(
+                                    __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), r + sub));
+                                const uint32_t bytes = src ? 16u : 0u;  // no key: zeros
+                                if (!src) src = reinterpret_cast<const unsigned char *>(a.q);
+                                cp_async16(raw + (r + sub) * q4::kRow + (16 * piece ^ (((r + sub) & 7) << 4)),
+                                           src + 16 * piece, bytes);
+                            }
+                        }
+                        cp_async_arrive(&ms->raw_full[rs]);
+                        if (lane == 0) {
+                            ms->raw_valid[rs][w] = m;
+                            tc::mbar_arrive(&ms->raw_full[rs]);
+                        }
+                        continue;
+                    }
                     ok = __all_sync(0xffffffffu, cx.wait(&ms->kv_empty[st], ((g / kStages) & 1) ^ 1, 41));
                     if (!ok) break;
                     // Half a row (512 bytes) an instruction: pieces of 128 bytes
@@ -560,6 +681,56 @@ sparse_mla_paged_kernel(const __grid_constant__ MlaPagedArgs a) {
                     if (lane == 0) {
                         ms->valid[st][w] = m;
                         tc::mbar_arrive(&ms->kv_full[st]);
+                    }
+                }
+            }
+        } else if (Q4 && warp > kFindWarp) {
+            // ================================================= spread warps
+            // Warp w: rows 8 w .. 8 w + 7 of every tile, from a raw tile or, in
+            // bf16, from global memory. (kv_full: 33 arrivals a warp, one of
+            // each lane's copies and one more, or all at once.)
+            const int w = warp - kFindWarp - 1;
+            bool ok = true;
+            for (int32_t i = 0; i < n_pieces && ok; ++i) {
+                const int32_t nt = 1 + ms->piece[i].j1 - ms->piece[i].j0, coded = first_coded(ms->piece[i]);
+                for (int32_t j = 0; j < nt; ++j, ++g) {
+                    const uint32_t st = g % kStages, rs = rc % kRaw;
+                    ok = __all_sync(0xffffffffu, cx.wait(&ms->ring_full[g % kRing], (g / kRing) & 1, 45));
+                    if (!ok) break;
+                    const __nv_bfloat16 *mine = ms->ring[g % kRing][32 * (w >> 2) + lane];
+                    tc::mbar_arrive(&ms->ring_empty[g % kRing]);
+                    ok = __all_sync(0xffffffffu,
+                                    cx.wait(&ms->kv_empty[st], ((g / kStages) & 1) ^ 1, 43) &&
+                                        (j < coded || cx.wait(&ms->raw_full[rs], (rc / kRaw) & 1, 44)));
+                    if (!ok) break;
+                    if (j < coded) {
+                        const uint32_t m = __ballot_sync(0xffffffffu, mine != nullptr);
+                        const uint32_t stage = tc::smem_u32(smem + st * kStage) + (lane >> 3) * 16384 + w * 2048;
+#pragma unroll 2
+                        for (int r = 0; r < 8; ++r) {
+                            const __nv_bfloat16 *src = reinterpret_cast<const __nv_bfloat16 *>(__shfl_sync(
+                                0xffffffffu, reinterpret_cast<unsigned long long>(mine), 8 * (w & 3) + r));
+                            const uint32_t bytes = src ? 16u : 0u;  // no key: zeros
+                            if (!src) src = a.q;
+                            const uint32_t dst = stage + r * 128 + (((lane ^ r) & 7) << 4);
+                            cp_async16(dst, src + lane * 8, bytes);
+                            cp_async16(dst + 1024, src + 256 + lane * 8, bytes);
+                        }
+                        cp_async_arrive(&ms->kv_full[st]);
+                        if (lane == 0) {
+                            if ((w & 3) == 0) ms->valid[st][w >> 2] = m;
+                            tc::mbar_arrive(&ms->kv_full[st]);
+                        }
+                        continue;
+                    }
+                    ++rc;
+                    if (lane == 0 && (w & 3) == 0) ms->valid[st][w >> 2] = ms->raw_valid[rs][w >> 2];
+                    spread_rows(smem + F::kOffRaw + rs * kRawTile, smem + st * kStage, w, lane);
+                    tc::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive_n(&ms->kv_full[st], 33);
+                        tc::mbar_arrive(&ms->raw_empty[rs]);
                     }
                 }
             }
@@ -602,7 +773,7 @@ sparse_mla_paged_kernel(const __grid_constant__ MlaPagedArgs a) {
                                     cx.wait(&ms->ring_empty[g % kRing], ((g / kRing) & 1) ^ 1, 50));
                     if (!ok) break;
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) ms->ring[g % kRing][32 * x + lane] = slot_ptr(a, s0[x]);
+                    for (int x = 0; x < 2; ++x) ms->ring[g % kRing][32 * x + lane] = slot_ptr<Q4>(a, s0[x]);
                     tc::mbar_arrive(&ms->ring_full[g % kRing]);
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
@@ -629,12 +800,18 @@ sparse_mla_paged_kernel(const __grid_constant__ MlaPagedArgs a) {
                 const unsigned char *q = smem + (g % kStages) * kStage + 2 * wg * 16384 + (h >> 3) * 2048 +
                                          hi * 1024 + (h & 7) * 128;
 #pragma unroll
-                for (int d = 0; d < 2; ++d) {
-                    uint4 v[8];
+                for (int d = 0; d < 64; d += kCols) {
+                    float v[kCols];  // the bits as they are
 #pragma unroll
-                    for (int u = 0; u < 8; ++u)
-                        v[u] = *reinterpret_cast<const uint4 *>(q + d * 16384 + ((u ^ (h & 7)) << 4));
-                    tmem_st32(lane_addr + kColQ + 64 * wg + 32 * d, v);
+                    for (int u = 0; u < kCols / 4; ++u) {
+                        const uint4 x = *reinterpret_cast<const uint4 *>(
+                            q + (d >> 5) * 16384 + (((u + (d & 31) / 4) ^ (h & 7)) << 4));
+                        v[4 * u] = __uint_as_float(x.x);
+                        v[4 * u + 1] = __uint_as_float(x.y);
+                        v[4 * u + 2] = __uint_as_float(x.z);
+                        v[4 * u + 3] = __uint_as_float(x.w);
+                    }
+                    tmem_st<kCols>(lane_addr + kColQ + 64 * wg + d, v);
                 }
                 tc::tmem_wait_st();
                 tc::tc_fence_before();
@@ -656,8 +833,23 @@ sparse_mla_paged_kernel(const __grid_constant__ MlaPagedArgs a) {
                     tc::tc_fence_after();
                     const uint32_t valid = ms->valid[g % kStages][wg] >> (16 * hi);
                     float s[16];
-                    {
-                        // columns 64 wg on: groups of 8 keys, low and high dims in turn
+                    // columns 64 wg on: groups of 8 keys, low and high dims in turn
+                    if constexpr (Q4) {  // half of them at a time: 96 registers a thread
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            float c0[16], c1[16];
+                            tc::tmem_ld16(lane_addr + kColS + 64 * wg + 16 * y, c0);
+                            tc::tmem_ld16(lane_addr + kColS + 64 * wg + 32 + 16 * y, c1);
+                            tc::tmem_wait_ld();
+#pragma unroll
+                            for (int x = 0; x < 8; ++x) {
+                                const float own = hi ? c1[x + 8] : c0[x], give = hi ? c0[x + 8] : c1[x];
+                                s[8 * y + x] = own + __shfl_xor_sync(0xffffffffu, give, 8);
+                            }
+                        }
+                        tc::tc_fence_before();
+                        tc::mbar_arrive(&ms->s_empty);
+                    } else {
                         float c0[32], c1[32];
                         tc::tmem_ld32(lane_addr + kColS + 64 * wg, c0);
                         tc::tmem_ld32(lane_addr + kColS + 64 * wg + 32, c1);
@@ -718,14 +910,15 @@ sparse_mla_paged_kernel(const __grid_constant__ MlaPagedArgs a) {
                                 tc::tc_fence_after();
                                 const int h0 = 32 * wg;
 #pragma unroll 1
-                                for (int d = 0; d < 4; ++d) {
-                                    float o[32];
-                                    const uint32_t addr = lane_addr + kColO + 64 * d + h0;
-                                    tc::tmem_ld32(addr, o);
+                                for (int d = 0; d < 128 / kCols; ++d) {
+                                    float o[kCols];
+                                    const int x0 = h0 + kCols * d % 32;
+                                    const uint32_t addr = lane_addr + kColO + 64 * (kCols * d / 32) + x0;
+                                    tmem_ld<kCols>(addr, o);
                                     tc::tmem_wait_ld();
 #pragma unroll
-                                    for (int x = 0; x < 32; ++x) o[x] *= ms->fac[h0 + x];
-                                    tc::tmem_st32(addr, o);
+                                    for (int x = 0; x < kCols; ++x) o[x] *= ms->fac[x0 + x];
+                                    tmem_st<kCols>(addr, o);
                                 }
                                 tc::tmem_wait_st();
                             }
@@ -794,25 +987,26 @@ sparse_mla_paged_kernel(const __grid_constant__ MlaPagedArgs a) {
                 const int dim = (q4 >> 1) * 256 + 32 * (q4 & 1) + lane;
                 __nv_bfloat16 *outp = a.out + ((int64_t)tt * a.H + h0) * 512 + dim;
 #pragma unroll 1
-                for (int d = 0; d < 4; ++d) {
-                    float o[32];
-                    tc::tmem_ld32(lane_addr + kColO + 64 * d + h0, o);
+                for (int c = 0; c < 128 / kCols; ++c) {
+                    const int d = kCols * c / 32, x0 = kCols * c % 32;
+                    float o[kCols];
+                    tmem_ld<kCols>(lane_addr + kColO + 64 * d + h0 + x0, o);
                     tc::tmem_wait_ld();
-                    if (d == 3) {  // O^T is read: the next token's may start
+                    if (c + 1 == 128 / kCols) {  // O^T is read: the next token's may start
                         tc::tc_fence_before();
                         tc::mbar_arrive(&ms->o_empty);
                     }
                     if (slot >= 0) {
 #pragma unroll
-                        for (int x = 0; x < 32; x += 4)
-                            if (x < n_h)
-                                *ws.sums(slot, (h0 + x) >> 2, dim + 64 * d) =
+                        for (int x = 0; x < kCols; x += 4)
+                            if (x0 + x < n_h)
+                                *ws.sums(slot, (h0 + x0 + x) >> 2, dim + 64 * d) =
                                     make_float4(o[x], o[x + 1], o[x + 2], o[x + 3]);
                     } else {
 #pragma unroll
-                        for (int x = 0; x < 32; ++x)
-                            if (x < n_h)
-                                outp[x * 512 + 64 * d] = __float2bfloat16_rn(o[x] * ms->fac[h0 + x]);
+                        for (int x = 0; x < kCols; ++x)
+                            if (x0 + x < n_h)
+                                outp[(x0 + x) * 512 + 64 * d] = __float2bfloat16_rn(o[x] * ms->fac[h0 + x0 + x]);
                     }
                 }
                 tc::named_bar_sync(1, 256);  // fac and red are read
@@ -820,10 +1014,10 @@ sparse_mla_paged_kernel(const __grid_constant__ MlaPagedArgs a) {
         }
         __syncthreads();
         if (cx.aborted()) break;
-    }
+    } while (ms->done < ms->run_e);  // written again behind a barrier of the next batch
 
     // ------------------------------------------------------------- teardown
-    if (warp == 8 || warp == 9) asm volatile("cp.async.wait_all;" ::: "memory");
+    if (warp == 8 || warp == 9 || warp > kFindWarp) asm volatile("cp.async.wait_all;" ::: "memory");
     if (tid == 32 * kMmaWarp && issued) {  // no MMA outlives its tensor memory
         tc::mma_commit(&ms->drain);
         if (!tc::mbar_wait(&ms->drain, 0)) cx.fail(24);
@@ -949,7 +1143,10 @@ size_t mla_paged_workspace_bytes(int32_t T, int32_t H) {
            (size_t)2 * kMaxGrid * (2 * 64 + (size_t)(H + 3) / 4 * 4 * 512) * sizeof(float);
 }
 
-cudaError_t launch_sparse_mla_paged(MlaPagedArgs a, cudaStream_t stream) {
+namespace {
+
+template <bool Q4>
+cudaError_t launch(const MlaPagedArgs &a, cudaStream_t stream) {
     static PerContext pc;
     int sms, dev;
     bool first;
@@ -958,13 +1155,13 @@ cudaError_t launch_sparse_mla_paged(MlaPagedArgs a, cudaStream_t stream) {
     if (e == cudaSuccess) e = sm_count(&sms);
     if (e != cudaSuccess) return e;
     if (first) {
-        e = cudaFuncSetAttribute(sparse_mla_paged_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)kSmemBytes);
+        e = cudaFuncSetAttribute(sparse_mla_paged_kernel<Q4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)smem_bytes<Q4>());
         if (e != cudaSuccess) return e;
         entered_context(pc, dev, ctx);
     }
     const int grid = min(sms, kMaxGrid);
-    e = launch_early(sparse_mla_paged_kernel, dim3(grid), dim3(kThreads), kSmemBytes, stream, a);
+    e = launch_early(sparse_mla_paged_kernel<Q4>, dim3(grid), dim3(Form<Q4>::kThreads), smem_bytes<Q4>(), stream, a);
     if (e != cudaSuccess) return e;
     // Small items while they fit at once: first the parts by four groups of
     // threads, then by two, then none, then two dims a thread.
@@ -976,5 +1173,11 @@ cudaError_t launch_sparse_mla_paged(MlaPagedArgs a, cudaStream_t stream) {
     return launch_early(sparse_mla_paged_join_kernel<2>, dim3(gx, max(1, min(quads, join_blocks(2) * sms / gx))),
                         dim3(kJoinThreads), 0, stream, a, 1);
 }
+
+}  // namespace
+
+cudaError_t launch_sparse_mla_paged(MlaPagedArgs a, cudaStream_t stream) { return launch<false>(a, stream); }
+
+cudaError_t launch_sparse_mla_paged_q4(MlaPagedArgs a, cudaStream_t stream) { return launch<true>(a, stream); }
 
 }  // namespace csa

@@ -11,6 +11,7 @@ import sparse_attention_csa_gb300 as csa
 from tests import _paged_ref as R
 from tests import _q4_ref as Q
 from tests.test_gpu_paged_mla import Case, i32
+from tests.test_gpu_paged_timeout import sweep
 
 pytestmark = pytest.mark.gpu
 
@@ -146,6 +147,19 @@ def test_not_finite():
     c.sinks[3] = math.nan
     out, lse = c.call()
     assert lse[:, 3].isnan().all() and not lse[:, :3].isnan().any() and out[:, 3].isnan().all()
+
+
+@pytest.mark.parametrize("tokens", [3, 40, 700])
+def test_waits_that_give_up(tokens):
+    rng = np.random.default_rng(tokens)
+    n = 20000 if tokens == 3 else 1500
+    c = Q4Case([n], 16, "all", seq=np.zeros(tokens, int), pos=rng.integers(0, n, tokens), seed=13,
+               win_left=300)
+    args = c.args()
+    want = csa.csa_sparse_mla_paged_q4(*args, return_softmax_lse=True)
+    assert sweep(lambda: csa.csa_sparse_mla_paged_q4(*args), 12)
+    got = csa.csa_sparse_mla_paged_q4(*args, return_softmax_lse=True)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
 def test_two_graphs_at_once_with_workspaces_of_their_own():
