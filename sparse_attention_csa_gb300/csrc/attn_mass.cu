@@ -1,119 +1,602 @@
-// The attention weight that cached compressed rows received (sm_103a):
+// The attention weight that cached compressed rows received (sm_103a, tcgen05,
+// cp.async):
 //
 //     out[b, j] = mass[b, j] + sum over the tokens t of sequence b that attend
 //                 row j, and their heads h, of e^(scale q[t,h].k_j - lse[t,h])
 //
 // Two kernels. The first leaves the weight of every (token, key slot), heads
 // summed, in the workspace; the second adds a sequence's tokens up in an order
-// that does not depend on the launch. Listed rows are added in shared memory as
-// fixed-point numbers, whose sums have no order (a row may be listed twice).
+// that does not depend on the launch.
+//
+// Weights. The 128-slot tiles of all tokens are dealt to the CTAs in equal
+// runs. A tile's rows are the MMA's M side, the heads its N side: S[j, h] =
+// k_j . q_h over 512 dims, so that with one lane of tensor memory a row the sum
+// over heads stays inside a thread, which takes e^(S - lse) as base-2
+// exponentials. Rows of 4 bits come to shared memory as they are (48 KB a tile)
+// and are turned into bf16 on the way to tensor memory, a thread a row: the
+// MMA's A operand is read from there, so that shared memory carries 96 KB of
+// rows and 64 KB of q a tile in place of 300 KB. Rows in bf16 are the operand
+// in shared memory as they come.
+//
+// Sums. A block has 2048 rows of one sequence. Weights are added as fixed-point
+// numbers of 64 bits, whose sums have no order (a row may be listed twice, and
+// by several tokens).
 #include "common.cuh"
 #include "internal.h"
 #include "paged.h"
 #include "q4.cuh"
+#include "tc_ptx.cuh"
 
 namespace csa {
 
 namespace {
 
-// Visible compressed rows of token t, and its sequence (-1: none).
-__device__ __forceinline__ int32_t visible_rows(const MassArgs &a, int32_t t, int32_t *seq, bool report) {
+// Key slots of token t: rows [0, vis) of sequence seq are visible, and its
+// slots are the list's entries or these rows.
+struct Slots {
+    int32_t seq, vis, n;
+};
+
+__device__ __forceinline__ Slots token_slots(const MassArgs &a, int32_t t, bool report) {
     const int32_t pos = __ldg(a.q_pos + t);
     const int32_t b = paged_seq(a.q_seq, a.batch, t, pos);
-    *seq = b < 0 ? -1 : b;
     if (b < 0) {
         if (b == -2 && report) report_error(a.err, kErrCheck, kKerMass, 1);
-        return 0;
+        return {-1, 0, 0};
     }
-    const int32_t n = (int32_t)(((uint32_t)pos + 1u) / (uint32_t)a.cmp_ratio);
-    if (n > a.max_rows) {
+    int32_t vis = (int32_t)(((uint32_t)pos + 1u) / (uint32_t)a.cmp_ratio);
+    if (vis > a.max_rows) {
         if (report) report_error(a.err, kErrCheck, kKerMass, 2);
-        return a.max_rows;
+        vis = a.max_rows;
     }
-    return n;
+    return {b, vis, a.idx ? (vis > 0 ? a.topk : 0) : vis};
 }
 
-constexpr int kThreads = 256;
+// ------------------------------------------------------------------- weights
+constexpr int kTile = 128;
+constexpr int kPieces = 16;    // tokens of a run described in shared memory at a time
+constexpr int kAcc = 2;        // tensor-memory accumulators of 64 columns
+constexpr int kPresent = 8;    // tiles whose slots with a row are remembered
+constexpr int kLoaders = 128;
+constexpr float kLog2e = 1.4426950408889634f;
 
-__global__ void __launch_bounds__(kThreads) attn_weight_kernel(const __grid_constant__ MassArgs a) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int32_t t = blockIdx.x;
+struct Piece {
+    int32_t t, j0, j1;  // tiles [j0, j1) of token t
+    Slots s;
+};
+
+// Q4 false: chunks of 128 rows x 128 dims in bf16 in shared memory. true: tiles
+// of 4-bit rows there (raw), chunks in tensor memory.
+template <bool Q4>
+struct Form {
+    static constexpr int kMmaWarp = Q4 ? 16 : 8;  // behind 4 epilogue, 4 loader and (Q4) 8 spread warps
+    static constexpr int kThreads = 32 * (kMmaWarp + 1);
+    static constexpr int kRaw = Q4 ? 2 : 0;
+    static constexpr int kChunks = Q4 ? 6 : 3;    // 64 columns or 32 KB each
+    static constexpr uint32_t kQ = 64 * 512 * 2;
+    static constexpr uint32_t kOffQ = 0;          // two tokens' heads
+    static constexpr uint32_t kOffRows = 2 * kQ;
+    static constexpr uint32_t kRawTile = kTile * q4::kRow;
+    static constexpr uint32_t kChunkBytes = kTile * 256;
+    static constexpr uint32_t kOffMisc = kOffRows + (Q4 ? kRaw * kRawTile : kChunks * kChunkBytes);
+    static constexpr uint32_t kColChunk = 64 * kAcc;
+    static constexpr uint32_t kCols = Q4 ? 512 : 128;
+    static_assert(!Q4 || kColChunk + 64 * kChunks <= kCols, "tensor memory");
+};
+
+template <bool Q4>
+struct Misc {
+    using F = Form<Q4>;
+    uint64_t q_full[2], q_empty[2];
+    uint64_t raw_full[2], raw_empty[2];
+    uint64_t chunk_full[F::kChunks], chunk_empty[F::kChunks];
+    uint64_t acc_full[kAcc], acc_empty[kAcc];
+    uint64_t present_full[kPresent];
+    uint64_t drain;
+    int64_t run_base, done;
+    int32_t run_t, n_pieces;
+    uint32_t tmem_base;
+    int32_t abort;
+    int32_t scan[F::kThreads / 32 + 1];
+    uint32_t present[kPresent][4];
+    Piece piece[kPieces];
+    alignas(16) float lse2[4][64];  // each epilogue warp's own
+};
+
+template <bool Q4>
+constexpr size_t smem_bytes() {
+    return Form<Q4>::kOffMisc + sizeof(Misc<Q4>) + 1024;
+}
+static_assert(smem_bytes<false>() <= 232448 && smem_bytes<true>() <= 232448, "shared memory budget");
+
+// D += A B with A in tensor memory (lane = row, two bf16 of K a column).
+__device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                            uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_words(uint32_t taddr, const uint4 (&v)[4]) {
+    float f[16];  // the bits as they are
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[4 * i] = __uint_as_float(v[i].x);
+        f[4 * i + 1] = __uint_as_float(v[i].y);
+        f[4 * i + 2] = __uint_as_float(v[i].z);
+        f[4 * i + 3] = __uint_as_float(v[i].w);
+    }
+    tc::tmem_st16(taddr, f);
+}
+
+template <bool Q4>
+__global__ void __launch_bounds__(Form<Q4>::kThreads, 1)
+attn_weight_kernel(const __grid_constant__ MassArgs a) {
+    using F = Form<Q4>;
+    constexpr int kThreads = F::kThreads, kMmaWarp = F::kMmaWarp, kChunks = F::kChunks;
+    constexpr int kRaw = Q4 ? F::kRaw : 1;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char *smem = reinterpret_cast<unsigned char *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    Misc<Q4> *ms = reinterpret_cast<Misc<Q4> *>(smem + F::kOffMisc);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const PipeWaits<Misc<Q4>, kKerMass> cx{ms, a.err, a.wait_ns};
+    const int32_t c = blockIdx.x;
+
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(&ms->q_full[i], kLoaders);
+            tc::mbar_init(&ms->q_empty[i], 1);
+            tc::mbar_init(&ms->raw_full[i], kLoaders);
+            tc::mbar_init(&ms->raw_empty[i], 8);
+        }
+        for (int i = 0; i < kChunks; ++i) {
+            tc::mbar_init(&ms->chunk_full[i], Q4 ? 4 : kLoaders);
+            tc::mbar_init(&ms->chunk_empty[i], 1);
+        }
+        for (int i = 0; i < kAcc; ++i) {
+            tc::mbar_init(&ms->acc_full[i], 1);
+            tc::mbar_init(&ms->acc_empty[i], 128);
+        }
+        for (int i = 0; i < kPresent; ++i) tc::mbar_init(&ms->present_full[i], 4);
+        tc::mbar_init(&ms->drain, 1);
+        ms->abort = 0;
+        tc::fence_mbar_init();
+    }
+    if (warp == kMmaWarp) {
+        tc::tmem_alloc(&ms->tmem_base, F::kCols);
+        tc::tmem_relinquish();
+    }
+    // heads past H: zero rows of both q buffers, never written again
+    for (int i = tid; i < 2 * (64 - a.H) * 64; i += kThreads) {
+        const int buf = i / ((64 - a.H) * 64), r = i - buf * (64 - a.H) * 64, h = a.H + (r >> 6), u = r & 63;
+        *reinterpret_cast<uint4 *>(smem + F::kOffQ + buf * F::kQ + (u >> 3) * 8192 + h * 128 + (u & 7) * 16) =
+            make_uint4(0, 0, 0, 0);
+    }
+    // everything above is local: wait for the kernels before this one
     grid_dependency_wait();
     launch_dependents();
-    int32_t b;
-    const int32_t vis = visible_rows(a, t, &b, true);
-    const int32_t slots = a.idx ? (vis > 0 ? a.topk : 0) : vis;
-    float *out = a.weights + t * a.slot_pad;
-    for (int64_t i = (int64_t)blockIdx.y * 8 + warp; i < slots; i += 8 * gridDim.y) {
-        const int32_t r = a.idx ? __ldg(a.idx + (int64_t)t * a.topk + i) : (int32_t)i;
-        float sum = 0.0f;
-        if (r >= 0 && r < vis) {
-            const uint32_t pg = (uint32_t)r / (uint32_t)a.cmp.page_size;
-            const int32_t phys = __ldg(a.cmp.pages + (int64_t)b * a.cmp.max_pages + pg);
-            if ((uint32_t)phys < (uint32_t)a.cmp.num_pages) {
-                const int64_t row = (int64_t)phys * a.cmp.page_size + (r - (int32_t)pg * a.cmp.page_size);
-                uint4 v[2];
-                if (a.q4) {
-                    q4::sixteen(reinterpret_cast<const uint8_t *>(a.cmp.base) + row * q4::kRow, lane, v);
-                } else {
-                    const uint4 *src = reinterpret_cast<const uint4 *>(a.cmp.base + row * 512) + 2 * lane;
-                    v[0] = __ldg(src);
-                    v[1] = __ldg(src + 1);
+    tc::fence_proxy_async_smem();
+    tc::tc_fence_before();
+
+    // ------------------------------------------------ this CTA's run of tiles
+    int32_t total = 0;
+    int64_t N = 0;
+    for (int32_t t0 = 0; t0 < a.T; t0 += kThreads) {
+        const int32_t t = t0 + tid;
+        const int32_t nt = t < a.T ? (token_slots(a, t, c == 0).n + kTile - 1) / kTile : 0;
+        block_exclusive_scan<kThreads>(nt, ms->scan, &total);
+        N += total;
+    }
+    tc::tc_fence_after();
+    const uint32_t tmem = ms->tmem_base;
+    const int64_t per = div64(N + gridDim.x - 1, gridDim.x);
+    const int64_t s = min(c * per, N), e = min(s + per, N);
+    if (s == e) {  // no run left for this CTA
+        __syncthreads();
+        if (warp == kMmaWarp) tc::tmem_dealloc(tmem, F::kCols);
+        return;
+    }
+    int64_t base = 0;  // the token holding tile s
+    for (int32_t t0 = 0; t0 < a.T && base <= s; t0 += kThreads) {
+        const int32_t t = t0 + tid;
+        const int32_t nt = t < a.T ? (token_slots(a, t, false).n + kTile - 1) / kTile : 0;
+        const int64_t bt = base + block_exclusive_scan<kThreads>(nt, ms->scan, &total);
+        if (bt <= s && s < bt + nt) {
+            ms->run_t = t;
+            ms->run_base = bt;
+        }
+        base += total;
+    }
+    __syncthreads();
+
+    uint32_t g = 0, np = 0;  // tiles and tokens so far, kept by every role
+    bool issued = false;
+    int64_t done = s;
+    while (done < e) {
+        // ------------------------------------------------- a batch of tokens
+        {
+            const int32_t t_first = ms->run_t, t = t_first + tid;
+            const int64_t b0 = ms->run_base;
+            Slots sl = {-1, 0, 0};
+            if (tid < kPieces && t < a.T) sl = token_slots(a, t, false);
+            const int32_t nt = (sl.n + kTile - 1) / kTile;
+            const int64_t b = b0 + block_exclusive_scan<kThreads>(nt, ms->scan, &total);
+            if (tid < kPieces && t < a.T && b < e) {  // a token without tiles has an empty piece
+                ms->piece[tid] = {t, (int32_t)max(s - b, (int64_t)0), (int32_t)min(e - b, (int64_t)nt), sl};
+                if (tid == kPieces - 1 || t + 1 == a.T || b + nt >= e) {
+                    ms->n_pieces = tid + 1;
+                    ms->done = min(e, b + nt);
                 }
-                const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
-                for (int h = 0; h < a.H; ++h) {
-                    const __nv_bfloat16 *q = a.q + ((int64_t)t * a.H + h) * 512 + 16 * lane;
-                    float s = 0.0f;
+            }
+            if (tid == 0) {
+                ms->run_t = t_first + kPieces;
+                ms->run_base = b0 + total;
+            }
+            __syncthreads();
+        }
+        done = ms->done;
+        const int32_t n_pieces = ms->n_pieces;
+
+        if (warp == kMmaWarp) {
+            // ===================================================== MMA warp
+            if (lane == 0) {
+                constexpr uint32_t id = tc::idesc_bf16(128, 64, false, false);
+                const uint64_t da = tc::smem_desc(tc::smem_u32(smem + F::kOffRows), 16, 1024);
+                const uint64_t db = tc::smem_desc(tc::smem_u32(smem + F::kOffQ), 16, 1024);
+                bool ok = true;
+                for (int32_t i = 0; i < n_pieces && ok; ++i) {
+                    const int32_t j0 = ms->piece[i].j0, j1 = ms->piece[i].j1;
+                    if (j0 >= j1) continue;
+                    ok = cx.wait(&ms->q_full[np & 1], (np >> 1) & 1, 20);
+                    for (int32_t j = j0; j < j1 && ok; ++j, ++g) {
+                        const uint32_t acc = g % kAcc;
+                        ok = cx.wait(&ms->acc_empty[acc], ((g / kAcc) & 1) ^ 1, 22);
+#pragma unroll 1
+                        for (uint32_t ch = 0; ch < 4 && ok; ++ch) {
+                            const uint32_t cc = 4 * g + ch, st = cc % kChunks;
+                            ok = cx.wait(&ms->chunk_full[st], (cc / kChunks) & 1, 21);
+                            if (!ok) break;
+                            tc::fence_proxy_async_smem();  // cp.async wrote through the generic proxy
+                            tc::tc_fence_after();
+                            const uint64_t bq = tc::desc_add(db, (np & 1) * F::kQ + ch * 16384);
 #pragma unroll
-                    for (int x = 0; x < 8; ++x) {
-                        s = fmaf(__bfloat162float(q[2 * x]), __uint_as_float(w[x] << 16), s);
-                        s = fmaf(__bfloat162float(q[2 * x + 1]), __uint_as_float(w[x] & 0xffff0000u), s);
+                            for (int kk = 0; kk < 8; ++kk) {
+                                const uint64_t b = tc::desc_add(bq, (kk >> 2) * 8192 + (kk & 3) * 32);
+                                if constexpr (Q4)
+                                    mma_bf16_ta(tmem + 64 * acc, tmem + F::kColChunk + 64 * st + 8 * kk, b, id,
+                                                (ch | kk) != 0);
+                                else
+                                    tc::mma_bf16(tmem + 64 * acc,
+                                                 tc::desc_add(da, st * F::kChunkBytes + (kk >> 2) * 16384 +
+                                                                      (kk & 3) * 32),
+                                                 b, id, (ch | kk) != 0);
+                            }
+                            issued = true;
+                            tc::mma_commit(&ms->chunk_empty[st]);
+                        }
+                        if (ok) tc::mma_commit(&ms->acc_full[acc]);
                     }
-                    s = warp_sum(s);
-                    const float lse = __ldg(a.lse + (int64_t)t * a.H + h);
-                    if (lse != -INFINITY) sum += expf(s * a.softmax_scale - lse);
+                    if (ok) tc::mma_commit(&ms->q_empty[np & 1]);
+                    ++np;
                 }
-            } else if (phys != CSA_PAGE_EVICTED) {
-                report_error(a.err, kErrCheck, kKerMass, 3);
+            }
+            __syncwarp();
+        } else if (warp >= 8) {
+            // ================================================= spread warps
+            // Four warps have the 128 rows, a thread one; two sets of them take
+            // turns with the chunks. A row's 14 pieces of 32 codes lie in 16-byte
+            // places permuted within its lines, so that 8 lanes meet no bank twice.
+            if constexpr (Q4) {
+                const int quarter = warp & 3, set = (warp - 8) >> 2, sw = (lane & 7) << 4;
+                const uint32_t col = tmem + ((uint32_t)(32 * quarter) << 16) + F::kColChunk;
+                bool ok = true;
+                for (int32_t i = 0; i < n_pieces && ok; ++i) {
+                    const int32_t j0 = ms->piece[i].j0, j1 = ms->piece[i].j1;
+                    for (int32_t j = j0; j < j1; ++j, ++g) {
+                        const uint32_t rs = g % kRaw;
+                        ok = __all_sync(0xffffffffu, cx.wait(&ms->raw_full[rs], (g / kRaw) & 1, 50));
+                        if (!ok) break;
+                        const unsigned char *row =
+                            smem + F::kOffRows + rs * F::kRawTile + (32 * quarter + lane) * q4::kRow;
+                        const float unit = q4::pow2((int)row[q4::kExp ^ sw] - 127);
+#pragma unroll 1
+                        for (int ch = set; ch < 4; ch += 2) {
+                            const uint32_t cc = 4 * g + ch, st = cc % kChunks;
+                            ok = __all_sync(0xffffffffu,
+                                            cx.wait(&ms->chunk_empty[st], ((cc / kChunks) & 1) ^ 1, 51));
+                            if (!ok) break;
+                            tc::tc_fence_after();
+                            uint4 next = *reinterpret_cast<const uint4 *>(row + ((64 * ch) ^ sw));
+#pragma unroll 1
+                            for (int p = 0; p < 4; ++p) {
+                                const int piece = 4 * ch + p;
+                                uint4 v[4];
+                                if (piece < 14) {
+                                    const uint4 w = next;
+                                    // of the rotary dims' first bytes at the end: not used
+                                    next = *reinterpret_cast<const uint4 *>(row + ((16 * (piece + 1)) ^ sw));
+                                    const float2 f = q4::scales2(*reinterpret_cast<const uint16_t *>(
+                                        row + ((q4::kScales + 2 * piece) ^ sw)));
+                                    const __nv_bfloat162 s0 = q4::scale_pair(f.x, unit);
+                                    const __nv_bfloat162 s1 = q4::scale_pair(f.y, unit);
+                                    v[0] = q4::eight(w.x, s0);
+                                    v[1] = q4::eight(w.y, s0);
+                                    v[2] = q4::eight(w.z, s1);
+                                    v[3] = q4::eight(w.w, s1);
+                                } else {
+#pragma unroll
+                                    for (int y = 0; y < 4; ++y)
+                                        v[y] = *reinterpret_cast<const uint4 *>(
+                                            row + ((q4::kTail + 64 * (piece - 14) + 16 * y) ^ sw));
+                                }
+                                tmem_st_words(col + 64 * st + 16 * p, v);
+                            }
+                            tc::tmem_wait_st();
+                            tc::tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) tc::mbar_arrive(&ms->chunk_full[st]);
+                        }
+                        if (!ok) break;
+                        __syncwarp();
+                        if (lane == 0) tc::mbar_arrive(&ms->raw_empty[rs]);
+                    }
+                }
+            }
+        } else if (warp >= 4) {
+            // ================================================= loader warps
+            // Warp w: slots 32 w .. 32 w + 31 of every tile, one a lane. Finding a
+            // row takes two dependent loads (the list's entry, the page); they run
+            // two tiles and one tile ahead.
+            const int w = warp - 4, li = tid - 128;
+            bool ok = true;
+            for (int32_t i = 0; i < n_pieces && ok; ++i) {
+                const Piece p = ms->piece[i];
+                if (p.j0 >= p.j1) continue;
+                auto row_at = [&](int32_t j) -> int32_t {
+                    const int64_t x = (int64_t)j * kTile + 32 * w + lane;
+                    if (j >= p.j1 || x >= p.s.n) return -1;
+                    const int32_t r = a.idx ? __ldg(a.idx + (int64_t)p.t * a.topk + x) : (int32_t)x;
+                    return r < p.s.vis ? r : -1;
+                };
+                auto page_of = [&](int32_t r, int32_t *in) -> int32_t {
+                    *in = -1;
+                    if (r < 0) return -1;
+                    const uint32_t pg = (uint32_t)r / (uint32_t)a.cmp.page_size;  // in the table: r < max_rows
+                    *in = r - (int32_t)pg * a.cmp.page_size;
+                    return __ldg(a.cmp.pages + (int64_t)p.s.seq * a.cmp.max_pages + pg);
+                };
+                int32_t in, row_next = row_at(p.j0 + 1);
+                int32_t page = page_of(row_at(p.j0), &in);
+                ok = __all_sync(0xffffffffu, cx.wait(&ms->q_empty[np & 1], ((np >> 1) & 1) ^ 1, 40));
+                if (!ok) break;
+                {
+                    const __nv_bfloat16 *q = a.q + (int64_t)p.t * a.H * 512;
+                    const uint32_t dst = tc::smem_u32(smem + F::kOffQ) + (np & 1) * F::kQ;
+#pragma unroll 4
+                    for (int u = li; u < a.H * 64; u += kLoaders) {
+                        const int h = u >> 6, y = u & 63;
+                        cp_async16(dst + (y >> 3) * 8192 + h * 128 + (((y ^ h) & 7) << 4), q + (int64_t)u * 8, 16);
+                    }
+                }
+                cp_async_arrive(&ms->q_full[np & 1]);
+                ++np;
+                for (int32_t j = p.j0; j < p.j1; ++j, ++g) {
+                    const unsigned char *mine = nullptr;
+                    if (in >= 0) {
+                        if ((uint32_t)page < (uint32_t)a.cmp.num_pages)
+                            mine = reinterpret_cast<const unsigned char *>(a.cmp.base) +
+                                   ((int64_t)page * a.cmp.page_size + in) * (Q4 ? q4::kRow : 1024);
+                        else if (page != CSA_PAGE_EVICTED)
+                            report_error(a.err, kErrCheck, kKerMass, 3);
+                    }
+                    const uint32_t m = __ballot_sync(0xffffffffu, mine != nullptr);
+                    page = page_of(row_next, &in);
+                    row_next = row_at(j + 2);
+                    if constexpr (Q4) {
+                        const uint32_t rs = g % kRaw;
+                        ok = __all_sync(0xffffffffu, cx.wait(&ms->raw_empty[rs], ((g / kRaw) & 1) ^ 1, 41));
+                        if (!ok) break;
+                        // four rows of 384 bytes are three instructions
+                        const uint32_t raw =
+                            tc::smem_u32(smem + F::kOffRows) + rs * F::kRawTile + 32 * w * q4::kRow;
+#pragma unroll 1
+                        for (int x = 0; x < 3; ++x) {
+                            const int sub = (32 * x + lane) / 24, piece = (32 * x + lane) % 24;
+#pragma unroll
+                            for (int r = 0; r < 32; r += 4) {
+                                const unsigned char *src = reinterpret_cast<const unsigned char *>(
+                                    __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), r + sub));
+                                const uint32_t bytes = src ? 16u : 0u;  // no row: zeros
+                                if (!src) src = reinterpret_cast<const unsigned char *>(a.q);
+                                cp_async16(raw + (r + sub) * q4::kRow + (16 * piece ^ (((r + sub) & 7) << 4)),
+                                           src + 16 * piece, bytes);
+                            }
+                        }
+                        cp_async_arrive(&ms->raw_full[rs]);
+                    } else {
+#pragma unroll 1
+                        for (uint32_t ch = 0; ch < 4; ++ch) {
+                            const uint32_t cc = 4 * g + ch, st = cc % kChunks;
+                            ok = __all_sync(0xffffffffu,
+                                            cx.wait(&ms->chunk_empty[st], ((cc / kChunks) & 1) ^ 1, 42));
+                            if (!ok) break;
+                            // two rows' 256 bytes an instruction
+                            const int y = lane & 15, sub = lane >> 4;
+                            const uint32_t base_s = tc::smem_u32(smem + F::kOffRows) + st * F::kChunkBytes +
+                                                    (y >> 3) * 16384 + 32 * w * 128;
+#pragma unroll
+                            for (int r = 0; r < 32; r += 2) {
+                                const unsigned char *src = reinterpret_cast<const unsigned char *>(
+                                    __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), r + sub));
+                                const uint32_t bytes = src ? 16u : 0u;
+                                if (!src) src = reinterpret_cast<const unsigned char *>(a.q);
+                                cp_async16(base_s + (r + sub) * 128 + (((y ^ (r + sub)) & 7) << 4),
+                                           src + 256 * ch + 16 * y, bytes);
+                            }
+                            cp_async_arrive(&ms->chunk_full[st]);
+                        }
+                        if (!ok) break;
+                    }
+                    if (lane == 0) {
+                        // read long before tile g + kPresent: at most four tiles lie between these warps and the epilogue
+                        ms->present[g % kPresent][w] = m;
+                        tc::mbar_arrive(&ms->present_full[g % kPresent]);
+                    }
+                }
+            }
+        } else {
+            // =============================================== epilogue warps
+            const uint32_t lane_addr = tmem + ((uint32_t)(32 * warp) << 16);
+            const float sc = a.softmax_scale * kLog2e;
+            bool ok = true;
+            for (int32_t i = 0; i < n_pieces && ok; ++i) {
+                const Piece p = ms->piece[i];
+                if (p.j0 >= p.j1) continue;
+                float *lse2 = ms->lse2[warp];
+                __syncwarp();
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {  // +inf: a head that counts nothing
+                    const int h = 32 * x + lane;
+                    const float l = h < a.H ? __ldg(a.lse + (int64_t)p.t * a.H + h) : -INFINITY;
+                    lse2[h] = l == -INFINITY ? INFINITY : l * kLog2e;
+                }
+                __syncwarp();
+                float *out = a.weights + (int64_t)p.t * a.slot_pad;
+                for (int32_t j = p.j0; j < p.j1; ++j, ++g) {
+                    const uint32_t acc = g % kAcc;
+                    ok = __all_sync(0xffffffffu,
+                                    cx.wait(&ms->present_full[g % kPresent], (g / kPresent) & 1, 31) &&
+                                        cx.wait(&ms->acc_full[acc], (g / kAcc) & 1, 32));
+                    if (!ok) break;
+                    tc::tc_fence_after();
+                    const bool there = (ms->present[g % kPresent][warp] >> lane) & 1u;
+                    float sum[2] = {0.0f, 0.0f};
+#pragma unroll
+                    for (int hh = 0; hh < 2; ++hh) {
+                        float v[32];
+                        tc::tmem_ld32(lane_addr + 64 * acc + 32 * hh, v);
+                        tc::tmem_wait_ld();
+                        if (hh) {
+                            tc::tc_fence_before();
+                            tc::mbar_arrive(&ms->acc_empty[acc]);
+                        }
+#pragma unroll
+                        for (int y = 0; y < 32; y += 4) {
+                            const float4 l = *reinterpret_cast<const float4 *>(lse2 + 32 * hh + y);
+                            sum[0] += tc::ex2_approx(fmaf(v[y], sc, -l.x));
+                            sum[1] += tc::ex2_approx(fmaf(v[y + 1], sc, -l.y));
+                            sum[0] += tc::ex2_approx(fmaf(v[y + 2], sc, -l.z));
+                            sum[1] += tc::ex2_approx(fmaf(v[y + 3], sc, -l.w));
+                        }
+                    }
+                    // NaN counts as 0; more than one a head only an lse that is not the attention's can give
+                    const float all = sum[0] + sum[1], most = (float)a.H;
+                    out[(int64_t)j * kTile + 32 * warp + lane] =
+                        there && all <= most ? all : there && all > most ? most : 0.0f;
+                }
             }
         }
-        // NaN counts as 0; more than one a head only an lse that is not the attention's can give
-        if (lane == 0) out[i] = sum <= (float)a.H ? sum : sum > (float)a.H ? (float)a.H : 0.0f;
+        __syncthreads();
+        if (cx.aborted()) break;
+    }
+
+    // ------------------------------------------------------------- teardown
+    if (warp >= 4 && warp < 8) asm volatile("cp.async.wait_all;" ::: "memory");
+    if (tid == 32 * kMmaWarp && issued) {  // no MMA outlives its tensor memory
+        tc::mma_commit(&ms->drain);
+        if (!tc::mbar_wait(&ms->drain, 0)) cx.fail(24);
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    if (warp == kMmaWarp) tc::tmem_dealloc(tmem, F::kCols);
+}
+
+// ---------------------------------------------------------------------- sums
+constexpr int kSumThreads = 256;
+constexpr int kSumRows = 2048;
+constexpr int kTokens = 512;  // of the sequence, known at a time
+
+__global__ void __launch_bounds__(kSumThreads) attn_mass_kernel(const __grid_constant__ MassArgs a) {
+    __shared__ unsigned long long acc[kSumRows];
+    __shared__ int32_t token[kTokens], slots[kTokens], seen[kTokens];
+    __shared__ int32_t n_tokens;
+    const int tid = threadIdx.x;
+    const int32_t b = blockIdx.y, r0 = blockIdx.x * kSumRows, n = min(kSumRows, a.max_rows - r0);
+    for (int i = tid; i < n; i += kSumThreads) acc[i] = 0;
+    if (tid == 0) n_tokens = 0;
+    __syncthreads();
+    grid_dependency_wait();
+    launch_dependents();
+    for (int32_t t0 = 0; t0 < a.T; t0 += kTokens) {
+        // the sequence's tokens, in any order: sums have none
+#pragma unroll
+        for (int x = 0; x < kTokens; x += kSumThreads) {
+            const int32_t t = t0 + x + tid;
+            if (t < a.T) {
+                const Slots s = token_slots(a, t, false);
+                if (s.seq == b && s.n > 0 && (a.idx || s.n > r0)) {
+                    const int32_t at = atomicAdd(&n_tokens, 1);
+                    token[at] = t;
+                    slots[at] = s.n;
+                    seen[at] = s.vis;
+                }
+            }
+        }
+        __syncthreads();
+        const int32_t nt = n_tokens;
+        __syncthreads();
+        if (tid == 0) n_tokens = 0;
+        for (int32_t k = 0; k < nt; ++k) {
+            const float *w = a.weights + (int64_t)token[k] * a.slot_pad;
+            if (a.idx) {
+                const int32_t *list = a.idx + (int64_t)token[k] * a.topk;
+                for (int32_t i = tid; i < slots[k]; i += kSumThreads) {
+                    const int32_t r = __ldg(list + i);
+                    if (r >= r0 && r < min(r0 + n, seen[k])) atomicAdd(&acc[r - r0], __float2ull_rn(w[i] * a.fixed));
+                }
+            } else {  // a thread always has the same rows
+                const int32_t m = min(n, slots[k] - r0);
+                for (int32_t i = tid; i < m; i += kSumThreads) acc[i] += __float2ull_rn(w[r0 + i] * a.fixed);
+            }
+        }
+        __syncthreads();
+    }
+    const double unit = 1.0 / (double)a.fixed;
+    for (int i = tid; i < n; i += kSumThreads) {
+        const int64_t o = (int64_t)b * a.max_rows + r0 + i;
+        const float old = a.mass ? a.mass[o] : 0.0f;
+        const unsigned long long sum = acc[i];
+        if (sum) a.out[o] = old + (float)((double)sum * unit);
+        else if (a.out != a.mass) a.out[o] = old;
     }
 }
 
-// out = mass + the weights: a block takes kRows rows of one sequence.
-constexpr int kRows = 4096;
-
-__global__ void __launch_bounds__(kThreads) attn_mass_kernel(const __grid_constant__ MassArgs a) {
-    __shared__ unsigned long long acc[kRows];
-    const int32_t b = blockIdx.y, r0 = blockIdx.x * kRows, n = min(kRows, a.max_rows - r0);
-    grid_dependency_wait();
-    launch_dependents();
-    for (int i = threadIdx.x; i < n; i += kThreads) acc[i] = 0;
-    __syncthreads();
-    for (int32_t t = 0; t < a.T; ++t) {
-        int32_t seq;
-        const int32_t vis = visible_rows(a, t, &seq, false);
-        if (seq != b) continue;
-        const int32_t slots = a.idx ? (vis > 0 ? a.topk : 0) : vis;
-        for (int32_t i = threadIdx.x; i < slots; i += kThreads) {
-            const int32_t r = a.idx ? __ldg(a.idx + (int64_t)t * a.topk + i) : i;
-            if (r >= vis || r < r0 || r >= r0 + n) continue;
-            atomicAdd(&acc[r - r0], __float2ull_rn(a.weights[t * a.slot_pad + i] * a.fixed));
-        }
+template <bool Q4>
+cudaError_t launch_weights(const MassArgs &a, cudaStream_t stream) {
+    static PerContext pc;
+    int sms, dev;
+    bool first;
+    unsigned long long ctx;
+    cudaError_t e = enter_context(pc, &first, &ctx, &dev);
+    if (e == cudaSuccess) e = sm_count(&sms);
+    if (e != cudaSuccess) return e;
+    if (first) {
+        e = cudaFuncSetAttribute(attn_weight_kernel<Q4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)smem_bytes<Q4>());
+        if (e != cudaSuccess) return e;
+        entered_context(pc, dev, ctx);
     }
-    __syncthreads();
-    for (int i = threadIdx.x; i < n; i += kThreads) {
-        const int64_t o = (int64_t)b * a.max_rows + r0 + i;
-        const float old = a.mass ? a.mass[o] : 0.0f;
-        a.out[o] = acc[i] ? old + (float)((double)acc[i] / (double)a.fixed) : old;
-    }
+    return launch_early(attn_weight_kernel<Q4>, dim3(sms), dim3(Form<Q4>::kThreads), smem_bytes<Q4>(), stream, a);
 }
 
 }  // namespace
 
-int64_t mass_slot_pad(int64_t slots) { return (slots + 127) & ~(int64_t)127; }
+int64_t mass_slot_pad(int64_t slots) { return (slots + kTile - 1) / kTile * kTile; }
 
 size_t mass_workspace_bytes(int32_t T, int64_t slots) {
     return T > 0 ? (size_t)T * (size_t)mass_slot_pad(slots) * 4 : 0;
@@ -121,12 +604,11 @@ size_t mass_workspace_bytes(int32_t T, int64_t slots) {
 
 cudaError_t launch_attn_mass(MassArgs a, cudaStream_t stream) {
     if (a.T > 0) {
-        const cudaError_t e = launch_early(attn_weight_kernel, dim3(a.T, 64), dim3(kThreads), 0, stream, a);
+        const cudaError_t e = a.q4 ? launch_weights<true>(a, stream) : launch_weights<false>(a, stream);
         if (e != cudaSuccess) return e;
     }
-    if (a.batch == 0 || a.max_rows == 0) return cudaSuccess;
-    return launch_early(attn_mass_kernel, dim3((a.max_rows + kRows - 1) / kRows, a.batch), dim3(kThreads), 0,
-                        stream, a);
+    return launch_early(attn_mass_kernel, dim3((a.max_rows + kSumRows - 1) / kSumRows, a.batch),
+                        dim3(kSumThreads), 0, stream, a);
 }
 
 }  // namespace csa
