@@ -58,6 +58,10 @@ constexpr int kPieces = 16;    // tokens of a run described in shared memory at 
 constexpr int kAcc = 2;        // tensor-memory accumulators of 64 columns
 constexpr int kPresent = 8;    // tiles whose slots with a row are remembered
 constexpr int kLoaders = 128;
+// Rows of 4 bits enter the product without their power of two, which the sum's
+// thread multiplies back: one multiplication a code in place of two. It is not
+// taken below this, so that rotary dims beside vanishing others stay finite.
+constexpr int kMinUp = -40;
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct Piece {
@@ -99,13 +103,14 @@ struct Misc {
     int32_t abort;
     int32_t scan[F::kThreads / 32 + 1];
     uint32_t present[kPresent][4];
+    int8_t up[kPresent][kTile];  // powers of two taken out of the rows (4 bits)
     Piece piece[kPieces];
     alignas(16) float lse2[4][64];  // each epilogue warp's own
 };
 
 template <bool Q4>
 constexpr size_t smem_bytes() {
-    return Form<Q4>::kOffMisc + sizeof(Misc<Q4>) + 1024;
+    return Form<Q4>::kOffMisc + sizeof(Misc<Q4>);
 }
 static_assert(smem_bytes<false>() <= 232448 && smem_bytes<true>() <= 232448, "shared memory budget");
 
@@ -138,9 +143,7 @@ attn_weight_kernel(const __grid_constant__ MassArgs a) {
     using F = Form<Q4>;
     constexpr int kThreads = F::kThreads, kMmaWarp = F::kMmaWarp, kChunks = F::kChunks;
     constexpr int kRaw = Q4 ? F::kRaw : 1;
-    extern __shared__ unsigned char smem_raw[];
-    unsigned char *smem = reinterpret_cast<unsigned char *>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    extern __shared__ __align__(1024) unsigned char smem[];  // swizzled tiles: lines of 8 x 128 bytes
     Misc<Q4> *ms = reinterpret_cast<Misc<Q4> *>(smem + F::kOffMisc);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const PipeWaits<Misc<Q4>, kKerMass> cx{ms, a.err, a.wait_ns};
@@ -252,6 +255,7 @@ attn_weight_kernel(const __grid_constant__ MassArgs a) {
                     const int32_t j0 = ms->piece[i].j0, j1 = ms->piece[i].j1;
                     if (j0 >= j1) continue;
                     ok = cx.wait(&ms->q_full[np & 1], (np >> 1) & 1, 20);
+                    tc::fence_proxy_async_smem();  // cp.async wrote through the generic proxy
                     for (int32_t j = j0; j < j1 && ok; ++j, ++g) {
                         const uint32_t acc = g % kAcc;
                         ok = cx.wait(&ms->acc_empty[acc], ((g / kAcc) & 1) ^ 1, 22);
@@ -260,7 +264,7 @@ attn_weight_kernel(const __grid_constant__ MassArgs a) {
                             const uint32_t cc = 4 * g + ch, st = cc % kChunks;
                             ok = cx.wait(&ms->chunk_full[st], (cc / kChunks) & 1, 21);
                             if (!ok) break;
-                            tc::fence_proxy_async_smem();  // cp.async wrote through the generic proxy
+                            if constexpr (!Q4) tc::fence_proxy_async_smem();
                             tc::tc_fence_after();
                             const uint64_t bq = tc::desc_add(db, (np & 1) * F::kQ + ch * 16384);
 #pragma unroll
@@ -302,7 +306,11 @@ attn_weight_kernel(const __grid_constant__ MassArgs a) {
                         if (!ok) break;
                         const unsigned char *row =
                             smem + F::kOffRows + rs * F::kRawTile + (32 * quarter + lane) * q4::kRow;
-                        const float unit = q4::pow2((int)row[q4::kExp ^ sw] - 127);
+                        const int ex = (int)row[q4::kExp ^ sw] - 127;
+                        // codes times this times their scale are the row over 2^(up + 8)
+                        const float unit = q4::pow2(118 + min(ex - kMinUp, 0));
+                        const __nv_bfloat162 down = __float2bfloat162_rn(q4::pow2(-max(ex, kMinUp) - 8));
+                        if (set == 0) ms->up[g % kPresent][32 * quarter + lane] = (int8_t)max(ex, kMinUp);
 #pragma unroll 1
                         for (int ch = set; ch < 4; ch += 2) {
                             const uint32_t cc = 4 * g + ch, st = cc % kChunks;
@@ -310,30 +318,39 @@ attn_weight_kernel(const __grid_constant__ MassArgs a) {
                                             cx.wait(&ms->chunk_empty[st], ((cc / kChunks) & 1) ^ 1, 51));
                             if (!ok) break;
                             tc::tc_fence_after();
-                            uint4 next = *reinterpret_cast<const uint4 *>(row + ((64 * ch) ^ sw));
+                            // four groups' scales at a time, of two pieces of 32 dims
 #pragma unroll 1
-                            for (int p = 0; p < 4; ++p) {
-                                const int piece = 4 * ch + p;
-                                uint4 v[4];
+                            for (int p = 0; p < 2; ++p) {
+                                const int piece = 4 * ch + 2 * p;
+                                const uint32_t at = col + 64 * st + 32 * p;
                                 if (piece < 14) {
-                                    const uint4 w = next;
-                                    // of the rotary dims' first bytes at the end: not used
-                                    next = *reinterpret_cast<const uint4 *>(row + ((16 * (piece + 1)) ^ sw));
-                                    const float2 f = q4::scales2(*reinterpret_cast<const uint16_t *>(
-                                        row + ((q4::kScales + 2 * piece) ^ sw)));
-                                    const __nv_bfloat162 s0 = q4::scale_pair(f.x, unit);
-                                    const __nv_bfloat162 s1 = q4::scale_pair(f.y, unit);
-                                    v[0] = q4::eight(w.x, s0);
-                                    v[1] = q4::eight(w.y, s0);
-                                    v[2] = q4::eight(w.z, s1);
-                                    v[3] = q4::eight(w.w, s1);
-                                } else {
+                                    const uint32_t four = *reinterpret_cast<const uint32_t *>(
+                                        row + ((q4::kScales + 2 * piece) ^ sw));
 #pragma unroll
-                                    for (int y = 0; y < 4; ++y)
-                                        v[y] = *reinterpret_cast<const uint4 *>(
-                                            row + ((q4::kTail + 64 * (piece - 14) + 16 * y) ^ sw));
+                                    for (int x = 0; x < 2; ++x) {
+                                        const uint4 w =
+                                            *reinterpret_cast<const uint4 *>(row + ((16 * (piece + x)) ^ sw));
+                                        const float2 f = q4::scales2((uint16_t)(four >> (16 * x)));
+                                        const __nv_bfloat162 s0 = q4::scale_pair(f.x, unit);
+                                        const __nv_bfloat162 s1 = q4::scale_pair(f.y, unit);
+                                        const uint4 v[4] = {q4::times(q4::eight_small(w.x), s0),
+                                                            q4::times(q4::eight_small(w.y), s0),
+                                                            q4::times(q4::eight_small(w.z), s1),
+                                                            q4::times(q4::eight_small(w.w), s1)};
+                                        tmem_st_words(at + 16 * x, v);
+                                    }
+                                } else {
+#pragma unroll 1
+                                    for (int x = 0; x < 2; ++x) {
+                                        uint4 v[4];
+#pragma unroll
+                                        for (int y = 0; y < 4; ++y)
+                                            v[y] = q4::times(*reinterpret_cast<const uint4 *>(
+                                                                 row + ((q4::kTail + 64 * x + 16 * y) ^ sw)),
+                                                             down);
+                                        tmem_st_words(at + 16 * x, v);
+                                    }
                                 }
-                                tmem_st_words(col + 64 * st + 16 * p, v);
                             }
                             tc::tmem_wait_st();
                             tc::tc_fence_before();
@@ -474,25 +491,24 @@ attn_weight_kernel(const __grid_constant__ MassArgs a) {
                     if (!ok) break;
                     tc::tc_fence_after();
                     const bool there = (ms->present[g % kPresent][warp] >> lane) & 1u;
+                    const float scr = Q4 ? sc * q4::pow2(ms->up[g % kPresent][32 * warp + lane] + 8) : sc;
                     float sum[2] = {0.0f, 0.0f};
-#pragma unroll
-                    for (int hh = 0; hh < 2; ++hh) {
-                        float v[32];
-                        tc::tmem_ld32(lane_addr + 64 * acc + 32 * hh, v);
+#pragma unroll 1
+                    for (int h = 0; h < 64; h += 16) {
+                        float v[16];
+                        tc::tmem_ld16(lane_addr + 64 * acc + h, v);
                         tc::tmem_wait_ld();
-                        if (hh) {
-                            tc::tc_fence_before();
-                            tc::mbar_arrive(&ms->acc_empty[acc]);
-                        }
 #pragma unroll
-                        for (int y = 0; y < 32; y += 4) {
-                            const float4 l = *reinterpret_cast<const float4 *>(lse2 + 32 * hh + y);
-                            sum[0] += tc::ex2_approx(fmaf(v[y], sc, -l.x));
-                            sum[1] += tc::ex2_approx(fmaf(v[y + 1], sc, -l.y));
-                            sum[0] += tc::ex2_approx(fmaf(v[y + 2], sc, -l.z));
-                            sum[1] += tc::ex2_approx(fmaf(v[y + 3], sc, -l.w));
+                        for (int y = 0; y < 16; y += 4) {
+                            const float4 l = *reinterpret_cast<const float4 *>(lse2 + h + y);
+                            sum[0] += tc::ex2_approx(fmaf(v[y], scr, -l.x));
+                            sum[1] += tc::ex2_approx(fmaf(v[y + 1], scr, -l.y));
+                            sum[0] += tc::ex2_approx(fmaf(v[y + 2], scr, -l.z));
+                            sum[1] += tc::ex2_approx(fmaf(v[y + 3], scr, -l.w));
                         }
                     }
+                    tc::tc_fence_before();
+                    tc::mbar_arrive(&ms->acc_empty[acc]);
                     // NaN counts as 0; more than one a head only an lse that is not the attention's can give
                     const float all = sum[0] + sum[1], most = (float)a.H;
                     out[(int64_t)j * kTile + 32 * warp + lane] =
@@ -566,12 +582,12 @@ __global__ void __launch_bounds__(kSumThreads) attn_mass_kernel(const __grid_con
         }
         __syncthreads();
     }
-    const double unit = 1.0 / (double)a.fixed;
+    const float unit = 1.0f / a.fixed;  // a power of two
     for (int i = tid; i < n; i += kSumThreads) {
         const int64_t o = (int64_t)b * a.max_rows + r0 + i;
         const float old = a.mass ? a.mass[o] : 0.0f;
         const unsigned long long sum = acc[i];
-        if (sum) a.out[o] = old + (float)((double)sum * unit);
+        if (sum) a.out[o] = old + __ull2float_rn(sum) * unit;
         else if (a.out != a.mass) a.out[o] = old;
     }
 }

@@ -49,25 +49,32 @@ __device__ __forceinline__ float2 scales2(uint16_t two) {
     return __half22float2(*reinterpret_cast<const __half2 *>(&h));
 }
 
-// Eight codes times their group's scale: four pairs of neighbouring dims. A
+// Eight codes as four pairs of neighbouring dims, 2^126 below their values. A
 // code's sign goes to bit 15 and the rest to bits 8-6 of its half: one product
 // with two powers of two makes both shifts (a multiplication, of which the SM
 // does as many as logical operations beside them; two shifts in its place made
 // the pairs take a quarter longer).
-__device__ __forceinline__ uint4 eight(uint32_t w, __nv_bfloat162 scale) {
+__device__ __forceinline__ uint4 eight_small(uint32_t w) {
     const uint32_t v = w >> 8, place = 0x81c081c0u;
-    const uint32_t bits[4] = {((w & 0x000f000fu) * 0x1040u) & place, ((w & 0x00f000f0u) * 0x104u) & place,
-                              ((v & 0x000f000fu) * 0x1040u) & place, ((v & 0x00f000f0u) * 0x104u) & place};
+    return make_uint4(((w & 0x000f000fu) * 0x1040u) & place, ((w & 0x00f000f0u) * 0x104u) & place,
+                      ((v & 0x000f000fu) * 0x1040u) & place, ((v & 0x00f000f0u) * 0x104u) & place);
+}
+
+__device__ __forceinline__ uint4 times(const uint4 &x, __nv_bfloat162 f) {
+    const uint32_t in[4] = {x.x, x.y, x.z, x.w};
     uint32_t out[4];
-    const uint32_t up = 0x7e807e80u;  // 2^126 twice
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 v = __hmul2(__hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&bits[i]),
-                                                 *reinterpret_cast<const __nv_bfloat162 *>(&up)),
-                                         scale);
+        const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&in[i]), f);
         out[i] = *reinterpret_cast<const uint32_t *>(&v);
     }
     return make_uint4(out[0], out[1], out[2], out[3]);
+}
+
+// Eight codes times their group's scale.
+__device__ __forceinline__ uint4 eight(uint32_t w, __nv_bfloat162 scale) {
+    const uint32_t up = 0x7e807e80u;  // 2^126 twice
+    return times(times(eight_small(w), *reinterpret_cast<const __nv_bfloat162 *>(&up)), scale);
 }
 
 // Dims 16 i .. 16 i + 15 of a row (i of 32) as bf16 pairs.
