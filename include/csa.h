@@ -720,8 +720,8 @@ csa_status_t csa_attn_mass_paged(const csa_bf16_t *q, const float *softmax_lse,
  * use stay, the lower page among equal sums, until keep_pages pages are held
  * with the former; the rest are given back: pages_out has CSA_PAGE_EVICTED in
  * their place, freed[b] lists their pool pages in the table's order (-1 padded)
- * and n_freed[b] is their number. Other entries are copied. Sums are formed in
- * 64 bits; one that is NaN ranks above all.
+ * and n_freed[b] is their number. Other entries are copied. Sums are held to
+ * 45 bits or more; one that is NaN ranks above all.
  * mass [batch, max_pages * page_size] fp32 (csa_attn_mass_paged), pages,
  * pages_out, freed [batch, max_pages], rows, n_freed [batch] int32; pages_out
  * may be pages itself, freed and n_freed may be NULL. A page that several

@@ -5,13 +5,17 @@
 //     2^e: e = floor(log2(max_g top_g / 6)) - 7 within [-100, 100],
 //     s_g = top_g / 6 / 2^e to e4m3, largest finite 448,
 //     code_d = |x_d| / (s_g 2^e) to the nearest of 0, 0.5, 1, 1.5, 2, 3, 4, 6,
-// ties to the even code. The nearest is found by comparing |x_d| with the seven
-// midpoints times the scale, which are exact products: a quotient would round
-// once more and could cross a midpoint. The rotary dims are rounded to bf16. A
+// ties to the even code. The quotient rounded to 32 bits decides as the exact one
+// does: midpoints are such numbers, and no other quotient by a scale of four
+// significant bits rounds to one of them (|x_d| one unit away is off by 2^-23 /
+// its mantissa, relative, half a unit of the quotient by 2^-24 / the
+// quotient's). It is the product with the scale's reciprocal and Markstein's
+// correction by the exact remainder. The rotary dims are rounded to bf16. A
 // group with a value that is not finite gets a NaN scale and reads as NaN.
 //
-// A warp takes a row, a lane one group: the lanes' 32 x 16 dims are the row's
-// 28 groups and 64 rotary dims, so the only exchange is one maximum.
+// A warp takes a row (four with many rows, for their loads to be on their way
+// together), a lane one group: the lanes' 32 x 16 dims are the row's 28 groups
+// and 64 rotary dims, so the only exchange is one maximum.
 #include "common.cuh"
 #include "internal.h"
 #include "paged.h"
@@ -27,9 +31,10 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kGroups = q4::kDims / q4::kGroup;
 
 // Row of the pool, or -1: padding, or absent (recorded unless evicted on purpose).
-__device__ __forceinline__ int64_t find_row(const Q4RowsArgs &a, int32_t t, bool writes) {
+__device__ __forceinline__ int64_t find_row(const Q4RowsArgs &a, int64_t t, bool writes) {
+    if (t >= a.T) return -1;
     const int32_t p = __ldg(a.row_pos + t);
-    const int32_t b = paged_seq(a.row_seq, a.batch, t, p);
+    const int32_t b = paged_seq(a.row_seq, a.batch, (int32_t)t, p);
     if (b == -2) report_error(a.err, kErrCheck, kKerCacheQ4, 1);
     if (b < 0) return -1;
     const uint32_t pg = (uint32_t)p / (uint32_t)a.page_size;
@@ -67,60 +72,89 @@ __device__ __forceinline__ void load16(const T *p, float (&x)[16]) {
     }
 }
 
-template <typename T, bool VEC>
+// Two values as codes: `a` in the low four bits.
+__device__ __forceinline__ uint32_t two_codes(float a, float b) {
+    uint32_t r;
+    asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %2, %1;\n\tcvt.u32.u8 %0, t;\n\t}"
+        : "=r"(r)
+        : "f"(a), "f"(b));
+    return r;
+}
+
+// ROWS rows a warp.
+template <typename T, bool VEC, int ROWS>
 __global__ void __launch_bounds__(kThreads) cache_append_q4_kernel(const __grid_constant__ Q4RowsArgs a) {
     __shared__ float tail_s[kWarps][64];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     float *tail = tail_s[warp];
     grid_dependency_wait();
     launch_dependents();
+    const int64_t t0 = ((int64_t)blockIdx.x * kWarps + warp) * ROWS;
+    float x[ROWS][16];
+#pragma unroll
+    for (int y = 0; y < ROWS; ++y)
+        if (t0 + y < a.T)
+            load16<T, VEC>(static_cast<const T *>(a.rows) + (t0 + y) * a.row_stride + 16 * lane, x[y]);
+    const int64_t found = lane < ROWS ? find_row(a, t0 + lane, true) : -1;
     const int np = a.n / 2;
     const uint64_t turns = lane < np ? fixed_turns(__ldg(a.inv_freq + lane)) : 0;
     // the pair of rotary dims that this lane turns, within the last 64
     const int d0 = a.off - q4::kDims + (a.half ? lane : 2 * lane), d1 = d0 + (a.half ? np : 1);
-    for (int64_t t = (int64_t)blockIdx.x * kWarps + warp; t < a.T; t += (int64_t)gridDim.x * kWarps) {
-        float x[16];
-        load16<T, VEC>(static_cast<const T *>(a.rows) + t * a.row_stride + 16 * lane, x);
-        const int64_t slot = find_row(a, (int32_t)t, true);
+#pragma unroll
+    for (int y = 0; y < ROWS; ++y) {
+        const int64_t slot = __shfl_sync(0xffffffffu, found, y);
         if (slot < 0) continue;
         uint8_t *row = a.cache + slot * q4::kRow;
-        float top = 0.0f;
-        bool fine = true;
+        // the largest magnitude, by its bits; of the finite values
+        uint32_t top = 0;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const float m = fabsf(x[i]);
-            const bool f = m <= 3.402823466e38f;
-            fine &= f;
-            top = fmaxf(top, f ? m : 0.0f);
+        for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(x[y][i]) & 0x7fffffffu);
+        const bool fine = top < 0x7f800000u;
+        if (!fine) {
+            top = 0;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const uint32_t m = __float_as_uint(x[y][i]) & 0x7fffffffu;
+                top = max(top, m < 0x7f800000u ? m : 0u);
+            }
         }
-        const float all = warp_max(lane < kGroups ? top : 0.0f);
+        const float all = __uint_as_float(__reduce_max_sync(0xffffffffu, lane < kGroups ? top : 0u));
         const int e = min(max((int)((__float_as_uint(__fdiv_rn(all, 6.0f)) >> 23) & 255u) - 127 - 7,
                               q4::kMinExp), q4::kMaxExp);
         if (lane < kGroups) {
-            const uint8_t s8 = fine ? (uint8_t)__nv_cvt_float_to_fp8(__fdiv_rn(top, 6.0f) * q4::pow2(-e),
-                                                                     __NV_SATFINITE, __NV_E4M3)
+            const uint8_t s8 = fine ? (uint8_t)__nv_cvt_float_to_fp8(
+                                          __fdiv_rn(__uint_as_float(top), 6.0f) * q4::pow2(-e), __NV_SATFINITE,
+                                          __NV_E4M3)
                                     : (uint8_t)0x7f;
-            const float s = q4::scales2(s8).x * q4::pow2(e);
-            uint32_t w[2] = {0u, 0u};
+            const float held = fine ? q4::scales2(s8).x * q4::pow2(e) : 0.0f;
+            const bool some = held > 0.0f;  // else a group that vanished, or without a scale: zeros
+            const float s = some ? held : 0.0f, inv = some ? __frcp_rn(s) : 0.0f;
+            const uint32_t keep = some ? 0xffffffffu : 0x80000000u;
+            float v[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                const float m = fabsf(x[i]);
-                uint32_t code = (m > 0.25f * s) + (m >= 0.75f * s) + (m > 1.25f * s) + (m >= 1.75f * s) +
-                                (m > 2.5f * s) + (m >= 3.5f * s) + (m > 5.0f * s);
-                if (!(s > 0.0f)) code = 0;  // a group that vanished, or without a scale
-                code |= (__float_as_uint(x[i]) >> 31) << 3;
-                w[i >> 3] |= code << (4 * ((i >> 1) & 3) + 16 * (i & 1));
+                const uint32_t bits = __float_as_uint(x[y][i]) & keep;
+                const float z = __uint_as_float(bits), q = z * inv;
+                const float r = fmaf(fmaf(-q, s, z), inv, q);
+                v[i] = __uint_as_float((__float_as_uint(r) & 0x7fffffffu) | (bits & 0x80000000u));
             }
+            uint32_t w[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                w[h] = two_codes(v[8 * h], v[8 * h + 2]) | two_codes(v[8 * h + 4], v[8 * h + 6]) << 8 |
+                       two_codes(v[8 * h + 1], v[8 * h + 3]) << 16 | two_codes(v[8 * h + 5], v[8 * h + 7]) << 24;
             reinterpret_cast<uint2 *>(row)[lane] = make_uint2(w[0], w[1]);
             row[q4::kScales + lane] = s8;
         } else {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) tail[16 * (lane - kGroups) + i] = x[i];
+            for (int i = 0; i < 4; ++i)
+                reinterpret_cast<float4 *>(tail)[4 * (lane - kGroups) + i] =
+                    make_float4(x[y][4 * i], x[y][4 * i + 1], x[y][4 * i + 2], x[y][4 * i + 3]);
             if (lane == kGroups) *reinterpret_cast<uint32_t *>(row + q4::kExp) = (uint32_t)(e + 127);
         }
         __syncwarp();
         if (lane < np) {
-            const float2 cs = cos_sin((int64_t)__ldg(a.row_pos + t) * a.pos_stride, turns, 1.0f, a.mscale);
+            const float2 cs = cos_sin((int64_t)__ldg(a.row_pos + t0 + y) * a.pos_stride, turns, 1.0f, a.mscale);
             const float u = tail[d0], v = tail[d1];
             tail[d0] = fmaf(u, cs.x, -v * cs.y);
             tail[d1] = fmaf(v, cs.x, u * cs.y);
@@ -132,37 +166,63 @@ __global__ void __launch_bounds__(kThreads) cache_append_q4_kernel(const __grid_
     }
 }
 
+template <int ROWS>
 __global__ void __launch_bounds__(kThreads) cache_read_q4_kernel(const __grid_constant__ Q4RowsArgs a) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     grid_dependency_wait();
     launch_dependents();
-    for (int64_t t = (int64_t)blockIdx.x * kWarps + warp; t < a.T; t += (int64_t)gridDim.x * kWarps) {
-        const int64_t slot = find_row(a, (int32_t)t, false);
-        uint4 v[2] = {};
-        if (slot >= 0) q4::sixteen(a.cache + slot * q4::kRow, lane, v);
-        uint4 *out = reinterpret_cast<uint4 *>(a.out + t * 512) + 2 * lane;
-        out[0] = v[0];
-        out[1] = v[1];
+    const int64_t t0 = ((int64_t)blockIdx.x * kWarps + warp) * ROWS;
+    const int64_t found = lane < ROWS ? find_row(a, t0 + lane, false) : -1;
+    q4::Sixteen v[ROWS];
+    int64_t slot[ROWS];
+#pragma unroll
+    for (int y = 0; y < ROWS; ++y) {
+        slot[y] = __shfl_sync(0xffffffffu, found, y);
+        if (slot[y] >= 0) v[y].load(a.cache + slot[y] * q4::kRow, lane);
+    }
+#pragma unroll
+    for (int y = 0; y < ROWS; ++y) {
+        if (t0 + y >= a.T) break;
+        uint4 *out = reinterpret_cast<uint4 *>(a.out + (t0 + y) * 512) + 2 * lane;
+        uint4 r[2] = {};
+        if (slot[y] >= 0) v[y].values(lane, r);
+        out[0] = r[0];
+        out[1] = r[1];
     }
 }
 
-unsigned row_blocks(int32_t T) { return (unsigned)(((int64_t)T + kWarps - 1) / kWarps); }
+// Four rows a warp while that leaves an SM sixteen warps.
+bool many_rows(int32_t T, int sms) { return T >= 64 * sms; }
+
+unsigned row_blocks(int32_t T, int rows) { return (unsigned)(((int64_t)T + kWarps * rows - 1) / (kWarps * rows)); }
+
+template <typename T, bool VEC>
+cudaError_t append_q4(const Q4RowsArgs &a, bool many, cudaStream_t stream) {
+    return many ? launch_early(cache_append_q4_kernel<T, VEC, 4>, dim3(row_blocks(a.T, 4)), dim3(kThreads), 0, stream, a)
+                : launch_early(cache_append_q4_kernel<T, VEC, 1>, dim3(row_blocks(a.T, 1)), dim3(kThreads), 0, stream, a);
+}
 
 }  // namespace
 
 cudaError_t launch_cache_append_q4(const Q4RowsArgs &a, cudaStream_t stream) {
+    int sms;
+    const cudaError_t e = sm_count(&sms);
+    if (e != cudaSuccess) return e;
     const int es = a.f32 ? 4 : 2;
     const bool vec = ((reinterpret_cast<uintptr_t>(a.rows) | (uintptr_t)(a.row_stride * es)) & 15u) == 0;
-    const dim3 grid(row_blocks(a.T)), block(kThreads);
-    if (a.f32)
-        return vec ? launch_early(cache_append_q4_kernel<float, true>, grid, block, 0, stream, a)
-                   : launch_early(cache_append_q4_kernel<float, false>, grid, block, 0, stream, a);
-    return vec ? launch_early(cache_append_q4_kernel<__nv_bfloat16, true>, grid, block, 0, stream, a)
-               : launch_early(cache_append_q4_kernel<__nv_bfloat16, false>, grid, block, 0, stream, a);
+    const bool many = many_rows(a.T, sms);
+    if (a.f32) return vec ? append_q4<float, true>(a, many, stream) : append_q4<float, false>(a, many, stream);
+    return vec ? append_q4<__nv_bfloat16, true>(a, many, stream)
+               : append_q4<__nv_bfloat16, false>(a, many, stream);
 }
 
 cudaError_t launch_cache_read_q4(const Q4RowsArgs &a, cudaStream_t stream) {
-    return launch_early(cache_read_q4_kernel, dim3(row_blocks(a.T)), dim3(kThreads), 0, stream, a);
+    int sms;
+    const cudaError_t e = sm_count(&sms);
+    if (e != cudaSuccess) return e;
+    return many_rows(a.T, sms)
+               ? launch_early(cache_read_q4_kernel<4>, dim3(row_blocks(a.T, 4)), dim3(kThreads), 0, stream, a)
+               : launch_early(cache_read_q4_kernel<1>, dim3(row_blocks(a.T, 1)), dim3(kThreads), 0, stream, a);
 }
 
 }  // namespace csa

@@ -77,20 +77,34 @@ __device__ __forceinline__ uint4 eight(uint32_t w, __nv_bfloat162 scale) {
     return times(times(eight_small(w), *reinterpret_cast<const __nv_bfloat162 *>(&up)), scale);
 }
 
-// Dims 16 i .. 16 i + 15 of a row (i of 32) as bf16 pairs.
-__device__ __forceinline__ void sixteen(const uint8_t *row, int i, uint4 (&v)[2]) {
-    if (i < kDims / kGroup) {
-        const uint2 w = __ldg(reinterpret_cast<const uint2 *>(row) + i);
-        const float unit = pow2((int)__ldg(row + kExp) - 127);
-        const __nv_bfloat162 s = scale_pair(scales2(__ldg(row + kScales + i)).x, unit);
-        v[0] = eight(w.x, s);
-        v[1] = eight(w.y, s);
-    } else {
-        const uint4 *p = reinterpret_cast<const uint4 *>(row + kTail) + 2 * (i - kDims / kGroup);
-        v[0] = __ldg(p);
-        v[1] = __ldg(p + 1);
+// Dims 16 i .. 16 i + 15 of a row (i of 32), as they are held and as bf16 pairs.
+struct Sixteen {
+    uint4 a, b;
+    uint32_t scale, exp;
+    __device__ __forceinline__ void load(const uint8_t *row, int i) {
+        if (i < kDims / kGroup) {
+            const uint2 w = __ldg(reinterpret_cast<const uint2 *>(row) + i);
+            a.x = w.x;
+            a.y = w.y;
+            scale = __ldg(row + kScales + i);
+            exp = __ldg(row + kExp);
+        } else {
+            const uint4 *p = reinterpret_cast<const uint4 *>(row + kTail) + 2 * (i - kDims / kGroup);
+            a = __ldg(p);
+            b = __ldg(p + 1);
+        }
     }
-}
+    __device__ __forceinline__ void values(int i, uint4 (&v)[2]) const {
+        if (i < kDims / kGroup) {
+            const __nv_bfloat162 s = scale_pair(scales2((uint16_t)scale).x, pow2((int)exp - 127));
+            v[0] = eight(a.x, s);
+            v[1] = eight(a.y, s);
+        } else {
+            v[0] = a;
+            v[1] = b;
+        }
+    }
+};
 
 }  // namespace q4
 }  // namespace csa
