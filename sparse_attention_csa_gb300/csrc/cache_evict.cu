@@ -7,11 +7,12 @@
 // heaviest stay while the budget lasts, the lower page among equals. The rest
 // are marked in the table and listed.
 //
-// One block a sequence. Groups of lanes sum a page each, as a 32-bit sum and
-// the sum of its rounding errors (each found exactly by Knuth's two-sum), so
-// that the order of the rows does not decide between two pages: 64-bit
-// additions, of which the SM does two a clock, made it 44 us for 512 pages and
-// 83 us for 64 sequences. The border between staying and going is found by
+// A cluster of blocks a sequence: they share its pages' sums, and the first one
+// chooses. Groups of lanes sum a page each, as a 32-bit sum and the sum of its
+// rounding errors (each found exactly by Knuth's two-sum), so that the order of
+// the rows does not decide between two pages: 64-bit additions, of which the SM
+// does two a clock, made it 44 us for 512 pages and 83 us for 64 sequences
+// (13.3 and 22.3 us with these sums and one block a sequence). The border between staying and going is found by
 // halving the interval of the sums' keys and counting, which ends as soon as a
 // value parts them right: some 12 counts for 512 pages, 64 at most (equal sums).
 #include "common.cuh"
@@ -22,7 +23,8 @@ namespace csa {
 
 namespace {
 
-constexpr int kThreads = 1024;
+constexpr int kThreads = 512;
+constexpr int kMine = 4;  // sums a thread keeps while the border is sought
 constexpr int kWarps = kThreads / 32;
 
 // A sum and what its roundings left out.
@@ -46,42 +48,67 @@ struct Sum {
     }
 };
 
-__global__ void __launch_bounds__(kThreads) cache_evict_kernel(const __grid_constant__ EvictArgs a) {
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// The address of `p` in the cluster's first block.
+__device__ __forceinline__ uint32_t in_first(const void *p) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"((uint32_t)__cvta_generic_to_shared(p)));
+    return r;
+}
+__device__ __forceinline__ void to_first(uint64_t *p, uint64_t v) {
+    asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(in_first(p)), "l"(v) : "memory");
+}
+__device__ __forceinline__ void add_to_first(int32_t *p, int32_t v) {
+    asm volatile("red.relaxed.cluster.shared::cluster.add.s32 [%0], %1;" ::"r"(in_first(p)), "r"(v) : "memory");
+}
+
+__global__ void __launch_bounds__(kThreads) cache_evict_kernel(const __grid_constant__ EvictArgs a, int32_t ranks) {
     extern __shared__ uint64_t key[];  // of each page: 0, stays or is not held
     __shared__ int32_t scan[kWarps + 1];
     __shared__ int32_t count[4];
-    __shared__ uint64_t ends[2][kWarps];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int32_t b = blockIdx.x, P = a.max_pages, page = a.page_size;
+    __shared__ uint32_t ends[2];
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int32_t rank = blockIdx.x % ranks;  // of the cluster
+    const int32_t b = blockIdx.x / ranks, P = a.max_pages, page = a.page_size;
     if (tid < 4) count[tid] = 0;
+    if (tid == 0) {
+        ends[0] = ~0u;
+        ends[1] = 0;
+    }
+    cluster_sync();  // the first block's counts are zero, and it is there
     grid_dependency_wait();
     launch_dependents();
     const int32_t *table = a.pages + (int64_t)b * P;
     int32_t rows = __ldg(a.rows + b);
     const int64_t cap = (int64_t)P * page;
     if (rows > cap) {
-        if (tid == 0) report_error(a.err, kErrCheck, kKerEvict, 1);
+        if (rank == 0 && tid == 0) report_error(a.err, kErrCheck, kKerEvict, 1);
         rows = (int32_t)cap;
     }
     rows = max(rows, 0);
     const int32_t used = (int32_t)(((int64_t)rows + page - 1) / page);
 
     // ---------------------------------------------------------- page weights
-    // 2^lg lanes a page, four dims a lane where pages and rows start on 16 bytes
+    // 2^lg lanes a page, with about four loads each (of four rows where pages and
+    // mass start on 16 bytes): more lanes spend more on adding their sums up
     const bool vec = page % 4 == 0 && (reinterpret_cast<uintptr_t>(a.mass) & 15u) == 0;
     const int units = vec ? page / 4 : page;
     int lg = 0;
-    while (lg < 5 && (1 << lg) < units) ++lg;
+    while (lg < 5 && (4 << lg) < units) ++lg;
     const int lanes = 1 << lg, li = lane & (lanes - 1), groups = kThreads >> lg;
     const float *mass = a.mass + (int64_t)b * cap;
     int32_t held_safe = 0, free_pages = 0;
-    constexpr int kAhead = 4;  // pages a group sums at a time
-    for (int32_t p0 = 0; p0 < used; p0 += groups * kAhead) {
+    constexpr int kAhead = 2;  // pages a group sums at a time
+    for (int32_t p0 = rank * groups; p0 < used; p0 += ranks * groups * kAhead) {
         Sum s[kAhead];
         int32_t phys[kAhead];
-        auto page_at = [&](int x) { return p0 + (x * groups) + (tid >> lg); };
+        auto page_at = [&](int x) { return p0 + x * ranks * groups + (tid >> lg); };
 #pragma unroll
         for (int x = 0; x < kAhead; ++x) phys[x] = page_at(x) < used ? table[page_at(x)] : -1;
+#pragma unroll 4
         for (int u = li; u < units; u += lanes) {
             float4 v[kAhead];
 #pragma unroll
@@ -110,20 +137,17 @@ __global__ void __launch_bounds__(kThreads) cache_evict_kernel(const __grid_cons
         }
 #pragma unroll
         for (int x = 0; x < kAhead; ++x) {
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
+            for (int o = lanes >> 1; o > 0; o >>= 1) {
                 const float hi = __shfl_xor_sync(0xffffffffu, s[x].hi, o);
                 const float lo = __shfl_xor_sync(0xffffffffu, s[x].lo, o);
-                if (o < lanes) {
-                    s[x].add(hi);
-                    s[x].lo += lo;
-                }
+                s[x].add(hi);
+                s[x].lo += lo;
             }
             const int32_t p = page_at(x);
             if (li == 0 && p < used) {
                 const int64_t first = (int64_t)p * page, end = first + page;
                 const bool safe = first < a.keep_first || end > max(rows - a.keep_last, 0);
-                key[p] = phys[x] >= 0 && !safe ? s[x].key() : 0ull;
+                to_first(&key[p], phys[x] >= 0 && !safe ? s[x].key() : 0ull);
                 held_safe += phys[x] >= 0 && safe;
                 free_pages += phys[x] >= 0 && !safe;
             }
@@ -131,12 +155,12 @@ __global__ void __launch_bounds__(kThreads) cache_evict_kernel(const __grid_cons
     }
     held_safe = __reduce_add_sync(0xffffffffu, held_safe);
     free_pages = __reduce_add_sync(0xffffffffu, free_pages);
-    __syncthreads();  // count is zero
     if (lane == 0) {
-        if (held_safe) atomicAdd(&count[0], held_safe);
-        if (free_pages) atomicAdd(&count[1], free_pages);
+        if (held_safe) add_to_first(&count[0], held_safe);
+        if (free_pages) add_to_first(&count[1], free_pages);
     }
-    __syncthreads();
+    cluster_sync();
+    if (rank != 0) return;
     held_safe = count[0];
     free_pages = count[1];
     const int32_t room = max(a.keep_pages - held_safe, 0);  // of the free pages, how many may stay
@@ -148,30 +172,26 @@ __global__ void __launch_bounds__(kThreads) cache_evict_kernel(const __grid_cons
     if (free_pages <= room) {
         border = 0;  // all stay
     } else if (room > 0) {
-        uint64_t lo = ~0ull, hi = 0;
+        // a thread's sums, and the first words of the smallest and the largest
+        uint64_t mine[kMine];
+        const bool few = used <= kMine * kThreads;
+        uint32_t least = ~0u, most = 0;
         for (int32_t p = tid; p < used; p += kThreads)
             if (key[p]) {
-                lo = min(lo, key[p]);
-                hi = max(hi, key[p]);
+                least = min(least, (uint32_t)(key[p] >> 32));
+                most = max(most, (uint32_t)(key[p] >> 32));
             }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            lo = min(lo, (uint64_t)__shfl_xor_sync(0xffffffffu, lo, o));
-            hi = max(hi, (uint64_t)__shfl_xor_sync(0xffffffffu, hi, o));
-        }
+        for (int i = 0; i < kMine; ++i) mine[i] = tid + i * kThreads < used ? key[tid + i * kThreads] : 0ull;
+        least = __reduce_min_sync(0xffffffffu, least);
+        most = __reduce_max_sync(0xffffffffu, most);
         if (lane == 0) {
-            ends[0][warp] = lo;
-            ends[1][warp] = hi;
+            atomicMin(&ends[0], least);
+            atomicMax(&ends[1], most);
         }
         __syncthreads();
         if (tid < 4) count[tid] = 0;
-        lo = ends[0][lane];
-        hi = ends[1][lane];
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            lo = min(lo, (uint64_t)__shfl_xor_sync(0xffffffffu, lo, o));
-            hi = max(hi, (uint64_t)__shfl_xor_sync(0xffffffffu, hi, o));
-        }
+        uint64_t lo = (uint64_t)ends[0] << 32, hi = (uint64_t)ends[1] << 32 | 0xffffffffu;
         __syncthreads();
         // at least `room` keys lie at lo or above, fewer above hi: the
         // room-th largest is in [lo, hi]
@@ -179,12 +199,18 @@ __global__ void __launch_bounds__(kThreads) cache_evict_kernel(const __grid_cons
         for (int step = 0; lo < hi && !exact; ++step) {
             const uint64_t mid = lo + (hi - lo) / 2 + 1;  // above lo
             int32_t n = 0;
-            for (int32_t p = tid; p < used; p += kThreads) n += key[p] >= mid;
-            n = __reduce_add_sync(0xffffffffu, n);
-            if (lane == 0 && n) atomicAdd(&count[step & 3], n);
-            if (tid == 0) count[(step + 2) & 3] = 0;
-            __syncthreads();
-            n = count[step & 3];
+            if (few) {
+#pragma unroll
+                for (int i = 0; i < kMine; ++i)
+                    if (i * kThreads < used) n += __syncthreads_count(mine[i] >= mid);
+            } else {
+                for (int32_t p = tid; p < used; p += kThreads) n += key[p] >= mid;
+                n = __reduce_add_sync(0xffffffffu, n);
+                if (lane == 0 && n) atomicAdd(&count[step & 3], n);
+                if (tid == 0) count[(step + 2) & 3] = 0;
+                __syncthreads();
+                n = count[step & 3];
+            }
             if (n >= room) lo = mid;
             else hi = mid - 1;
             exact = n == room;
@@ -241,7 +267,29 @@ cudaError_t launch_cache_evict(const EvictArgs &a, cudaStream_t stream) {
         if (e != cudaSuccess) return e;
         entered_context(pc, dev, ctx);
     }
-    return launch_early(cache_evict_kernel, dim3(a.batch), dim3(kThreads), (size_t)a.max_pages * 8, stream, a);
+    // as many blocks as their groups of lanes have pages, up to 8, while all of
+    // them fit the GPU (four an SM)
+    int sms, units = a.page_size % 4 == 0 ? a.page_size / 4 : a.page_size, lg = 0;
+    e = sm_count(&sms);
+    if (e != cudaSuccess) return e;
+    while (lg < 5 && (4 << lg) < units) ++lg;
+    int ranks = 1;
+    while (ranks < 8 && (int64_t)ranks * (kThreads >> lg) < a.max_pages && (int64_t)ranks * a.batch <= 2 * sms)
+        ranks *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ranks * a.batch);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = (size_t)a.max_pages * 8;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ranks;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, cache_evict_kernel, a, (int32_t)ranks);
 }
 
 }  // namespace csa

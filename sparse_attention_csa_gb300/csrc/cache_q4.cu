@@ -13,9 +13,10 @@
 // correction by the exact remainder. The rotary dims are rounded to bf16. A
 // group with a value that is not finite gets a NaN scale and reads as NaN.
 //
-// A warp takes a row (four with many rows, for their loads to be on their way
-// together), a lane one group: the lanes' 32 x 16 dims are the row's 28 groups
-// and 64 rotary dims, so the only exchange is one maximum.
+// A warp takes a row, a lane one group: the lanes' 32 x 16 dims are the row's 28
+// groups and 64 rotary dims, so the only exchange is one maximum. (Two or four
+// rows a warp took registers, hence warps on an SM: 16368 rows and their reading
+// back 15.8 us with one, 16.4 and 22.7.)
 #include "common.cuh"
 #include "internal.h"
 #include "paged.h"
@@ -81,91 +82,89 @@ __device__ __forceinline__ uint32_t two_codes(float a, float b) {
     return r;
 }
 
-// ROWS rows a warp.
-template <typename T, bool VEC, int ROWS>
-__global__ void __launch_bounds__(kThreads) cache_append_q4_kernel(const __grid_constant__ Q4RowsArgs a) {
-    __shared__ float tail_s[kWarps][64];
+// x / s rounded to 32 bits, inv being 1 / s rounded so (0 with s 0: 0). A zero
+// keeps its sign.
+__device__ __forceinline__ float quotient(float x, float s, float inv) {
+    const float q = x * inv;
+    return fmaf(-fmaf(q, s, -x), inv, q);
+}
+
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kThreads, 6) cache_append_q4_kernel(const __grid_constant__ Q4RowsArgs a) {
+    __shared__ alignas(16) float tail_s[kWarps][64];
+    __shared__ uint64_t turns_s[32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     float *tail = tail_s[warp];
     grid_dependency_wait();
     launch_dependents();
-    const int64_t t0 = ((int64_t)blockIdx.x * kWarps + warp) * ROWS;
-    float x[ROWS][16];
-#pragma unroll
-    for (int y = 0; y < ROWS; ++y)
-        if (t0 + y < a.T)
-            load16<T, VEC>(static_cast<const T *>(a.rows) + (t0 + y) * a.row_stride + 16 * lane, x[y]);
-    const int64_t found = lane < ROWS ? find_row(a, t0 + lane, true) : -1;
     const int np = a.n / 2;
-    const uint64_t turns = lane < np ? fixed_turns(__ldg(a.inv_freq + lane)) : 0;
+    if (warp == 0 && lane < np) turns_s[lane] = fixed_turns(__ldg(a.inv_freq + lane));  // once: 64-bit products
+    const int64_t t = (int64_t)blockIdx.x * kWarps + warp;
+    float x[16];
+    if (t < a.T) load16<T, VEC>(static_cast<const T *>(a.rows) + t * a.row_stride + 16 * lane, x);
+    const int64_t slot = find_row(a, t, true);
+    __syncthreads();
+    if (slot < 0) return;
+    const uint64_t turns = lane < np ? turns_s[lane] : 0;
     // the pair of rotary dims that this lane turns, within the last 64
     const int d0 = a.off - q4::kDims + (a.half ? lane : 2 * lane), d1 = d0 + (a.half ? np : 1);
+    uint8_t *row = a.cache + slot * q4::kRow;
+    // the largest magnitude, by its bits; of the finite values
+    uint32_t top = 0;
 #pragma unroll
-    for (int y = 0; y < ROWS; ++y) {
-        const int64_t slot = __shfl_sync(0xffffffffu, found, y);
-        if (slot < 0) continue;
-        uint8_t *row = a.cache + slot * q4::kRow;
-        // the largest magnitude, by its bits; of the finite values
-        uint32_t top = 0;
+    for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
+    const bool fine = top < 0x7f800000u;
+    if (!fine && lane < kGroups) {
+        top = 0;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(x[y][i]) & 0x7fffffffu);
-        const bool fine = top < 0x7f800000u;
-        if (!fine) {
-            top = 0;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const uint32_t m = __float_as_uint(x[y][i]) & 0x7fffffffu;
-                top = max(top, m < 0x7f800000u ? m : 0u);
-            }
+        for (int i = 0; i < 16; ++i) {
+            const uint32_t m = __float_as_uint(x[i]) & 0x7fffffffu;
+            top = max(top, m < 0x7f800000u ? m : 0u);
+            x[i] = copysignf(0.0f, x[i]);
         }
-        const float all = __uint_as_float(__reduce_max_sync(0xffffffffu, lane < kGroups ? top : 0u));
-        const int e = min(max((int)((__float_as_uint(__fdiv_rn(all, 6.0f)) >> 23) & 255u) - 127 - 7,
-                              q4::kMinExp), q4::kMaxExp);
-        if (lane < kGroups) {
-            const uint8_t s8 = fine ? (uint8_t)__nv_cvt_float_to_fp8(
-                                          __fdiv_rn(__uint_as_float(top), 6.0f) * q4::pow2(-e), __NV_SATFINITE,
-                                          __NV_E4M3)
-                                    : (uint8_t)0x7f;
-            const float held = fine ? q4::scales2(s8).x * q4::pow2(e) : 0.0f;
-            const bool some = held > 0.0f;  // else a group that vanished, or without a scale: zeros
-            const float s = some ? held : 0.0f, inv = some ? __frcp_rn(s) : 0.0f;
-            const uint32_t keep = some ? 0xffffffffu : 0x80000000u;
-            float v[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const uint32_t bits = __float_as_uint(x[y][i]) & keep;
-                const float z = __uint_as_float(bits), q = z * inv;
-                const float r = fmaf(fmaf(-q, s, z), inv, q);
-                v[i] = __uint_as_float((__float_as_uint(r) & 0x7fffffffu) | (bits & 0x80000000u));
-            }
-            uint32_t w[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                w[h] = two_codes(v[8 * h], v[8 * h + 2]) | two_codes(v[8 * h + 4], v[8 * h + 6]) << 8 |
-                       two_codes(v[8 * h + 1], v[8 * h + 3]) << 16 | two_codes(v[8 * h + 5], v[8 * h + 7]) << 24;
-            reinterpret_cast<uint2 *>(row)[lane] = make_uint2(w[0], w[1]);
-            row[q4::kScales + lane] = s8;
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                reinterpret_cast<float4 *>(tail)[4 * (lane - kGroups) + i] =
-                    make_float4(x[y][4 * i], x[y][4 * i + 1], x[y][4 * i + 2], x[y][4 * i + 3]);
-            if (lane == kGroups) *reinterpret_cast<uint32_t *>(row + q4::kExp) = (uint32_t)(e + 127);
-        }
-        __syncwarp();
-        if (lane < np) {
-            const float2 cs = cos_sin((int64_t)__ldg(a.row_pos + t0 + y) * a.pos_stride, turns, 1.0f, a.mscale);
-            const float u = tail[d0], v = tail[d1];
-            tail[d0] = fmaf(u, cs.x, -v * cs.y);
-            tail[d1] = fmaf(v, cs.x, u * cs.y);
-        }
-        __syncwarp();
-        reinterpret_cast<__nv_bfloat162 *>(row + q4::kTail)[lane] =
-            __floats2bfloat162_rn(tail[2 * lane], tail[2 * lane + 1]);
-        __syncwarp();
     }
+    const uint32_t all = __reduce_max_sync(0xffffffffu, lane < kGroups ? top : 0u);
+    // floor(log2(all / 6)) - 7: a sixth of a mantissa below 1.5 is below 1 / 4
+    const int e = min(max((int)(all >> 23) - 127 - 3 + ((all & 0x7fffffu) >= 0x400000u) - 7, q4::kMinExp),
+                      q4::kMaxExp);
+    if (lane < kGroups) {
+        const float scaled = fine ? quotient(__uint_as_float(top) * q4::pow2(-e), 6.0f, 1.0f / 6.0f) : 0.0f;
+        uint8_t s8 = (uint8_t)__nv_cvt_float_to_fp8(scaled, __NV_SATFINITE, __NV_E4M3);
+        const float s = q4::scales2(s8).x * q4::pow2(e);
+        const float inv = s > 0.0f ? __frcp_rn(s) : 0.0f;  // a group that vanished, or without a scale: zeros
+        if (!fine) s8 = 0x7f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = quotient(x[i], s, inv);
+        uint32_t w[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float *v = x + 8 * h;
+            w[h] = two_codes(v[0], v[2]) | two_codes(v[4], v[6]) << 8 | two_codes(v[1], v[3]) << 16 |
+                   two_codes(v[5], v[7]) << 24;
+        }
+        reinterpret_cast<uint2 *>(row)[lane] = make_uint2(w[0], w[1]);
+        row[q4::kScales + lane] = s8;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            reinterpret_cast<float4 *>(tail)[4 * (lane - kGroups) + i] =
+                make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+        if (lane == kGroups) *reinterpret_cast<uint32_t *>(row + q4::kExp) = (uint32_t)(e + 127);
+    }
+    __syncwarp();
+    if (lane < np) {
+        const float2 cs = cos_sin((int64_t)__ldg(a.row_pos + t) * a.pos_stride, turns, 1.0f, a.mscale);
+        const float u = tail[d0], v = tail[d1];
+        tail[d0] = fmaf(u, cs.x, -v * cs.y);
+        tail[d1] = fmaf(v, cs.x, u * cs.y);
+    }
+    __syncwarp();
+    reinterpret_cast<__nv_bfloat162 *>(row + q4::kTail)[lane] =
+        __floats2bfloat162_rn(tail[2 * lane], tail[2 * lane + 1]);
 }
 
+// A lane has two pieces of eight dims, 256 dims apart: a warp writes 512 bytes
+// at a time.
 template <int ROWS>
 __global__ void __launch_bounds__(kThreads) cache_read_q4_kernel(const __grid_constant__ Q4RowsArgs a) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -173,55 +172,44 @@ __global__ void __launch_bounds__(kThreads) cache_read_q4_kernel(const __grid_co
     launch_dependents();
     const int64_t t0 = ((int64_t)blockIdx.x * kWarps + warp) * ROWS;
     const int64_t found = lane < ROWS ? find_row(a, t0 + lane, false) : -1;
-    q4::Sixteen v[ROWS];
-    int64_t slot[ROWS];
+    q4::Eight v[ROWS][2];
 #pragma unroll
     for (int y = 0; y < ROWS; ++y) {
-        slot[y] = __shfl_sync(0xffffffffu, found, y);
-        if (slot[y] >= 0) v[y].load(a.cache + slot[y] * q4::kRow, lane);
+        const int64_t slot = __shfl_sync(0xffffffffu, found, y);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) v[y][h].load(slot < 0 ? nullptr : a.cache + slot * q4::kRow, lane + 32 * h);
     }
 #pragma unroll
     for (int y = 0; y < ROWS; ++y) {
         if (t0 + y >= a.T) break;
-        uint4 *out = reinterpret_cast<uint4 *>(a.out + (t0 + y) * 512) + 2 * lane;
-        uint4 r[2] = {};
-        if (slot[y] >= 0) v[y].values(lane, r);
-        out[0] = r[0];
-        out[1] = r[1];
+        uint4 *out = reinterpret_cast<uint4 *>(a.out + (t0 + y) * 512) + lane;
+        out[0] = v[y][0].values(lane);
+        out[32] = v[y][1].values(lane + 32);
     }
 }
-
-// Four rows a warp while that leaves an SM sixteen warps.
-bool many_rows(int32_t T, int sms) { return T >= 64 * sms; }
 
 unsigned row_blocks(int32_t T, int rows) { return (unsigned)(((int64_t)T + kWarps * rows - 1) / (kWarps * rows)); }
 
 template <typename T, bool VEC>
-cudaError_t append_q4(const Q4RowsArgs &a, bool many, cudaStream_t stream) {
-    return many ? launch_early(cache_append_q4_kernel<T, VEC, 4>, dim3(row_blocks(a.T, 4)), dim3(kThreads), 0, stream, a)
-                : launch_early(cache_append_q4_kernel<T, VEC, 1>, dim3(row_blocks(a.T, 1)), dim3(kThreads), 0, stream, a);
+cudaError_t append_q4(const Q4RowsArgs &a, cudaStream_t stream) {
+    return launch_early(cache_append_q4_kernel<T, VEC>, dim3(row_blocks(a.T, 1)), dim3(kThreads), 0, stream, a);
 }
 
 }  // namespace
 
 cudaError_t launch_cache_append_q4(const Q4RowsArgs &a, cudaStream_t stream) {
-    int sms;
-    const cudaError_t e = sm_count(&sms);
-    if (e != cudaSuccess) return e;
     const int es = a.f32 ? 4 : 2;
     const bool vec = ((reinterpret_cast<uintptr_t>(a.rows) | (uintptr_t)(a.row_stride * es)) & 15u) == 0;
-    const bool many = many_rows(a.T, sms);
-    if (a.f32) return vec ? append_q4<float, true>(a, many, stream) : append_q4<float, false>(a, many, stream);
-    return vec ? append_q4<__nv_bfloat16, true>(a, many, stream)
-               : append_q4<__nv_bfloat16, false>(a, many, stream);
+    if (a.f32) return vec ? append_q4<float, true>(a, stream) : append_q4<float, false>(a, stream);
+    return vec ? append_q4<__nv_bfloat16, true>(a, stream) : append_q4<__nv_bfloat16, false>(a, stream);
 }
 
 cudaError_t launch_cache_read_q4(const Q4RowsArgs &a, cudaStream_t stream) {
     int sms;
     const cudaError_t e = sm_count(&sms);
     if (e != cudaSuccess) return e;
-    return many_rows(a.T, sms)
-               ? launch_early(cache_read_q4_kernel<4>, dim3(row_blocks(a.T, 4)), dim3(kThreads), 0, stream, a)
+    return a.T >= 64 * sms  // two rows a warp while that leaves an SM 32 warps
+               ? launch_early(cache_read_q4_kernel<2>, dim3(row_blocks(a.T, 2)), dim3(kThreads), 0, stream, a)
                : launch_early(cache_read_q4_kernel<1>, dim3(row_blocks(a.T, 1)), dim3(kThreads), 0, stream, a);
 }
 

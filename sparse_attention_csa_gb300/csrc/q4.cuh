@@ -77,32 +77,22 @@ __device__ __forceinline__ uint4 eight(uint32_t w, __nv_bfloat162 scale) {
     return times(times(eight_small(w), *reinterpret_cast<const __nv_bfloat162 *>(&up)), scale);
 }
 
-// Dims 16 i .. 16 i + 15 of a row (i of 32), as they are held and as bf16 pairs.
-struct Sixteen {
-    uint4 a, b;
-    uint32_t scale, exp;
-    __device__ __forceinline__ void load(const uint8_t *row, int i) {
-        if (i < kDims / kGroup) {
-            const uint2 w = __ldg(reinterpret_cast<const uint2 *>(row) + i);
-            a.x = w.x;
-            a.y = w.y;
-            scale = __ldg(row + kScales + i);
+// Dims 8 i .. 8 i + 7 of a row (i of 64), as they are held and as bf16 pairs.
+struct Eight {
+    uint4 v = {0, 0, 0, 0};
+    uint32_t scale = 0, exp = 0;
+    __device__ __forceinline__ void load(const uint8_t *row, int i) {  // nullptr: zeros
+        if (!row) return;
+        if (i < kDims / 8) {
+            v.x = __ldg(reinterpret_cast<const uint32_t *>(row) + i);
+            scale = __ldg(row + kScales + i / 2);
             exp = __ldg(row + kExp);
         } else {
-            const uint4 *p = reinterpret_cast<const uint4 *>(row + kTail) + 2 * (i - kDims / kGroup);
-            a = __ldg(p);
-            b = __ldg(p + 1);
+            v = __ldg(reinterpret_cast<const uint4 *>(row + kTail) + (i - kDims / 8));
         }
     }
-    __device__ __forceinline__ void values(int i, uint4 (&v)[2]) const {
-        if (i < kDims / kGroup) {
-            const __nv_bfloat162 s = scale_pair(scales2((uint16_t)scale).x, pow2((int)exp - 127));
-            v[0] = eight(a.x, s);
-            v[1] = eight(a.y, s);
-        } else {
-            v[0] = a;
-            v[1] = b;
-        }
+    __device__ __forceinline__ uint4 values(int i) const {
+        return i < kDims / 8 ? eight(v.x, scale_pair(scales2((uint16_t)scale).x, pow2((int)exp - 127))) : v;
     }
 };
 
