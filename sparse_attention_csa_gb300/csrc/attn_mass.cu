@@ -186,12 +186,16 @@ attn_weight_kernel(const __grid_constant__ MassArgs a) {
     tc::tc_fence_before();
 
     // ------------------------------------------------ this CTA's run of tiles
-    int32_t total = 0;
-    int64_t N = 0;
+    const bool one_scan = a.T <= kThreads;
+    Slots sl = {-1, 0, 0};
+    int32_t nt = 0, total = 0;
+    int64_t N = 0, b = 0;  // tiles in all, and before the thread's token
     for (int32_t t0 = 0; t0 < a.T; t0 += kThreads) {
         const int32_t t = t0 + tid;
-        const int32_t nt = t < a.T ? (token_slots(a, t, c == 0).n + kTile - 1) / kTile : 0;
-        block_exclusive_scan<kThreads>(nt, ms->scan, &total);
+        sl = {-1, 0, 0};
+        if (t < a.T) sl = token_slots(a, t, c == 0);
+        nt = (sl.n + kTile - 1) / kTile;
+        b = block_exclusive_scan<kThreads>(nt, ms->scan, &total);
         N += total;
     }
     tc::tc_fence_after();
@@ -203,16 +207,20 @@ attn_weight_kernel(const __grid_constant__ MassArgs a) {
         if (warp == kMmaWarp) tc::tmem_dealloc(tmem, F::kCols);
         return;
     }
-    int64_t base = 0;  // the token holding tile s
-    for (int32_t t0 = 0; t0 < a.T && base <= s; t0 += kThreads) {
-        const int32_t t = t0 + tid;
-        const int32_t nt = t < a.T ? (token_slots(a, t, false).n + kTile - 1) / kTile : 0;
-        const int64_t bt = base + block_exclusive_scan<kThreads>(nt, ms->scan, &total);
-        if (bt <= s && s < bt + nt) {
-            ms->run_t = t;
-            ms->run_base = bt;
+    if (one_scan) {
+        if (b <= s && s < b + nt) ms->run_t = tid;
+    } else {  // the token holding tile s
+        int64_t base = 0;
+        for (int32_t t0 = 0; t0 < a.T && base <= s; t0 += kThreads) {
+            const int32_t t = t0 + tid;
+            const int32_t k = t < a.T ? (token_slots(a, t, false).n + kTile - 1) / kTile : 0;
+            const int64_t bt = base + block_exclusive_scan<kThreads>(k, ms->scan, &total);
+            if (bt <= s && s < bt + k) {
+                ms->run_t = t;
+                ms->run_base = bt;
+            }
+            base += total;
         }
-        base += total;
     }
     __syncthreads();
 
@@ -221,25 +229,29 @@ attn_weight_kernel(const __grid_constant__ MassArgs a) {
     int64_t done = s;
     while (done < e) {
         // ------------------------------------------------- a batch of tokens
-        {
-            const int32_t t_first = ms->run_t, t = t_first + tid;
-            const int64_t b0 = ms->run_base;
-            Slots sl = {-1, 0, 0};
+        const int32_t t_first = ms->run_t;
+        int32_t t = tid;
+        int x = tid - t_first;  // place in the batch
+        if (!one_scan) {
+            const int64_t base = ms->run_base;
+            t = t_first + tid;
+            x = tid;
+            sl = {-1, 0, 0};
             if (tid < kPieces && t < a.T) sl = token_slots(a, t, false);
-            const int32_t nt = (sl.n + kTile - 1) / kTile;
-            const int64_t b = b0 + block_exclusive_scan<kThreads>(nt, ms->scan, &total);
-            if (tid < kPieces && t < a.T && b < e) {  // a token without tiles has an empty piece
-                ms->piece[tid] = {t, (int32_t)max(s - b, (int64_t)0), (int32_t)min(e - b, (int64_t)nt), sl};
-                if (tid == kPieces - 1 || t + 1 == a.T || b + nt >= e) {
-                    ms->n_pieces = tid + 1;
-                    ms->done = min(e, b + nt);
-                }
+            nt = (sl.n + kTile - 1) / kTile;
+            b = base + block_exclusive_scan<kThreads>(nt, ms->scan, &total);
+        }
+        if (x >= 0 && x < kPieces && t < a.T && b < e) {  // a token without tiles has an empty piece
+            ms->piece[x] = {t, (int32_t)max(s - b, (int64_t)0), (int32_t)min(e - b, (int64_t)nt), sl};
+            if (x == kPieces - 1 || t + 1 == a.T || b + nt >= e) {
+                ms->n_pieces = x + 1;
+                ms->done = min(e, b + nt);
             }
-            if (tid == 0) {
-                ms->run_t = t_first + kPieces;
-                ms->run_base = b0 + total;
-            }
-            __syncthreads();
+        }
+        __syncthreads();
+        if (tid == 0) {
+            ms->run_t = t_first + kPieces;
+            if (!one_scan) ms->run_base += total;
         }
         done = ms->done;
         const int32_t n_pieces = ms->n_pieces;
@@ -535,6 +547,7 @@ attn_weight_kernel(const __grid_constant__ MassArgs a) {
 // ---------------------------------------------------------------------- sums
 constexpr int kSumThreads = 256;
 constexpr int kSumRows = 2048;
+constexpr int kMine = kSumRows / kSumThreads;  // rows a thread finishes
 constexpr int kTokens = 512;  // of the sequence, known at a time
 
 __global__ void __launch_bounds__(kSumThreads) attn_mass_kernel(const __grid_constant__ MassArgs a) {
@@ -543,11 +556,19 @@ __global__ void __launch_bounds__(kSumThreads) attn_mass_kernel(const __grid_con
     __shared__ int32_t n_tokens;
     const int tid = threadIdx.x;
     const int32_t b = blockIdx.y, r0 = blockIdx.x * kSumRows, n = min(kSumRows, a.max_rows - r0);
+    const int64_t row = (int64_t)b * a.max_rows + r0;
+    const bool in_place = a.out == a.mass;
     for (int i = tid; i < n; i += kSumThreads) acc[i] = 0;
     if (tid == 0) n_tokens = 0;
     __syncthreads();
     grid_dependency_wait();
     launch_dependents();
+    // what the sums are added to is on its way while they are formed (in place
+    // only rows with weight are touched)
+    float old[kMine];
+#pragma unroll
+    for (int i = 0; i < kMine; ++i)
+        old[i] = !in_place && a.mass && tid + i * kSumThreads < n ? __ldg(a.mass + row + tid + i * kSumThreads) : 0.0f;
     for (int32_t t0 = 0; t0 < a.T; t0 += kTokens) {
         // the sequence's tokens, in any order: sums have none
 #pragma unroll
@@ -571,24 +592,34 @@ __global__ void __launch_bounds__(kSumThreads) attn_mass_kernel(const __grid_con
             const float *w = a.weights + (int64_t)token[k] * a.slot_pad;
             if (a.idx) {
                 const int32_t *list = a.idx + (int64_t)token[k] * a.topk;
+                const int32_t end = min(r0 + n, seen[k]);
+#pragma unroll 4
                 for (int32_t i = tid; i < slots[k]; i += kSumThreads) {
                     const int32_t r = __ldg(list + i);
-                    if (r >= r0 && r < min(r0 + n, seen[k])) atomicAdd(&acc[r - r0], __float2ull_rn(w[i] * a.fixed));
+                    const float x = w[i];
+                    if (r >= r0 && r < end && x != 0.0f) atomicAdd(&acc[r - r0], __float2ull_rn(x * a.fixed));
                 }
             } else {  // a thread always has the same rows
                 const int32_t m = min(n, slots[k] - r0);
+#pragma unroll 4
                 for (int32_t i = tid; i < m; i += kSumThreads) acc[i] += __float2ull_rn(w[r0 + i] * a.fixed);
             }
         }
         __syncthreads();
     }
     const float unit = 1.0f / a.fixed;  // a power of two
-    for (int i = tid; i < n; i += kSumThreads) {
-        const int64_t o = (int64_t)b * a.max_rows + r0 + i;
-        const float old = a.mass ? a.mass[o] : 0.0f;
-        const unsigned long long sum = acc[i];
-        if (sum) a.out[o] = old + __ull2float_rn(sum) * unit;
-        else if (a.out != a.mass) a.out[o] = old;
+    if (in_place) {
+#pragma unroll
+        for (int i = 0; i < kMine; ++i)
+            if (tid + i * kSumThreads < n && acc[tid + i * kSumThreads]) old[i] = a.out[row + tid + i * kSumThreads];
+    }
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+        const int r = tid + i * kSumThreads;
+        if (r >= n) break;
+        const unsigned long long sum = acc[r];
+        if (sum) a.out[row + r] = old[i] + __ull2float_rn(sum) * unit;
+        else if (!in_place) a.out[row + r] = old[i];
     }
 }
 
