@@ -70,13 +70,17 @@ struct Piece {
 };
 
 // Q4 false: chunks of 128 rows x 128 dims in bf16 in shared memory. true: tiles
-// of 4-bit rows there (raw), chunks in tensor memory.
+// of 4-bit rows there (raw), chunks of 256 dims in tensor memory. (A chunk costs
+// the issuing thread some 600 clocks besides its MMAs, in a wait, a commit and
+// their latencies: with chunks of 128 dims six long contexts took 47.7 us.)
 template <bool Q4>
 struct Form {
     static constexpr int kMmaWarp = Q4 ? 16 : 8;  // behind 4 epilogue, 4 loader and (Q4) 8 spread warps
     static constexpr int kThreads = 32 * (kMmaWarp + 1);
     static constexpr int kRaw = Q4 ? 2 : 0;
-    static constexpr int kChunks = Q4 ? 6 : 3;    // 64 columns or 32 KB each
+    static constexpr int kPerTile = Q4 ? 2 : 4;   // chunks
+    static constexpr int kChunks = 3;             // at a time, of 128 columns or 32 KB
+    static constexpr int kMmas = 32 / kPerTile;   // of a chunk, 16 dims each
     static constexpr uint32_t kQ = 64 * 512 * 2;
     static constexpr uint32_t kOffQ = 0;          // two tokens' heads
     static constexpr uint32_t kOffRows = 2 * kQ;
@@ -85,7 +89,7 @@ struct Form {
     static constexpr uint32_t kOffMisc = kOffRows + (Q4 ? kRaw * kRawTile : kChunks * kChunkBytes);
     static constexpr uint32_t kColChunk = 64 * kAcc;
     static constexpr uint32_t kCols = Q4 ? 512 : 128;
-    static_assert(!Q4 || kColChunk + 64 * kChunks <= kCols, "tensor memory");
+    static_assert(!Q4 || kColChunk + 128 * kChunks <= kCols, "tensor memory");
 };
 
 template <bool Q4>
@@ -95,7 +99,7 @@ struct Misc {
     uint64_t raw_full[2], raw_empty[2];
     uint64_t chunk_full[F::kChunks], chunk_empty[F::kChunks];
     uint64_t acc_full[kAcc], acc_empty[kAcc];
-    uint64_t present_full[kPresent];
+    uint64_t present_full[kPresent];  // which slots have a row (loaders) and their powers of two (spread warps)
     uint64_t drain;
     int64_t run_base, done;
     int32_t run_t, n_pieces;
@@ -164,7 +168,7 @@ attn_weight_kernel(const __grid_constant__ MassArgs a) {
             tc::mbar_init(&ms->acc_full[i], 1);
             tc::mbar_init(&ms->acc_empty[i], 128);
         }
-        for (int i = 0; i < kPresent; ++i) tc::mbar_init(&ms->present_full[i], 4);
+        for (int i = 0; i < kPresent; ++i) tc::mbar_init(&ms->present_full[i], Q4 ? 8 : 4);
         tc::mbar_init(&ms->drain, 1);
         ms->abort = 0;
         tc::fence_mbar_init();
@@ -272,18 +276,19 @@ attn_weight_kernel(const __grid_constant__ MassArgs a) {
                         const uint32_t acc = g % kAcc;
                         ok = cx.wait(&ms->acc_empty[acc], ((g / kAcc) & 1) ^ 1, 22);
 #pragma unroll 1
-                        for (uint32_t ch = 0; ch < 4 && ok; ++ch) {
-                            const uint32_t cc = 4 * g + ch, st = cc % kChunks;
-                            ok = cx.wait(&ms->chunk_full[st], (cc / kChunks) & 1, 21);
+                        for (uint32_t ch = 0; ch < F::kPerTile && ok; ++ch) {
+                            const uint32_t cc = F::kPerTile * g + ch, st = cc % kChunks;
+                            ok = tc::mbar_test(&ms->chunk_full[st], (cc / kChunks) & 1) ||
+                                 cx.wait(&ms->chunk_full[st], (cc / kChunks) & 1, 21);
                             if (!ok) break;
                             if constexpr (!Q4) tc::fence_proxy_async_smem();
                             tc::tc_fence_after();
-                            const uint64_t bq = tc::desc_add(db, (np & 1) * F::kQ + ch * 16384);
+                            const uint64_t bq = tc::desc_add(db, (np & 1) * F::kQ + ch * (F::kMmas * 2048));
 #pragma unroll
-                            for (int kk = 0; kk < 8; ++kk) {
+                            for (int kk = 0; kk < F::kMmas; ++kk) {
                                 const uint64_t b = tc::desc_add(bq, (kk >> 2) * 8192 + (kk & 3) * 32);
                                 if constexpr (Q4)
-                                    mma_bf16_ta(tmem + 64 * acc, tmem + F::kColChunk + 64 * st + 8 * kk, b, id,
+                                    mma_bf16_ta(tmem + 64 * acc, tmem + F::kColChunk + 128 * st + 8 * kk, b, id,
                                                 (ch | kk) != 0);
                                 else
                                     tc::mma_bf16(tmem + 64 * acc,
@@ -322,56 +327,56 @@ attn_weight_kernel(const __grid_constant__ MassArgs a) {
                         // codes times this times their scale are the row over 2^(up + 8)
                         const float unit = q4::pow2(118 + min(ex - kMinUp, 0));
                         const __nv_bfloat162 down = __float2bfloat162_rn(q4::pow2(-max(ex, kMinUp) - 8));
-                        if (set == 0) ms->up[g % kPresent][32 * quarter + lane] = (int8_t)max(ex, kMinUp);
+                        if (set == 0) {
+                            ms->up[g % kPresent][32 * quarter + lane] = (int8_t)max(ex, kMinUp);
+                            __syncwarp();
+                            if (lane == 0) tc::mbar_arrive(&ms->present_full[g % kPresent]);
+                        }
+                        const uint32_t cc = 2 * g + set, st = cc % kChunks;
+                        ok = __all_sync(0xffffffffu,
+                                        cx.wait(&ms->chunk_empty[st], ((cc / kChunks) & 1) ^ 1, 51));
+                        if (!ok) break;
+                        tc::tc_fence_after();
+                        // four groups' scales at a time, of two pieces of 32 dims
 #pragma unroll 1
-                        for (int ch = set; ch < 4; ch += 2) {
-                            const uint32_t cc = 4 * g + ch, st = cc % kChunks;
-                            ok = __all_sync(0xffffffffu,
-                                            cx.wait(&ms->chunk_empty[st], ((cc / kChunks) & 1) ^ 1, 51));
-                            if (!ok) break;
-                            tc::tc_fence_after();
-                            // four groups' scales at a time, of two pieces of 32 dims
-#pragma unroll 1
-                            for (int p = 0; p < 2; ++p) {
-                                const int piece = 4 * ch + 2 * p;
-                                const uint32_t at = col + 64 * st + 32 * p;
-                                if (piece < 14) {
-                                    const uint32_t four = *reinterpret_cast<const uint32_t *>(
-                                        row + ((q4::kScales + 2 * piece) ^ sw));
+                        for (int p = 0; p < 4; ++p) {
+                            const int piece = 8 * set + 2 * p;
+                            const uint32_t at = col + 128 * st + 32 * p;
+                            if (piece < 14) {
+                                const uint32_t four = *reinterpret_cast<const uint32_t *>(
+                                    row + ((q4::kScales + 2 * piece) ^ sw));
 #pragma unroll
-                                    for (int x = 0; x < 2; ++x) {
-                                        const uint4 w =
-                                            *reinterpret_cast<const uint4 *>(row + ((16 * (piece + x)) ^ sw));
-                                        const float2 f = q4::scales2((uint16_t)(four >> (16 * x)));
-                                        const __nv_bfloat162 s0 = q4::scale_pair(f.x, unit);
-                                        const __nv_bfloat162 s1 = q4::scale_pair(f.y, unit);
-                                        const uint4 v[4] = {q4::times(q4::eight_small(w.x), s0),
-                                                            q4::times(q4::eight_small(w.y), s0),
-                                                            q4::times(q4::eight_small(w.z), s1),
-                                                            q4::times(q4::eight_small(w.w), s1)};
-                                        tmem_st_words(at + 16 * x, v);
-                                    }
-                                } else {
+                                for (int x = 0; x < 2; ++x) {
+                                    const uint4 w = *reinterpret_cast<const uint4 *>(row + ((16 * (piece + x)) ^ sw));
+                                    const float2 f = q4::scales2((uint16_t)(four >> (16 * x)));
+                                    const __nv_bfloat162 s0 = q4::scale_pair(f.x, unit);
+                                    const __nv_bfloat162 s1 = q4::scale_pair(f.y, unit);
+                                    const uint4 v[4] = {q4::times(q4::eight_small(w.x), s0),
+                                                        q4::times(q4::eight_small(w.y), s0),
+                                                        q4::times(q4::eight_small(w.z), s1),
+                                                        q4::times(q4::eight_small(w.w), s1)};
+                                    tmem_st_words(at + 16 * x, v);
+                                }
+                            } else {
 #pragma unroll 1
-                                    for (int x = 0; x < 2; ++x) {
-                                        uint4 v[4];
+                                for (int x = 0; x < 2; ++x) {
+                                    uint4 v[4];
 #pragma unroll
-                                        for (int y = 0; y < 4; ++y)
-                                            v[y] = q4::times(*reinterpret_cast<const uint4 *>(
-                                                                 row + ((q4::kTail + 64 * x + 16 * y) ^ sw)),
-                                                             down);
-                                        tmem_st_words(at + 16 * x, v);
-                                    }
+                                    for (int y = 0; y < 4; ++y)
+                                        v[y] = q4::times(*reinterpret_cast<const uint4 *>(
+                                                             row + ((q4::kTail + 64 * x + 16 * y) ^ sw)),
+                                                         down);
+                                    tmem_st_words(at + 16 * x, v);
                                 }
                             }
-                            tc::tmem_wait_st();
-                            tc::tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) tc::mbar_arrive(&ms->chunk_full[st]);
                         }
-                        if (!ok) break;
+                        tc::tmem_wait_st();
+                        tc::tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) tc::mbar_arrive(&ms->raw_empty[rs]);
+                        if (lane == 0) {
+                            tc::mbar_arrive(&ms->chunk_full[st]);
+                            tc::mbar_arrive(&ms->raw_empty[rs]);
+                        }
                     }
                 }
             }

@@ -59,6 +59,19 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t *bar, uint32_t parity,
     return ok != 0;
 }
 
+// Test the phase without sleeping.
+__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.b32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 // Suspend hint of a probe: 1 ms, or the wait's whole limit when that is shorter.
 __device__ __forceinline__ uint32_t probe_hint(uint64_t limit_ns) {
     return limit_ns < 1000000ull ? (uint32_t)(limit_ns > 0 ? limit_ns : 1) : 1000000u;
