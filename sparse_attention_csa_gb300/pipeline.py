@@ -17,7 +17,9 @@ side stream, joined before returning); nothing synchronises.
 
 ``csa_layer_decode`` continues sequences whose rows are cached: the new rows go
 to their slots (rotated on the way), the indexer chooses compressed rows, the
-attention reads the paged caches.
+attention reads the paged caches (compressed rows in bf16 or held in 4 bits), and
+the weight that the compressed rows received is added up where the cache keeps
+it. ``csa_layer_evict`` gives pages back by that weight.
 """
 
 from __future__ import annotations
@@ -26,9 +28,9 @@ from dataclasses import dataclass
 
 import torch
 
-from . import (csa_cache_append, csa_compress_cu_seqlens, csa_indexer_topk,
-               csa_indexer_topk_paged, csa_indexer_topk_workspace_size, csa_rope,
-               csa_sparse_mla_fwd, csa_sparse_mla_paged, csa_window_idx)
+from . import (csa_attn_mass_paged, csa_cache_append, csa_cache_evict, csa_compress_cu_seqlens,
+               csa_indexer_topk, csa_indexer_topk_paged, csa_indexer_topk_workspace_size, csa_rope,
+               csa_sparse_mla_fwd, csa_sparse_mla_paged, csa_sparse_mla_paged_q4, csa_window_idx)
 
 
 @dataclass
@@ -102,9 +104,12 @@ class PagedLayerCache:
     their own; the indexer's rows share the compressed rows' table."""
     ori: torch.Tensor                    # [pages, page_size, 512] bf16
     ori_pages: torch.Tensor              # [batch, max_pages] int32
-    cmp: torch.Tensor | None = None      # [pages, page_size, 512] bf16
+    cmp: torch.Tensor | None = None      # [pages, page_size, 512] bf16, or [.., 384] uint8 (4 bits)
     cmp_pages: torch.Tensor | None = None
     k_idx: torch.Tensor | None = None    # [pages, page_size, Di] bf16 (INDEXER layers)
+    # attention weight that the compressed rows received so far, where it is
+    # wanted: [batch, max_pages * page_size] fp32, zero for a new sequence
+    mass: torch.Tensor | None = None
 
 
 @dataclass
@@ -118,7 +123,7 @@ def csa_layer_decode(q, kv, cache: PagedLayerCache, q_seq, q_pos, sinks, softmax
                      cmp_ratio: int, ori_win_left: int, inv_freq=None, rope_layout="interleaved",
                      turn_back: bool = False, q_idx=None, w=None, topk: int = 0,
                      return_softmax_lse: bool = False, indexer_workspace=None,
-                     attention_workspace=None) -> DecodeOutputs:
+                     attention_workspace=None, mass_workspace=None) -> DecodeOutputs:
     """New tokens of one layer: q [T, H, 512] and their rows kv [T, 512] at
     positions ``q_pos`` [T] (negative: padding) of sequences ``q_seq`` [T]
     (None: token t is sequence t's).
@@ -134,7 +139,8 @@ def csa_layer_decode(q, kv, cache: PagedLayerCache, q_seq, q_pos, sinks, softmax
     before the call (``csa_cache_append`` with the group's number as position
     and ``pos_stride=cmp_ratio``), and with them the raw projections of the
     unfinished group, and of the one before it for overlapping layers, that
-    ``csa_compress_thd`` makes a row from; the rotation of the indexer's
+    ``csa_compress_thd`` makes a row from (``csa_cache_append_q4`` where
+    ``cache.cmp`` holds rows in 4 bits); the rotation of the indexer's
     queries and rows (``q_idx`` comes as the indexer takes it); an ``mscale``
     other than 1 (rotate by ``csa_rope`` and ``csa_cache_append``, and leave
     ``inv_freq`` and ``kv`` out)."""
@@ -147,10 +153,30 @@ def csa_layer_decode(q, kv, cache: PagedLayerCache, q_seq, q_pos, sinks, softmax
     if q_idx is not None:
         idx, _ = csa_indexer_topk_paged(q_idx, cache.k_idx, w, cache.cmp_pages, q_seq, q_pos,
                                         cmp_ratio, topk, workspace=indexer_workspace)
-    out, lse = csa_sparse_mla_paged(q, cache.ori, cache.cmp, idx, cache.ori_pages,
-                                    cache.cmp_pages, q_seq, q_pos, sinks, softmax_scale, cmp_ratio,
-                                    ori_win_left, return_softmax_lse=return_softmax_lse,
-                                    workspace=attention_workspace)
+    weigh = cache.mass is not None and cache.cmp is not None
+    attend = (csa_sparse_mla_paged_q4 if cache.cmp is not None and cache.cmp.dtype is torch.uint8
+              else csa_sparse_mla_paged)
+    out, lse = attend(q, cache.ori, cache.cmp, idx, cache.ori_pages, cache.cmp_pages, q_seq, q_pos,
+                      sinks, softmax_scale, cmp_ratio, ori_win_left,
+                      return_softmax_lse=return_softmax_lse or weigh,
+                      workspace=attention_workspace)
+    if weigh:
+        csa_attn_mass_paged(q, lse, cache.cmp, idx, cache.cmp_pages, q_seq, q_pos, cache.mass,
+                            softmax_scale, cmp_ratio, out=cache.mass, workspace=mass_workspace)
     if inv_freq is not None and turn_back:
         csa_rope(out, q_pos, inv_freq, layout=rope_layout, inverse=True, out=out)
-    return DecodeOutputs(out, lse, idx)
+    return DecodeOutputs(out, lse if return_softmax_lse else None, idx)
+
+
+def csa_layer_evict(cache: PagedLayerCache, rows, keep_pages: int, keep_first: int = 0,
+                    keep_last: int = 0):
+    """Gives back pages of compressed rows (and with them the indexer's) of every
+    sequence that holds more than ``keep_pages``: those whose rows received the
+    least attention weight by ``cache.mass``; ``rows`` [batch] int32 compressed
+    rows are in use (negative: leave the sequence alone). ``cache.cmp_pages`` is
+    changed in place. Returns ``(freed [batch, max_pages] pool pages, -1 padded,
+    n_freed [batch])``."""
+    _, freed, n_freed = csa_cache_evict(cache.mass, cache.cmp_pages, rows, keep_pages,
+                                        keep_first=keep_first, keep_last=keep_last,
+                                        out=cache.cmp_pages)
+    return freed, n_freed
