@@ -12,9 +12,12 @@
 // rounding errors (each found exactly by Knuth's two-sum), so that the order of
 // the rows does not decide between two pages: 64-bit additions, of which the SM
 // does two a clock, made it 44 us for 512 pages and 83 us for 64 sequences
-// (13.3 and 22.3 us with these sums and one block a sequence). The border between staying and going is found by
-// halving the interval of the sums' keys and counting, which ends as soon as a
-// value parts them right: some 12 counts for 512 pages, 64 at most (equal sums).
+// (13.3 and 22.3 us with these sums and one block a sequence). The border
+// between staying and going: one histogram over the interval of the sums' keys
+// leaves a few sums in the border's bin, which are ranked among themselves. More
+// than kCand of them (sums that are close, or equal, beside far ones) are parted
+// by halving the interval and counting, 64 counts at most. (Halving alone took
+// 8 to 20 counts of 500 clocks.)
 #include "common.cuh"
 #include "internal.h"
 #include "paged.h"
@@ -24,7 +27,8 @@ namespace csa {
 namespace {
 
 constexpr int kThreads = 512;
-constexpr int kMine = 4;  // sums a thread keeps while the border is sought
+constexpr int kBins = 2 * kThreads;
+constexpr int kCand = 256;
 constexpr int kWarps = kThreads / 32;
 
 // A sum and what its roundings left out.
@@ -70,6 +74,9 @@ __global__ void __launch_bounds__(kThreads) cache_evict_kernel(const __grid_cons
     __shared__ int32_t scan[kWarps + 1];
     __shared__ int32_t count[4];
     __shared__ uint32_t ends[2];
+    __shared__ int32_t bins[kBins];
+    __shared__ uint64_t cand[kCand], border_s;
+    __shared__ int32_t n_cand, equal_s, found[3];
     const int tid = threadIdx.x, lane = tid & 31;
     const int32_t rank = blockIdx.x % ranks;  // of the cluster
     const int32_t b = blockIdx.x / ranks, P = a.max_pages, page = a.page_size;
@@ -126,8 +133,7 @@ __global__ void __launch_bounds__(kThreads) cache_evict_kernel(const __grid_cons
                 }
             }
 #pragma unroll
-            for (int x = 0; x < kAhead; ++x)
-            {
+            for (int x = 0; x < kAhead; ++x) {
                 s[x].add(v[x].x);
                 if (!vec) continue;
                 s[x].add(v[x].y);
@@ -172,58 +178,92 @@ __global__ void __launch_bounds__(kThreads) cache_evict_kernel(const __grid_cons
     if (free_pages <= room) {
         border = 0;  // all stay
     } else if (room > 0) {
-        // a thread's sums, and the first words of the smallest and the largest
-        uint64_t mine[kMine];
-        const bool few = used <= kMine * kThreads;
+        // the first words of the smallest and the largest sum
         uint32_t least = ~0u, most = 0;
         for (int32_t p = tid; p < used; p += kThreads)
             if (key[p]) {
                 least = min(least, (uint32_t)(key[p] >> 32));
                 most = max(most, (uint32_t)(key[p] >> 32));
             }
-#pragma unroll
-        for (int i = 0; i < kMine; ++i) mine[i] = tid + i * kThreads < used ? key[tid + i * kThreads] : 0ull;
         least = __reduce_min_sync(0xffffffffu, least);
         most = __reduce_max_sync(0xffffffffu, most);
         if (lane == 0) {
             atomicMin(&ends[0], least);
             atomicMax(&ends[1], most);
         }
+        bins[2 * tid] = bins[2 * tid + 1] = 0;
+        if (tid == 0) n_cand = 0;
         __syncthreads();
         if (tid < 4) count[tid] = 0;
         uint64_t lo = (uint64_t)ends[0] << 32, hi = (uint64_t)ends[1] << 32 | 0xffffffffu;
+        // the bin of the room-th largest: equal keys share a bin, larger ones
+        // never fall lower
+        static_assert(kBins == 1 << 10, "bins");
+        const int shift = max(64 - __clzll((long long)(hi - lo)) - 10, 0);
+        for (int32_t p = tid; p < used; p += kThreads)
+            if (key[p]) atomicAdd(&bins[(key[p] - lo) >> shift], 1);
         __syncthreads();
-        // at least `room` keys lie at lo or above, fewer above hi: the
-        // room-th largest is in [lo, hi]
-        bool exact = false;
-        for (int step = 0; lo < hi && !exact; ++step) {
-            const uint64_t mid = lo + (hi - lo) / 2 + 1;  // above lo
-            int32_t n = 0;
-            if (few) {
-#pragma unroll
-                for (int i = 0; i < kMine; ++i)
-                    if (i * kThreads < used) n += __syncthreads_count(mine[i] >= mid);
-            } else {
+        {
+            const int top = kBins - 1 - 2 * tid;  // two bins a thread, from the highest down
+            const int32_t n0 = bins[top], n1 = bins[top - 1];
+            int32_t total;
+            const int32_t above = block_exclusive_scan<kThreads>(n0 + n1, scan, &total);
+            if (above < room && room <= above + n0 + n1) {
+                const bool first = room <= above + n0;
+                found[0] = first ? top : top - 1;
+                found[1] = first ? above : above + n0;
+                found[2] = first ? n0 : n1;
+            }
+        }
+        __syncthreads();
+        const int32_t need = room - found[1], there = found[2];
+        lo += (uint64_t)found[0] << shift;
+        hi = min(hi, lo + (((uint64_t)1 << shift) - 1));
+        bool exact = need == there;
+        if (!exact && there <= kCand) {
+            for (int32_t p = tid; p < used; p += kThreads)
+                if (key[p] >= lo && key[p] <= hi) cand[atomicAdd(&n_cand, 1)] = key[p];
+            __syncthreads();
+            if (tid < there) {
+                const uint64_t mine = cand[tid];
+                int32_t above = 0, from = 0;
+                for (int32_t i = 0; i < there; ++i) {
+                    above += cand[i] > mine;
+                    from += cand[i] >= mine;
+                }
+                if (above < need && need <= from) {  // equal keys write the same
+                    border_s = mine;
+                    equal_s = need - above;
+                }
+            }
+            __syncthreads();
+            border = border_s;
+            equal = equal_s;
+        } else {
+            // at least `room` keys lie at lo or above, fewer above hi
+            for (int step = 0; lo < hi && !exact; ++step) {
+                const uint64_t mid = lo + (hi - lo) / 2 + 1;  // above lo
+                int32_t n = 0;
                 for (int32_t p = tid; p < used; p += kThreads) n += key[p] >= mid;
                 n = __reduce_add_sync(0xffffffffu, n);
                 if (lane == 0 && n) atomicAdd(&count[step & 3], n);
                 if (tid == 0) count[(step + 2) & 3] = 0;
                 __syncthreads();
                 n = count[step & 3];
+                if (n >= room) lo = mid;
+                else hi = mid - 1;
+                exact = n == room;
             }
-            if (n >= room) lo = mid;
-            else hi = mid - 1;
-            exact = n == room;
-        }
-        border = lo;
-        if (exact) {
-            equal = INT32_MAX;
-        } else {  // how many of the keys at the border fit beside those above it
-            int32_t n = 0;
-            for (int32_t p = tid; p < used; p += kThreads) n += key[p] > border;
-            int32_t total;
-            block_exclusive_scan<kThreads>(n, scan, &total);
-            equal = room - total;
+            border = lo;
+            if (exact) {
+                equal = INT32_MAX;
+            } else {  // how many of the keys at the border fit beside those above it
+                int32_t n = 0;
+                for (int32_t p = tid; p < used; p += kThreads) n += key[p] > border;
+                int32_t total;
+                block_exclusive_scan<kThreads>(n, scan, &total);
+                equal = room - total;
+            }
         }
     }
 

@@ -80,6 +80,20 @@ def test_equal_sums_keep_the_lower_page():
         check(mass, table(lens, page, P, rng), lens, page, keep, in_place=True)
 
 
+def test_close_sums_beside_far_ones():
+    """More sums in one bin of the interval than are ranked at once: close
+    together, equal among them, beside a tiny and a huge one."""
+    rng = np.random.default_rng(1)
+    P, page = 3000, 4
+    lens = [P * page] * 2
+    mass = np.ones((2, P * page))
+    mass[0] += rng.integers(0, 60, P * page) * 2.0 ** -23     # few distinct sums
+    mass[1] += rng.random(P * page) * 2.0 ** -10
+    mass[:, :page], mass[:, page:2 * page] = 1e-30, 1e30
+    for keep in (1, 2, 700, 1500, 2999):
+        check(mass, table(lens, page, P, rng), lens, page, keep)
+
+
 def test_sums_of_any_kind():
     """Negative, tiny, infinite and NaN sums rank as numbers do, NaN above all."""
     rng = np.random.default_rng(2)
