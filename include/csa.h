@@ -531,9 +531,9 @@ csa_status_t csa_cache_append(const void *rows, csa_dtype_t dtype, int64_t row_s
  * visible to a token at position p are j < floor((p + 1) / cmp_ratio) of its
  * sequence, and topk_idx receives rows of the sequence (not of the pool), in
  * ascending order, -1 padded; a padding slot gets -1 (-inf) throughout. Rows
- * that the table holds no page for are recorded and rank last (-inf) where a
- * token is scored; one that sees at most topk rows is not, unless the values
- * are asked for, and selects them all.
+ * that the table holds no page for (recorded unless evicted) rank last (-inf)
+ * where a token is scored; one that sees at most topk rows is not, unless the
+ * values are asked for, and selects them all.
  * As in csa_indexer_topk a product that is NaN counts as 0; a score that is
  * NaN ranks above all others.
  * csa_indexer_topk_paged_workspace_size: bytes for the scores, 4 for every

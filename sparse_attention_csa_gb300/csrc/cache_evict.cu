@@ -18,6 +18,9 @@
 // than kCand of them (sums that are close, or equal, beside far ones) are parted
 // by halving the interval and counting, 64 counts at most. (Halving alone took
 // 8 to 20 counts of 500 clocks.)
+//
+// Bound by the latency of its steps: 512 pages of 64 rows 5.4 us, 64 sequences
+// of up to 1024 pages (8.6 MB) 13.9 us.
 #include "common.cuh"
 #include "internal.h"
 #include "paged.h"

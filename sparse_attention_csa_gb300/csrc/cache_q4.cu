@@ -17,6 +17,10 @@
 // groups and 64 rotary dims, so the only exchange is one maximum. (Two or four
 // rows a warp took registers, hence warps on an SM: 16368 rows and their reading
 // back 15.8 us with one, 16.4 and 22.7.)
+//
+// The append is bound by its 420 instructions a row, which issue 41 % of the time
+// behind the look-up of their slot (16368 bf16 rows, 23 MB: 9 us of the 15.8);
+// the read by memory and the look-up (40955 rows, 58 MB: 12.8 us, 4.5 TB/s).
 #include "common.cuh"
 #include "internal.h"
 #include "paged.h"

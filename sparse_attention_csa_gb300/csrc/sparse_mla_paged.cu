@@ -1,7 +1,7 @@
 // Sparse MLA attention of new tokens over paged caches (sm_103a, tcgen05
 // tensor cores, cp.async gathers): the keys of token t are the window rows of
 // its sequence in the original-KV cache and the listed (or every visible) rows
-// of the compressed cache.
+// of the compressed cache, which holds them in bf16 or in 4 bits (q4.cuh).
 //
 //     l_i = scale q.kv_i ; Z = sum e^(l_i - m) + e^(sink - m)
 //     out = sum e^(l_i - m) kv_i / Z ; lse = m + ln Z
@@ -45,6 +45,20 @@
 // Bound by HBM with long rows, by the latency of its steps with few tiles a
 // CTA. With 64 heads, join included: one token of 640 keys 12.8 us, 64 of them
 // 26.4 us, six long rows (225 MB read) 59.9 us or 3.8 TB/s.
+//
+// Compressed rows in 4 bits (Q4). The window's slots are padded to whole tiles,
+// so that a tile is of one kind. A tile of 4-bit rows comes to shared memory as
+// it is (24 KB, three on their way) and eight more warps turn it into a bf16
+// tile, of which two fit beside them; what follows is as above, over values
+// that bf16 holds exactly. The same cases: one token 14.8 us, 64 tokens 29.1,
+// long rows (85 MB read) 71.1 or 1.2 TB/s. Long rows are bound by a tile's way
+// through the two stages: turning it 2000 clocks beside the softmax (1320 by
+// itself), scores 1400 and 650 until they are seen, softmax 1400, O^T 830 and
+// 390; the tensor core is busy a quarter of the time. Measured on the way and
+// dropped, long rows: a bulk copy a row 100 us; the turning unrolled, four warps
+// of it 105, as a loop 73; stages filled and given back in quarters 89; codes
+// prefetched into registers in place of raw tiles, with three bf16 stages 74 to
+// 81; scores and O^T issued by two warps 71.2.
 #include "common.cuh"
 #include "internal.h"
 #include "paged.h"
@@ -74,7 +88,8 @@ constexpr int kFindWarp = 11;
 // Both forms of compressed rows: Q4 false, bf16; true, 4 bits.
 template <bool Q4>
 struct Form {
-    // 8 softmax and epilogue warps, 2 loaders, 1 MMA, 1 look-up, and 8 that turn 4-bit rows into bf16
+    // 8 softmax and epilogue warps, 2 loaders, 1 MMA, 1 look-up; with 4-bit rows
+    // 8 more that turn them into bf16
     static constexpr int kSpreadWarps = Q4 ? 8 : 0;
     static constexpr int kThreads = 384 + 32 * kSpreadWarps;
     static constexpr int kStages = Q4 ? 2 : 3;  // tiles in bf16
