@@ -693,9 +693,10 @@ csa_status_t csa_sparse_mla_paged_q4(
  * cmp_ratio < 2, total_tokens or batch > 65535, an unknown format, a list (or,
  * without one, a table) of more than 2^27 rows, q or cmp_cache not 16-byte
  * aligned, out overlapping mass without being mass -> CSA_ERR_UNSUPPORTED;
- * NULL out, or with tokens q/softmax_lse/cmp_cache/cmp_pages/q_pos ->
- * CSA_ERR_NULL; a short or misaligned workspace -> CSA_ERR_WORKSPACE. No
- * sequence or no page launches nothing; without tokens out receives mass.
+ * NULL out, or with tokens q/softmax_lse/cmp_cache/cmp_pages/q_pos (an empty
+ * pool may be NULL) -> CSA_ERR_NULL; a short or misaligned workspace ->
+ * CSA_ERR_WORKSPACE. A batch or a table of nothing launches nothing; without
+ * tokens out receives mass.
  */
 typedef enum { CSA_ROWS_BF16 = 0, CSA_ROWS_Q4 = 1 } csa_rows_t;
 

@@ -869,7 +869,7 @@ def csa_attn_mass_paged(q, softmax_lse, cmp_cache, cmp_sparse_indices, cmp_pages
 
     ``out`` may be ``mass`` (None: a new tensor). Returns out."""
     T, H, D = _dims(q, "q", 3)
-    n_pages, page, width = _dims(cmp_cache, "cmp_cache", 3)
+    n_pages, page, _ = _dims(cmp_cache, "cmp_cache", 3)
     batch, max_pages = _dims(cmp_pages, "cmp_pages", 2)
     dev = q.get_device()
     q4 = cmp_cache.dtype is torch.uint8

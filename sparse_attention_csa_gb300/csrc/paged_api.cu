@@ -412,7 +412,7 @@ csa_status_t csa_attn_mass_paged(const csa_bf16_t *q, const float *softmax_lse,
     if ((cmp_sparse_indices ? topk : max_rows) > kMaxKeys) return CSA_ERR_UNSUPPORTED;
     if (batch == 0 || max_rows == 0) return CSA_OK;  // no row to weigh
     if (!out) return CSA_ERR_NULL;
-    if (total_tokens > 0 && (!q || !softmax_lse || !cmp_cache || !cmp_pages || !q_pos))
+    if (total_tokens > 0 && (!q || !softmax_lse || !cmp_pages || !q_pos || (num_pages > 0 && !cmp_cache)))
         return CSA_ERR_NULL;
     if (misaligned(q, 16) || misaligned(cmp_cache, 16) || misaligned(mass, 4) || misaligned(out, 4))
         return CSA_ERR_UNSUPPORTED;

@@ -204,3 +204,50 @@ def test_offsets_beyond_32_bits():
     t = m.c.cmp_table
     m.c.cmp_table = t + np.where(t >= 0, 90000, 0).astype(np.int32)
     R.check(m.call(), *want, "mass")
+
+
+@pytest.mark.parametrize("mode", ["list", "all"])
+def test_wide_table_and_empty_pool(mode):
+    """A table much wider than its sequences, and one without any page."""
+    m = Mass([900, 50], 8, mode, topk=100, page=64, seed=31)
+    t = m.c.cmp_table
+    wide = np.full((2, 5000), -1, np.int32)
+    wide[:, :t.shape[1]] = t
+    m.c.cmp_table = wide
+    m.base = torch.rand((2, 5000 * 64), generator=torch.Generator().manual_seed(1)).cuda()
+    m.check()
+    m.c.cmp_table[:] = -1
+    m.rows = m.rows[:0]
+    got = m.call()
+    assert csa.csa_device_error()[0] == 6
+    assert torch.equal(got, m.base)
+
+
+def test_two_graphs_at_once_with_workspaces_of_their_own():
+    ms = [Mass([5000, 77], 64, "list", topk=512, seed=40 + i, bits=b) for i, b in enumerate((4, 16))]
+    want = [m.call() for m in ms]
+    graphs = []
+    for m in ms:
+        args, out = m.args(m.base), torch.empty_like(m.base)
+        ws = torch.empty(csa.csa_attn_mass_paged_workspace_size(2, 512), dtype=torch.uint8, device="cuda")
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=torch.cuda.Stream()):
+            csa.csa_attn_mass_paged(*args, out=out, workspace=ws)
+        graphs.append((g, args, ws, out))
+    streams = [torch.cuda.Stream() for _ in graphs]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for (g, *_), s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for (_, _, _, out), w in zip(graphs, want):
+        assert torch.equal(out, w)
+
+
+@pytest.mark.parametrize("bits", [4, 16])
+def test_more_tokens_than_threads(bits):
+    """More tokens than one pass over them holds, few of each sequence."""
+    rng = np.random.default_rng(50)
+    lens = rng.integers(5, 400, 650)
+    Mass(lens.tolist(), 4, "list", topk=20, new=2, page=16, seed=51, bits=bits).check()

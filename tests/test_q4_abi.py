@@ -11,6 +11,7 @@ import torch
 import sparse_attention_csa_gb300 as csa
 from tests import _q4_ref as Q
 from tests.test_paged_abi import L, NUL, P, caller  # noqa: F401
+from tests.test_paged_sources import kernels, test_nothing_is_read_before_the_wait as waits_first
 
 FAR = C.c_void_p(0x10000000)
 
@@ -82,6 +83,7 @@ def test_mass_rejects(L):  # noqa: F811
     assert call(out=C.c_void_p(0x10000 + 4)) == call(mass=C.c_void_p(0x10000000 + 508)) == 3
     assert call(ws=NUL) == call(wsb=need - 1) == call(ws=C.c_void_p(0x10010)) == 4
     assert call(batch=0) == call(maxp=0) == call(T=0, out=P) == 0
+    assert call(cmp=NUL, ws=NUL) == 1 and call(cmp=NUL, nump=0, ws=NUL) == 4  # an empty pool
 
 
 def test_evict_rejects(L):  # noqa: F811
@@ -140,3 +142,32 @@ def test_plain_format_round_trips():
     # the widest step (4 to 6) is a third of the scale's 6, the scale off by 2^-4
     assert (np.abs(g - h) <= top / 6 * (1 + 2.0 ** -4) + top * 2.0 ** -4).all()
     assert np.abs(h[np.abs(g) == top]).min() > 0
+
+
+@pytest.mark.parametrize("name,expected", [
+    ("cache_q4.cu", {"cache_append_q4_kernel", "cache_read_q4_kernel"}),
+    ("attn_mass.cu", {"attn_weight_kernel", "attn_mass_kernel"}),
+    ("cache_evict.cu", {"cache_evict_kernel"}),
+])
+def test_nothing_is_read_before_the_wait(name, expected):
+    """As in the paged kernels: what a launch that starts early touches lies
+    behind its wait for the kernels before it."""
+    waits_first(name, expected)
+    for kernel in expected:
+        body = kernels(name)[kernel]
+        ahead = body[:body.index("grid_dependency_wait();")]
+        for touch in ("token_slots(", "find_row(", "a.rows[", "a.pages[", "table["):
+            assert touch not in ahead, f"{kernel}: {touch} before the wait"
+
+
+def test_waits_of_whole_warps_are_voted():
+    """A warp's lanes go on alike after a wait of the weight kernel: every one
+    outside the thread that issues MMAs is voted on."""
+    body = kernels("attn_mass.cu")["attn_weight_kernel"]
+    one_lane = body[body.index("if (lane == 0) {\n                constexpr"):body.index("__syncwarp();\n        } else if")]
+    import re
+    rest = body.replace(one_lane, "")
+    waits = [" ".join(x.split()) for x in re.split(r"[;{}]", rest) if "cx.wait(" in x]
+    assert len(waits) == 6
+    for x in waits:
+        assert "__all_sync(0xffffffffu, cx.wait(" in x, x
