@@ -5,8 +5,8 @@
 //                 row j, and their heads h, of e^(scale q[t,h].k_j - lse[t,h])
 //
 // Two kernels. The first leaves the weight of every (token, key slot), heads
-// summed, in the workspace; the second adds a sequence's tokens up in an order
-// that does not depend on the launch.
+// summed, in the workspace; the second, one of two, adds a sequence's tokens up
+// to a result that does not depend on the launch.
 //
 // Weights. The 128-slot tiles of all tokens are dealt to the CTAs in equal
 // runs. A tile's rows are the MMA's M side, the heads its N side: S[j, h] =
@@ -18,13 +18,14 @@
 // rows and 64 KB of q a tile in place of 300 KB. Rows in bf16 are the operand
 // in shared memory as they come.
 //
-// Sums. A block has 2048 rows of one sequence. Weights are added as fixed-point
-// numbers of 64 bits, whose sums have no order (a row may be listed twice, and
-// by several tokens).
+// Sums. Weights are added as fixed-point numbers of 64 bits, whose sums have no
+// order (a row may be listed twice, and by several tokens). With lists a block
+// has 2048 rows of one sequence in shared memory; without them 1024 in
+// registers (six long rows 38.4 us; in shared memory as well 42.1).
 //
 // Bound by the latencies of both kernels' steps with few rows: one token of 512
-// listed rows 12.9 us. 81 tokens' 41472 bf16 rows (42 MB) 23.4 us: at most three
-// tiles a CTA, and the sums. Six long rows (84 MB in 4 bits) 42.1 us, 2.0 TB/s:
+// listed rows 12.5 us. 81 tokens' 41472 bf16 rows (42 MB) 22.8 us: at most three
+// tiles a CTA, and the sums. Six long rows (84 MB in 4 bits) 38.4 us, 2.2 TB/s:
 // 128 rows' MMAs take 67 clocks each, 2150 a tile, and the issuing thread some
 // 600 a chunk besides; the turning of the rows takes as long beside it.
 #include "common.cuh"
@@ -557,17 +558,82 @@ attn_weight_kernel(const __grid_constant__ MassArgs a) {
 }
 
 // ---------------------------------------------------------------------- sums
+// One block on an SM is asked for: left to itself the compiler keeps to 32
+// registers and spills (one token 14.0 us in place of 12.5).
 constexpr int kSumThreads = 256;
-constexpr int kSumRows = 2048;
-constexpr int kMine = kSumRows / kSumThreads;  // rows a thread finishes
 constexpr int kTokens = 512;  // of the sequence, known at a time
 
-__global__ void __launch_bounds__(kSumThreads) attn_mass_kernel(const __grid_constant__ MassArgs a) {
-    __shared__ unsigned long long acc[kSumRows];
+// Without lists: a thread's four rows keep their sums in registers.
+constexpr int kAllMine = 4;
+constexpr int kAllRows = kAllMine * kSumThreads;
+
+__global__ void __launch_bounds__(kSumThreads, 1) attn_mass_all_kernel(const __grid_constant__ MassArgs a) {
+    __shared__ int32_t token[kTokens], slots[kTokens];
+    __shared__ int32_t n_tokens;
+    const int tid = threadIdx.x;
+    const int32_t b = blockIdx.y, r0 = blockIdx.x * kAllRows, n = min(kAllRows, a.max_rows - r0);
+    const int64_t row = (int64_t)b * a.max_rows + r0;
+    const bool in_place = a.out == a.mass;
+    if (tid == 0) n_tokens = 0;
+    __syncthreads();
+    grid_dependency_wait();
+    launch_dependents();
+    // what the sums are added to is on its way while they are formed (in place
+    // only rows with weight are touched)
+    float old[kAllMine];
+    unsigned long long sum[kAllMine] = {};
+#pragma unroll
+    for (int i = 0; i < kAllMine; ++i)
+        old[i] = !in_place && a.mass && tid + i * kSumThreads < n ? __ldg(a.mass + row + tid + i * kSumThreads) : 0.0f;
+    for (int32_t t0 = 0; t0 < a.T; t0 += kTokens) {
+        // the sequence's tokens, in any order: sums have none
+#pragma unroll
+        for (int x = 0; x < kTokens; x += kSumThreads) {
+            const int32_t t = t0 + x + tid;
+            if (t < a.T) {
+                const Slots s = token_slots(a, t, false);
+                if (s.seq == b && s.n > r0) {
+                    const int32_t at = atomicAdd(&n_tokens, 1);
+                    token[at] = t;
+                    slots[at] = s.n;
+                }
+            }
+        }
+        __syncthreads();
+        const int32_t nt = n_tokens;
+        __syncthreads();
+        if (tid == 0) n_tokens = 0;
+        for (int32_t k = 0; k < nt; ++k) {
+            const float *w = a.weights + (int64_t)token[k] * a.slot_pad + r0;
+            const int32_t m = min(n, slots[k] - r0);
+            float x[kAllMine];
+#pragma unroll
+            for (int i = 0; i < kAllMine; ++i) x[i] = tid + i * kSumThreads < m ? w[tid + i * kSumThreads] : 0.0f;
+#pragma unroll
+            for (int i = 0; i < kAllMine; ++i) sum[i] += __float2ull_rn(x[i] * a.fixed);
+        }
+        __syncthreads();
+    }
+    const float unit = 1.0f / a.fixed;  // a power of two
+#pragma unroll
+    for (int i = 0; i < kAllMine; ++i) {
+        const int r = tid + i * kSumThreads;
+        if (r >= n) break;
+        if (sum[i]) a.out[row + r] = (in_place ? a.out[row + r] : old[i]) + __ull2float_rn(sum[i]) * unit;
+        else if (!in_place) a.out[row + r] = old[i];
+    }
+}
+
+// With lists: a block's rows keep their sums in shared memory.
+constexpr int kListRows = 2048;
+constexpr int kListMine = kListRows / kSumThreads;  // rows a thread finishes
+
+__global__ void __launch_bounds__(kSumThreads, 1) attn_mass_list_kernel(const __grid_constant__ MassArgs a) {
+    __shared__ unsigned long long acc[kListRows];
     __shared__ int32_t token[kTokens], slots[kTokens], seen[kTokens];
     __shared__ int32_t n_tokens;
     const int tid = threadIdx.x;
-    const int32_t b = blockIdx.y, r0 = blockIdx.x * kSumRows, n = min(kSumRows, a.max_rows - r0);
+    const int32_t b = blockIdx.y, r0 = blockIdx.x * kListRows, n = min(kListRows, a.max_rows - r0);
     const int64_t row = (int64_t)b * a.max_rows + r0;
     const bool in_place = a.out == a.mass;
     for (int i = tid; i < n; i += kSumThreads) acc[i] = 0;
@@ -577,9 +643,9 @@ __global__ void __launch_bounds__(kSumThreads) attn_mass_kernel(const __grid_con
     launch_dependents();
     // what the sums are added to is on its way while they are formed (in place
     // only rows with weight are touched)
-    float old[kMine];
+    float old[kListMine];
 #pragma unroll
-    for (int i = 0; i < kMine; ++i)
+    for (int i = 0; i < kListMine; ++i)
         old[i] = !in_place && a.mass && tid + i * kSumThreads < n ? __ldg(a.mass + row + tid + i * kSumThreads) : 0.0f;
     for (int32_t t0 = 0; t0 < a.T; t0 += kTokens) {
         // the sequence's tokens, in any order: sums have none
@@ -588,7 +654,7 @@ __global__ void __launch_bounds__(kSumThreads) attn_mass_kernel(const __grid_con
             const int32_t t = t0 + x + tid;
             if (t < a.T) {
                 const Slots s = token_slots(a, t, false);
-                if (s.seq == b && s.n > 0 && (a.idx || s.n > r0)) {
+                if (s.seq == b && s.n > 0) {
                     const int32_t at = atomicAdd(&n_tokens, 1);
                     token[at] = t;
                     slots[at] = s.n;
@@ -602,19 +668,13 @@ __global__ void __launch_bounds__(kSumThreads) attn_mass_kernel(const __grid_con
         if (tid == 0) n_tokens = 0;
         for (int32_t k = 0; k < nt; ++k) {
             const float *w = a.weights + (int64_t)token[k] * a.slot_pad;
-            if (a.idx) {
-                const int32_t *list = a.idx + (int64_t)token[k] * a.topk;
-                const int32_t end = min(r0 + n, seen[k]);
+            const int32_t *list = a.idx + (int64_t)token[k] * a.topk;
+            const int32_t end = min(r0 + n, seen[k]);
 #pragma unroll 4
-                for (int32_t i = tid; i < slots[k]; i += kSumThreads) {
-                    const int32_t r = __ldg(list + i);
-                    const float x = w[i];
-                    if (r >= r0 && r < end && x != 0.0f) atomicAdd(&acc[r - r0], __float2ull_rn(x * a.fixed));
-                }
-            } else {  // a thread always has the same rows
-                const int32_t m = min(n, slots[k] - r0);
-#pragma unroll 4
-                for (int32_t i = tid; i < m; i += kSumThreads) acc[i] += __float2ull_rn(w[r0 + i] * a.fixed);
+            for (int32_t i = tid; i < slots[k]; i += kSumThreads) {
+                const int32_t r = __ldg(list + i);
+                const float x = w[i];
+                if (r >= r0 && r < end && x != 0.0f) atomicAdd(&acc[r - r0], __float2ull_rn(x * a.fixed));
             }
         }
         __syncthreads();
@@ -622,11 +682,11 @@ __global__ void __launch_bounds__(kSumThreads) attn_mass_kernel(const __grid_con
     const float unit = 1.0f / a.fixed;  // a power of two
     if (in_place) {
 #pragma unroll
-        for (int i = 0; i < kMine; ++i)
+        for (int i = 0; i < kListMine; ++i)
             if (tid + i * kSumThreads < n && acc[tid + i * kSumThreads]) old[i] = a.out[row + tid + i * kSumThreads];
     }
 #pragma unroll
-    for (int i = 0; i < kMine; ++i) {
+    for (int i = 0; i < kListMine; ++i) {
         const int r = tid + i * kSumThreads;
         if (r >= n) break;
         const unsigned long long sum = acc[r];
@@ -666,8 +726,10 @@ cudaError_t launch_attn_mass(MassArgs a, cudaStream_t stream) {
         const cudaError_t e = a.q4 ? launch_weights<true>(a, stream) : launch_weights<false>(a, stream);
         if (e != cudaSuccess) return e;
     }
-    return launch_early(attn_mass_kernel, dim3((a.max_rows + kSumRows - 1) / kSumRows, a.batch),
-                        dim3(kSumThreads), 0, stream, a);
+    const auto sums = a.idx ? attn_mass_list_kernel : attn_mass_all_kernel;
+    const int rows = a.idx ? kListRows : kAllRows;
+    return launch_early(sums, dim3((unsigned)(((int64_t)a.max_rows + rows - 1) / rows), a.batch), dim3(kSumThreads), 0,
+                        stream, a);
 }
 
 }  // namespace csa

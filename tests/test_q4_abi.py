@@ -146,7 +146,7 @@ def test_plain_format_round_trips():
 
 @pytest.mark.parametrize("name,expected", [
     ("cache_q4.cu", {"cache_append_q4_kernel", "cache_read_q4_kernel"}),
-    ("attn_mass.cu", {"attn_weight_kernel", "attn_mass_kernel"}),
+    ("attn_mass.cu", {"attn_weight_kernel", "attn_mass_all_kernel", "attn_mass_list_kernel"}),
     ("cache_evict.cu", {"cache_evict_kernel"}),
 ])
 def test_nothing_is_read_before_the_wait(name, expected):
