@@ -12,15 +12,16 @@
 // rounding errors (each found exactly by Knuth's two-sum), so that the order of
 // the rows does not decide between two pages: 64-bit additions, of which the SM
 // does two a clock, made it 44 us for 512 pages and 83 us for 64 sequences
-// (13.3 and 22.3 us with these sums and one block a sequence). The border
+// (13.3 and 22.3 us with these sums and one block a sequence). A group has one
+// page at a time (two, with more loads on their way, take 0.5 and 2 us more). The border
 // between staying and going: one histogram over the interval of the sums' keys
 // leaves a few sums in the border's bin, which are ranked among themselves. More
 // than kCand of them (sums that are close, or equal, beside far ones) are parted
 // by halving the interval and counting, 64 counts at most. (Halving alone took
 // 8 to 20 counts of 500 clocks.)
 //
-// Bound by the latency of its steps: 512 pages of 64 rows 5.4 us, 64 sequences
-// of up to 1024 pages (8.6 MB) 13.9 us.
+// Bound by the latency of its steps: 512 pages of 64 rows 4.8 us, 64 sequences
+// of up to 1024 pages (8.6 MB) 9.8 us.
 #include "common.cuh"
 #include "internal.h"
 #include "paged.h"
@@ -111,55 +112,36 @@ __global__ void __launch_bounds__(kThreads) cache_evict_kernel(const __grid_cons
     const int lanes = 1 << lg, li = lane & (lanes - 1), groups = kThreads >> lg;
     const float *mass = a.mass + (int64_t)b * cap;
     int32_t held_safe = 0, free_pages = 0;
-    constexpr int kAhead = 2;  // pages a group sums at a time
-    for (int32_t p0 = rank * groups; p0 < used; p0 += ranks * groups * kAhead) {
-        Sum s[kAhead];
-        int32_t phys[kAhead];
-        auto page_at = [&](int x) { return p0 + x * ranks * groups + (tid >> lg); };
-#pragma unroll
-        for (int x = 0; x < kAhead; ++x) phys[x] = page_at(x) < used ? table[page_at(x)] : -1;
+    for (int32_t p0 = rank * groups; p0 < used; p0 += ranks * groups) {
+        const int32_t p = p0 + (tid >> lg);
+        const int32_t phys = p < used ? table[p] : -1;
+        const int64_t first = (int64_t)p * page, end = first + page;
+        Sum s;
 #pragma unroll 4
         for (int u = li; u < units; u += lanes) {
-            float4 v[kAhead];
-#pragma unroll
-            for (int x = 0; x < kAhead; ++x) {
-                const int64_t r = (int64_t)page_at(x) * page + (vec ? 4 * u : u);
-                v[x] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                if (r >= rows) continue;
-                if (vec) {
-                    v[x] = __ldg(reinterpret_cast<const float4 *>(mass + r));
-                    if (r + 1 >= rows) v[x].y = 0.0f;
-                    if (r + 2 >= rows) v[x].z = 0.0f;
-                    if (r + 3 >= rows) v[x].w = 0.0f;
-                } else {
-                    v[x].x = __ldg(mass + r);
-                }
-            }
-#pragma unroll
-            for (int x = 0; x < kAhead; ++x) {
-                s[x].add(v[x].x);
-                if (!vec) continue;
-                s[x].add(v[x].y);
-                s[x].add(v[x].z);
-                s[x].add(v[x].w);
+            const int64_t r = first + (vec ? 4 * u : u);
+            if (r >= rows) continue;
+            if (vec) {
+                const float4 v = __ldg(reinterpret_cast<const float4 *>(mass + r));
+                s.add(v.x);
+                s.add(r + 1 < rows ? v.y : 0.0f);
+                s.add(r + 2 < rows ? v.z : 0.0f);
+                s.add(r + 3 < rows ? v.w : 0.0f);
+            } else {
+                s.add(__ldg(mass + r));
             }
         }
-#pragma unroll
-        for (int x = 0; x < kAhead; ++x) {
-            for (int o = lanes >> 1; o > 0; o >>= 1) {
-                const float hi = __shfl_xor_sync(0xffffffffu, s[x].hi, o);
-                const float lo = __shfl_xor_sync(0xffffffffu, s[x].lo, o);
-                s[x].add(hi);
-                s[x].lo += lo;
-            }
-            const int32_t p = page_at(x);
-            if (li == 0 && p < used) {
-                const int64_t first = (int64_t)p * page, end = first + page;
-                const bool safe = first < a.keep_first || end > max(rows - a.keep_last, 0);
-                to_first(&key[p], phys[x] >= 0 && !safe ? s[x].key() : 0ull);
-                held_safe += phys[x] >= 0 && safe;
-                free_pages += phys[x] >= 0 && !safe;
-            }
+        for (int o = lanes >> 1; o > 0; o >>= 1) {
+            const float hi = __shfl_xor_sync(0xffffffffu, s.hi, o);
+            const float lo = __shfl_xor_sync(0xffffffffu, s.lo, o);
+            s.add(hi);
+            s.lo += lo;
+        }
+        if (li == 0 && p < used) {
+            const bool safe = first < a.keep_first || end > max(rows - a.keep_last, 0);
+            to_first(&key[p], phys >= 0 && !safe ? s.key() : 0ull);
+            held_safe += phys >= 0 && safe;
+            free_pages += phys >= 0 && !safe;
         }
     }
     held_safe = __reduce_add_sync(0xffffffffu, held_safe);
@@ -310,14 +292,14 @@ cudaError_t launch_cache_evict(const EvictArgs &a, cudaStream_t stream) {
         if (e != cudaSuccess) return e;
         entered_context(pc, dev, ctx);
     }
-    // as many blocks as their groups of lanes have pages, up to 8, while all of
-    // them fit the GPU (four an SM)
+    // as many blocks as their groups of lanes have pages, up to 8, while there are
+    // three an SM at most (64 sequences: 4 blocks each 9.8 us, 8 each 11.8)
     int sms, units = a.page_size % 4 == 0 ? a.page_size / 4 : a.page_size, lg = 0;
     e = sm_count(&sms);
     if (e != cudaSuccess) return e;
     while (lg < 5 && (4 << lg) < units) ++lg;
     int ranks = 1;
-    while (ranks < 8 && (int64_t)ranks * (kThreads >> lg) < a.max_pages && (int64_t)ranks * a.batch <= 2 * sms)
+    while (ranks < 8 && (int64_t)ranks * (kThreads >> lg) < a.max_pages && (int64_t)2 * ranks * a.batch <= 3 * sms)
         ranks *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ranks * a.batch);
