@@ -21,11 +21,11 @@
 // Sums. Weights are added as fixed-point numbers of 64 bits, whose sums have no
 // order (a row may be listed twice, and by several tokens). With lists a block
 // has 2048 rows of one sequence in shared memory; without them 1024 in
-// registers (six long rows 38.4 us; in shared memory as well 42.1).
+// registers (six long rows 38.2 us; in shared memory as well 42.1).
 //
 // Bound by the latencies of both kernels' steps with few rows: one token of 512
-// listed rows 12.5 us. 81 tokens' 41472 bf16 rows (42 MB) 22.8 us: at most three
-// tiles a CTA, and the sums. Six long rows (84 MB in 4 bits) 38.4 us, 2.2 TB/s:
+// listed rows 12.4 us. 81 tokens' 41472 bf16 rows (42 MB) 22.6 us: at most three
+// tiles a CTA, and the sums. Six long rows (84 MB in 4 bits) 38.2 us, 2.2 TB/s:
 // 128 rows' MMAs take 67 clocks each, 2150 a tile, and the issuing thread some
 // 600 a chunk besides; the turning of the rows takes as long beside it.
 #include "common.cuh"
@@ -559,7 +559,7 @@ attn_weight_kernel(const __grid_constant__ MassArgs a) {
 
 // ---------------------------------------------------------------------- sums
 // One block on an SM is asked for: left to itself the compiler keeps to 32
-// registers and spills (one token 14.0 us in place of 12.5).
+// registers and spills (one token 14.0 us in place of 12.4).
 constexpr int kSumThreads = 256;
 constexpr int kTokens = 512;  // of the sequence, known at a time
 

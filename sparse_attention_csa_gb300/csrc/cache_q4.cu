@@ -16,11 +16,12 @@
 // A warp takes a row, a lane one group: the lanes' 32 x 16 dims are the row's 28
 // groups and 64 rotary dims, so the only exchange is one maximum. (Two or four
 // rows a warp took registers, hence warps on an SM: 16368 rows and their reading
-// back 15.8 us with one, 16.4 and 22.7.)
+// back, in blocks of 256 threads, 15.8 us with one, 16.4 and 22.7. Blocks of 128
+// threads 15.2; warps that take rows in turn, the next one's on its way, spill.)
 //
 // The append is bound by its 420 instructions a row, which issue 41 % of the time
-// behind the look-up of their slot (16368 bf16 rows, 23 MB: 9 us of the 15.8);
-// the read by memory and the look-up (40955 rows, 58 MB: 12.8 us, 4.5 TB/s).
+// behind the look-up of their slot (16368 bf16 rows, 23 MB: 9 us of the 15.2);
+// the read by memory and the look-up (40955 rows, 58 MB: 12.6 us, 4.6 TB/s).
 #include "common.cuh"
 #include "internal.h"
 #include "paged.h"
@@ -31,7 +32,7 @@ namespace csa {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kGroups = q4::kDims / q4::kGroup;
 
@@ -94,7 +95,7 @@ __device__ __forceinline__ float quotient(float x, float s, float inv) {
 }
 
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(kThreads, 6) cache_append_q4_kernel(const __grid_constant__ Q4RowsArgs a) {
+__global__ void __launch_bounds__(kThreads, 12) cache_append_q4_kernel(const __grid_constant__ Q4RowsArgs a) {
     __shared__ alignas(16) float tail_s[kWarps][64];
     __shared__ uint64_t turns_s[32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
