@@ -13,15 +13,15 @@
 // the rows does not decide between two pages: 64-bit additions, of which the SM
 // does two a clock, made it 44 us for 512 pages and 83 us for 64 sequences
 // (13.3 and 22.3 us with these sums and one block a sequence). A group has one
-// page at a time (two, with more loads on their way, take 0.5 and 2 us more). The border
+// page at a time (two, with more loads on their way, took 0.5 and 2 us more). The border
 // between staying and going: one histogram over the interval of the sums' keys
 // leaves a few sums in the border's bin, which are ranked among themselves. More
 // than kCand of them (sums that are close, or equal, beside far ones) are parted
 // by halving the interval and counting, 64 counts at most. (Halving alone took
 // 8 to 20 counts of 500 clocks.)
 //
-// Bound by the latency of its steps: 512 pages of 64 rows 4.8 us, 64 sequences
-// of up to 1024 pages (8.6 MB) 9.8 us.
+// Bound by the latency of its steps: 512 pages of 64 rows 5.2 us, 64 sequences
+// of up to 1024 pages (8.6 MB) 11.4 us.
 #include "common.cuh"
 #include "internal.h"
 #include "paged.h"
@@ -293,7 +293,7 @@ cudaError_t launch_cache_evict(const EvictArgs &a, cudaStream_t stream) {
         entered_context(pc, dev, ctx);
     }
     // as many blocks as their groups of lanes have pages, up to 8, while there are
-    // three an SM at most (64 sequences: 4 blocks each 9.8 us, 8 each 11.8)
+    // three an SM at most (64 sequences: 4 blocks each 11.4 us, 8 each 12.0)
     int sms, units = a.page_size % 4 == 0 ? a.page_size / 4 : a.page_size, lg = 0;
     e = sm_count(&sms);
     if (e != cudaSuccess) return e;
