@@ -58,7 +58,8 @@
 // dropped, long rows: a bulk copy a row 100 us; the turning unrolled, four warps
 // of it 105, as a loop 73; stages filled and given back in quarters 89; codes
 // prefetched into registers in place of raw tiles, with three bf16 stages 74 to
-// 81; scores and O^T issued by two warps 71.2.
+// 81; scores and O^T issued by two warps 71.2; that over tiles of 32 keys, four
+// stages and scores twice buffered 70.0 (64 tokens 29.3).
 #include "common.cuh"
 #include "internal.h"
 #include "paged.h"
