@@ -681,8 +681,9 @@ csa_status_t csa_sparse_mla_paged_q4(
  * negative or not visible count nothing, and neither do rows without a page
  * (recorded unless evicted) and heads whose lse is -inf. A row's weight from
  * one token that is NaN counts as 0, one above the number of heads (an lse
- * that is not this attention's) as that number. Sums do not depend on the
- * order of the tokens' work: equal calls give equal bits.
+ * that is not this attention's) as that number; a token that lists a row more
+ * than three times with such an lse gives it no defined weight. Sums do not
+ * depend on the order of the tokens' work: equal calls give equal bits.
  * workspace: csa_attn_mass_paged_workspace_size(total_tokens, topk with
  * cmp_sparse_indices, else max_pages * page_size) bytes, 256-byte aligned; its
  * contents do not matter before the call and mean nothing after it, and calls
