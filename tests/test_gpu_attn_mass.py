@@ -85,8 +85,9 @@ def test_many_tokens(n_seq, new, mode):
     Mass(lens.tolist(), 8, mode, topk=96, new=new, page=32, seed=n_seq).check()
 
 
-def test_in_place_and_from_nothing():
-    m = Mass([500, 3000, 60], 16, "list", topk=40, new=2, seed=3)
+@pytest.mark.parametrize("mode", ["list", "all"])
+def test_in_place_and_from_nothing(mode):
+    m = Mass([500, 3000, 60], 16, mode, topk=40, new=2, seed=3)
     want = m.call()
     fresh = m.call(None)
     assert torch.equal(fresh, m.call(torch.zeros_like(m.base)))
