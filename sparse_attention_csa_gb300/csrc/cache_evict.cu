@@ -20,8 +20,8 @@
 // by halving the interval and counting, 64 counts at most. (Halving alone took
 // 8 to 20 counts of 500 clocks.)
 //
-// Bound by the latency of its steps: 512 pages of 64 rows 5.2 us, 64 sequences
-// of up to 1024 pages (8.6 MB) 11.4 us.
+// Bound by the latency of its steps: 512 pages of 64 rows 4.7 us, 64 sequences
+// of up to 1024 pages (8.6 MB) 10.2 us.
 #include "common.cuh"
 #include "internal.h"
 #include "paged.h"
@@ -72,12 +72,18 @@ __device__ __forceinline__ void to_first(uint64_t *p, uint64_t v) {
 __device__ __forceinline__ void add_to_first(int32_t *p, int32_t v) {
     asm volatile("red.relaxed.cluster.shared::cluster.add.s32 [%0], %1;" ::"r"(in_first(p)), "r"(v) : "memory");
 }
+__device__ __forceinline__ void min_to_first(uint32_t *p, uint32_t v) {
+    asm volatile("red.relaxed.cluster.shared::cluster.min.u32 [%0], %1;" ::"r"(in_first(p)), "r"(v) : "memory");
+}
+__device__ __forceinline__ void max_to_first(uint32_t *p, uint32_t v) {
+    asm volatile("red.relaxed.cluster.shared::cluster.max.u32 [%0], %1;" ::"r"(in_first(p)), "r"(v) : "memory");
+}
 
-__global__ void __launch_bounds__(kThreads) cache_evict_kernel(const __grid_constant__ EvictArgs a, int32_t ranks) {
+__global__ void __launch_bounds__(kThreads, 2) cache_evict_kernel(const __grid_constant__ EvictArgs a, int32_t ranks) {
     extern __shared__ uint64_t key[];  // of each page: 0, stays or is not held
     __shared__ int32_t scan[kWarps + 1];
-    __shared__ int32_t count[4];
-    __shared__ uint32_t ends[2];
+    __shared__ int32_t held[2], count[4];
+    __shared__ uint32_t ends[2];  // first words of the smallest and the largest sum
     __shared__ int32_t bins[kBins];
     __shared__ uint64_t cand[kCand], border_s;
     __shared__ int32_t n_cand, equal_s, found[3];
@@ -86,9 +92,12 @@ __global__ void __launch_bounds__(kThreads) cache_evict_kernel(const __grid_cons
     const int32_t b = blockIdx.x / ranks, P = a.max_pages, page = a.page_size;
     if (tid < 4) count[tid] = 0;
     if (tid == 0) {
+        held[0] = held[1] = 0;
         ends[0] = ~0u;
         ends[1] = 0;
+        n_cand = 0;
     }
+    bins[2 * tid] = bins[2 * tid + 1] = 0;
     cluster_sync();  // the first block's counts are zero, and it is there
     grid_dependency_wait();
     launch_dependents();
@@ -112,6 +121,7 @@ __global__ void __launch_bounds__(kThreads) cache_evict_kernel(const __grid_cons
     const int lanes = 1 << lg, li = lane & (lanes - 1), groups = kThreads >> lg;
     const float *mass = a.mass + (int64_t)b * cap;
     int32_t held_safe = 0, free_pages = 0;
+    uint32_t least = ~0u, most = 0;
     for (int32_t p0 = rank * groups; p0 < used; p0 += ranks * groups) {
         const int32_t p = p0 + (tid >> lg);
         const int32_t phys = p < used ? table[p] : -1;
@@ -139,47 +149,43 @@ __global__ void __launch_bounds__(kThreads) cache_evict_kernel(const __grid_cons
         }
         if (li == 0 && p < used) {
             const bool safe = first < a.keep_first || end > max(rows - a.keep_last, 0);
-            to_first(&key[p], phys >= 0 && !safe ? s.key() : 0ull);
+            uint64_t k = 0;
+            if (phys >= 0 && !safe) {
+                k = s.key();
+                least = min(least, (uint32_t)(k >> 32));
+                most = max(most, (uint32_t)(k >> 32));
+                ++free_pages;
+            }
+            to_first(&key[p], k);
             held_safe += phys >= 0 && safe;
-            free_pages += phys >= 0 && !safe;
         }
     }
     held_safe = __reduce_add_sync(0xffffffffu, held_safe);
     free_pages = __reduce_add_sync(0xffffffffu, free_pages);
+    least = __reduce_min_sync(0xffffffffu, least);
+    most = __reduce_max_sync(0xffffffffu, most);
     if (lane == 0) {
-        if (held_safe) add_to_first(&count[0], held_safe);
-        if (free_pages) add_to_first(&count[1], free_pages);
+        if (held_safe) add_to_first(&held[0], held_safe);
+        if (free_pages) {
+            add_to_first(&held[1], free_pages);
+            min_to_first(&ends[0], least);
+            max_to_first(&ends[1], most);
+        }
     }
     cluster_sync();
     if (rank != 0) return;
-    held_safe = count[0];
-    free_pages = count[1];
+    held_safe = held[0];
+    free_pages = held[1];
     const int32_t room = max(a.keep_pages - held_safe, 0);  // of the free pages, how many may stay
 
     // -------------------------------------------------------------- the border
-    // Pages with keys above `border` stay, and the first `equal` at it.
+    // Pages with keys above `border` stay, and the first `equal` at it (all, if
+    // INT32_MAX).
     uint64_t border = ~0ull;
     int32_t equal = 0;
     if (free_pages <= room) {
         border = 0;  // all stay
     } else if (room > 0) {
-        // the first words of the smallest and the largest sum
-        uint32_t least = ~0u, most = 0;
-        for (int32_t p = tid; p < used; p += kThreads)
-            if (key[p]) {
-                least = min(least, (uint32_t)(key[p] >> 32));
-                most = max(most, (uint32_t)(key[p] >> 32));
-            }
-        least = __reduce_min_sync(0xffffffffu, least);
-        most = __reduce_max_sync(0xffffffffu, most);
-        if (lane == 0) {
-            atomicMin(&ends[0], least);
-            atomicMax(&ends[1], most);
-        }
-        bins[2 * tid] = bins[2 * tid + 1] = 0;
-        if (tid == 0) n_cand = 0;
-        __syncthreads();
-        if (tid < 4) count[tid] = 0;
         uint64_t lo = (uint64_t)ends[0] << 32, hi = (uint64_t)ends[1] << 32 | 0xffffffffu;
         // the bin of the room-th largest: equal keys share a bin, larger ones
         // never fall lower
@@ -218,7 +224,7 @@ __global__ void __launch_bounds__(kThreads) cache_evict_kernel(const __grid_cons
                 }
                 if (above < need && need <= from) {  // equal keys write the same
                     border_s = mine;
-                    equal_s = need - above;
+                    equal_s = need == from ? INT32_MAX : need - above;
                 }
             }
             __syncthreads();
@@ -293,7 +299,7 @@ cudaError_t launch_cache_evict(const EvictArgs &a, cudaStream_t stream) {
         entered_context(pc, dev, ctx);
     }
     // as many blocks as their groups of lanes have pages, up to 8, while there are
-    // three an SM at most (64 sequences: 4 blocks each 11.4 us, 8 each 12.0)
+    // three an SM at most (64 sequences: 4 blocks each 10.4 us, 8 each 10.9)
     int sms, units = a.page_size % 4 == 0 ? a.page_size / 4 : a.page_size, lg = 0;
     e = sm_count(&sms);
     if (e != cudaSuccess) return e;
