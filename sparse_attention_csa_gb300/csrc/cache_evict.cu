@@ -13,12 +13,13 @@
 // the rows does not decide between two pages: 64-bit additions, of which the SM
 // does two a clock, made it 44 us for 512 pages and 83 us for 64 sequences
 // (13.3 and 22.3 us with these sums and one block a sequence). A group has one
-// page at a time (two, with more loads on their way, took 0.5 and 2 us more). The border
-// between staying and going: one histogram over the interval of the sums' keys
-// leaves a few sums in the border's bin, which are ranked among themselves. More
-// than kCand of them (sums that are close, or equal, beside far ones) are parted
-// by halving the interval and counting, 64 counts at most. (Halving alone took
-// 8 to 20 counts of 500 clocks.)
+// page at a time (two, with more loads on their way, took 0.5 and 2 us more).
+// The border between staying and going: one histogram over the interval of the
+// sums' keys, which is found with them, leaves a few sums in the border's bin,
+// which are ranked among themselves. More than kCand of them (sums that are
+// close, or equal, beside far ones) are parted by halving the interval and
+// counting, 64 counts at most. (Halving alone took 8 to 20 counts of 500
+// clocks.)
 //
 // Bound by the latency of its steps: 512 pages of 64 rows 4.7 us, 64 sequences
 // of up to 1024 pages (8.6 MB) 10.2 us.
