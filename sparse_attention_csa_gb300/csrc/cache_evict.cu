@@ -210,7 +210,8 @@ __global__ void __launch_bounds__(kThreads, 2) cache_evict_kernel(const __grid_c
         __syncthreads();
         const int32_t need = room - found[1], there = found[2];
         lo += (uint64_t)found[0] << shift;
-        hi = min(hi, lo + (((uint64_t)1 << shift) - 1));
+        const uint64_t width = ((uint64_t)1 << shift) - 1;
+        if (hi - lo > width) hi = lo + width;  // the last bin may reach past 2^64: a NaN's key is 2^64 - 1
         bool exact = need == there;
         if (!exact && there <= kCand) {
             for (int32_t p = tid; p < used; p += kThreads)
