@@ -127,19 +127,21 @@ __global__ void __launch_bounds__(kThreads, 2) cache_evict_kernel(const __grid_c
         const int32_t p = p0 + (tid >> lg);
         const int32_t phys = p < used ? table[p] : -1;
         const int64_t first = (int64_t)p * page, end = first + page;
+        // of the page's rows those in use, and the loads they take; both below
+        // 2^31, so that a step of up to 32 past them stays in 32 bits
+        const uint32_t n = p < used ? (uint32_t)min((int64_t)page, rows - first) : 0u;
+        const uint32_t loads = vec ? (n + 3u) / 4u : n;
         Sum s;
 #pragma unroll 4
-        for (int u = li; u < units; u += lanes) {
-            const int64_t r = first + (vec ? 4 * u : u);
-            if (r >= rows) continue;
+        for (uint32_t u = li; u < loads; u += lanes) {
             if (vec) {
-                const float4 v = __ldg(reinterpret_cast<const float4 *>(mass + r));
+                const float4 v = __ldg(reinterpret_cast<const float4 *>(mass + first) + u);
                 s.add(v.x);
-                s.add(r + 1 < rows ? v.y : 0.0f);
-                s.add(r + 2 < rows ? v.z : 0.0f);
-                s.add(r + 3 < rows ? v.w : 0.0f);
+                s.add(4u * u + 1u < n ? v.y : 0.0f);
+                s.add(4u * u + 2u < n ? v.z : 0.0f);
+                s.add(4u * u + 3u < n ? v.w : 0.0f);
             } else {
-                s.add(__ldg(mass + r));
+                s.add(__ldg(mass + first + u));
             }
         }
         for (int o = lanes >> 1; o > 0; o >>= 1) {
