@@ -722,8 +722,11 @@ csa_status_t csa_attn_mass_paged(const csa_bf16_t *q, const float *softmax_lse,
  * use stay, the lower page among equal sums, until keep_pages pages are held
  * with the former; the rest are given back: pages_out has CSA_PAGE_EVICTED in
  * their place, freed[b] lists their pool pages in the table's order (-1 padded)
- * and n_freed[b] is their number. Other entries are copied. Sums are held to
- * 45 bits or more; one that is NaN ranks above all.
+ * and n_freed[b] is their number. Other entries are copied. With S the sum of
+ * a page's magnitudes, sums are exact, whatever the order of the rows, where
+ * these are multiples of 2^-63 S; otherwise they are off by page_size 2^-67 S
+ * or 2^-58 S at most, whichever is more. They are compared by their upper 47
+ * bits. One that is NaN ranks above all.
  * mass [batch, max_pages * page_size] fp32 (csa_attn_mass_paged), pages,
  * pages_out, freed [batch, max_pages], rows, n_freed [batch] int32; pages_out
  * may be pages itself, freed and n_freed may be NULL. A page that several

@@ -8,12 +8,12 @@
 // are marked in the table and listed.
 //
 // A cluster of blocks a sequence: they share its pages' sums, and the first one
-// chooses. Groups of lanes sum a page each, as a 32-bit sum and the sum of its
-// rounding errors (each found exactly by Knuth's two-sum), so that the order of
-// the rows does not decide between two pages: 64-bit additions, of which the SM
-// does two a clock, made it 44 us for 512 pages and 83 us for 64 sequences
-// (13.3 and 22.3 us with these sums and one block a sequence). A group has one
-// page at a time (two, with more loads on their way, took 0.5 and 2 us more).
+// chooses. Groups of lanes sum a page each in three 32-bit words (roundings are
+// found exactly by Knuth's two-sum), so that the order of the rows does not
+// decide between two pages: 64-bit additions, of which the SM does two a clock,
+// made it 44 us for 512 pages and 83 us for 64 sequences (13.3 and 22.3 us with
+// two such words and one block a sequence). A group has one page at a time (two,
+// with more loads on their way, took 0.5 and 2 us more).
 // The border between staying and going: one histogram over the interval of the
 // sums' keys, which is found with them, leaves a few sums in the border's bin,
 // which are ranked among themselves. More than kCand of them (sums that are
@@ -21,8 +21,8 @@
 // counting, 64 counts at most. (Halving alone took 8 to 20 counts of 500
 // clocks.)
 //
-// Bound by the latency of its steps: 512 pages of 64 rows 4.7 us, 64 sequences
-// of up to 1024 pages (8.6 MB) 10.2 us.
+// Bound by the latency of its steps: 512 pages of 64 rows 4.9 us, 64 sequences
+// of up to 1024 pages (8.6 MB) 11.1 us.
 #include "common.cuh"
 #include "internal.h"
 #include "paged.h"
@@ -35,23 +35,64 @@ constexpr int kThreads = 512;
 constexpr int kBins = 2 * kThreads;
 constexpr int kCand = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr float kLargest = 3.402823466e38f;
 
-// A sum and what its roundings left out.
+// s = a + b rounded; returns what the rounding left out, exactly (Knuth).
+__device__ __forceinline__ float two_sum(float a, float b, float *s) {
+    const float t = a + b, c = t - a;
+    *s = t;
+    return (a - (t - c)) + (b - c);
+}
+
+__device__ __forceinline__ float next_below(float x) {  // x finite, not 0
+    const int32_t u = __float_as_int(x);
+    return __int_as_float(u > 0 ? u - 1 : u + 1);
+}
+
+// A sum in three words: the sum, what its roundings left out, and what the
+// roundings of that did. With a `fold` after every four loads (16 rows) the
+// second word stays below 17 2^-24 of the magnitudes' sum S, the third, lanes
+// joined, below 2^-39. So the sum is exact for rows that are multiples of
+// 2^-63 S, and otherwise each of a lane's rows rounds it by 2^-63 S at most.
+// (In two words, pages of the same 64 rows in another order came out apart, and
+// pages of 4096 rows held 37 bits. A fold after every load and every join: 5.2
+// and 11.8 us in place of 4.9 and 11.1.)
 struct Sum {
-    float hi = 0.0f, lo = 0.0f;
-    __device__ __forceinline__ void add(float x) {
-        const float s = hi + x, b = s - hi;
-        lo += (hi - (s - b)) + (x - b);
-        hi = s;
+    float hi = 0.0f, lo = 0.0f, rest = 0.0f;
+    __device__ __forceinline__ void add(float x) { rest += two_sum(lo, two_sum(hi, x, &hi), &lo); }
+    __device__ __forceinline__ void add(float x, float y, float z) {  // another sum
+        add(x);
+        rest += two_sum(lo, y, &lo) + z;
     }
-    // Order-preserving map of hi + lo to uint64, above 0; NaN above all. The
-    // first word is the sum rounded to 32 bits, the second what is left of it.
+    __device__ __forceinline__ void fold() {
+        float t;
+        const float l = two_sum(hi, lo, &t);
+        if (fabsf(t) <= kLargest) {  // an infinite or NaN sum keeps its first word
+            hi = t;
+            rest = two_sum(l, rest, &lo);
+        }
+    }
+    // Order-preserving map to uint64, above 0; NaN above all. The first word is
+    // the sum rounded down to 32 bits, the second what is left of it, rounded
+    // down too: unlike rounding to the nearest, it has one result for a sum
+    // whatever its three words.
     __device__ __forceinline__ uint64_t key() const {
         if (hi != hi) return ~0ull;
         float h = hi, l = 0.0f;
-        if (fabsf(hi) <= 3.402823466e38f) {
-            h = hi + lo;
-            l = lo - (h - hi);
+        if (fabsf(hi) <= kLargest && fabsf(lo) <= kLargest) {
+            float t, r = two_sum(lo, rest, &t);
+            l = two_sum(hi, t, &h);
+            r = two_sum(l, r, &l);
+            l = two_sum(h, l, &h);  // now |l| is half a unit of h at most, |r| half one of l
+            r = two_sum(l, r, &l);
+            if (l < 0.0f) {
+                const float d = h;
+                h = next_below(h);
+                r += two_sum(d - h, l, &l);
+                r = two_sum(l, r, &l);
+            }
+            if (r < 0.0f) l = next_below(l);
+            if (!(fabsf(h) <= kLargest)) l = 0.0f;  // passed the largest number here
         }
         return (uint64_t)float_key(h) << 32 | float_key(l);
     }
@@ -132,6 +173,7 @@ __global__ void __launch_bounds__(kThreads, 2) cache_evict_kernel(const __grid_c
         const uint32_t n = p < used ? (uint32_t)min((int64_t)page, rows - first) : 0u;
         const uint32_t loads = vec ? (n + 3u) / 4u : n;
         Sum s;
+        int i = 0;
 #pragma unroll 4
         for (uint32_t u = li; u < loads; u += lanes) {
             if (vec) {
@@ -143,12 +185,12 @@ __global__ void __launch_bounds__(kThreads, 2) cache_evict_kernel(const __grid_c
             } else {
                 s.add(__ldg(mass + first + u));
             }
+            if ((++i & 3) == 0) s.fold();
         }
         for (int o = lanes >> 1; o > 0; o >>= 1) {
             const float hi = __shfl_xor_sync(0xffffffffu, s.hi, o);
             const float lo = __shfl_xor_sync(0xffffffffu, s.lo, o);
-            s.add(hi);
-            s.lo += lo;
+            s.add(hi, lo, __shfl_xor_sync(0xffffffffu, s.rest, o));
         }
         if (li == 0 && p < used) {
             const bool safe = first < a.keep_first || end > max(rows - a.keep_last, 0);
@@ -303,7 +345,7 @@ cudaError_t launch_cache_evict(const EvictArgs &a, cudaStream_t stream) {
         entered_context(pc, dev, ctx);
     }
     // as many blocks as their groups of lanes have pages, up to 8, while there are
-    // three an SM at most (64 sequences: 4 blocks each 10.4 us, 8 each 10.9)
+    // three an SM at most (64 sequences: 4 blocks each 10.4 us, 8 each 10.9, with sums of two words)
     int sms, units = a.page_size % 4 == 0 ? a.page_size / 4 : a.page_size, lg = 0;
     e = sm_count(&sms);
     if (e != cudaSuccess) return e;
