@@ -97,6 +97,7 @@ struct Form {
     static constexpr uint32_t kColChunk = 64 * kAcc;
     static constexpr uint32_t kCols = Q4 ? 512 : 128;
     static_assert(!Q4 || kColChunk + 128 * kChunks <= kCols, "tensor memory");
+    static_assert((int64_t)kThreads * (kMaxKeys / kTile) <= INT32_MAX, "a scan's sum");
 };
 
 template <bool Q4>

@@ -117,6 +117,10 @@ struct IndexerPagedArgs {
 size_t indexer_paged_workspace_bytes(int32_t T, int64_t max_rows);
 cudaError_t launch_indexer_topk_paged(IndexerPagedArgs a, cudaStream_t stream);
 
+// Of a token in either cache: the kernels scan the tile counts of many tokens in
+// 32 bits.
+constexpr int32_t kMaxKeys = 1 << 27;
+
 struct MlaPagedArgs {
     const __nv_bfloat16 *q;  // [T, H, 512]
     PagedRows ori;           // width 512

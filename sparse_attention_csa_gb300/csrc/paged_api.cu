@@ -20,7 +20,7 @@ bool known(csa_dtype_t d) { return d == CSA_BF16 || d == CSA_F32; }
 bool known(csa_rope_layout_t l) { return l == CSA_ROPE_INTERLEAVED || l == CSA_ROPE_HALF; }
 
 constexpr int32_t kMaxRopeDim = 1024;
-constexpr int32_t kMaxKeys = 1 << 27;  // of a token in either cache: tile counts of many tokens stay in 32 bits
+using csa::kMaxKeys;
 
 // Do [a, a + len) and [b, b + len) share a byte without being the same?
 bool crosses(const void *a, const void *b, int64_t len) {

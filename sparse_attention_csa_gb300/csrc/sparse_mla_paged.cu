@@ -82,6 +82,11 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr uint32_t kStage = 65536;  // 4 dim groups x 8 x [low, high] x [8 keys x 128 B]
 constexpr uint32_t kRawTile = kTile * q4::kRow;  // rows as they are, each line of 128 bytes swizzled
 
+// Tokens whose tiles are counted in one scan, whatever the block's threads: a
+// token has up to kMaxKeys slots in either cache, and their sum takes 32 bits.
+constexpr int kScan = 384;
+static_assert((int64_t)kScan * 2 * (kMaxKeys / kTile) <= INT32_MAX, "a scan's sum");
+
 constexpr int kLoaders = 64;
 constexpr int kMmaWarp = 10;
 constexpr int kFindWarp = 11;
@@ -482,13 +487,15 @@ sparse_mla_paged_kernel(const __grid_constant__ MlaPagedArgs a) {
             ms->done = ms->run_e = 1;
         }
     } else {
-        // Equal runs. Tokens are scanned kThreads at a time: once to count the
+        // Equal runs. Tokens are scanned kScan at a time: once to count the
         // tiles, once for the token that holds the run's first one.
+        auto tiles_of = [&](int32_t t, bool report) {
+            return tid < kScan && t < a.T ? token_keys<Q4>(a, t, report).tiles() : 0;
+        };
         int64_t N = 0;
         int32_t total;
-        for (int32_t t0 = 0; t0 < a.T; t0 += kThreads) {
-            const int32_t t = t0 + tid;
-            block_exclusive_scan<kThreads>(t < a.T ? token_keys<Q4>(a, t, c == 0).tiles() : 0, ms->scan, &total);
+        for (int32_t t0 = 0; t0 < a.T; t0 += kScan) {
+            block_exclusive_scan<kThreads>(tiles_of(t0 + tid, c == 0), ms->scan, &total);
             N += total;
         }
         tc::tc_fence_after();
@@ -505,8 +512,8 @@ sparse_mla_paged_kernel(const __grid_constant__ MlaPagedArgs a) {
             return;
         }
         int64_t base = 0;
-        for (int32_t t0 = 0; t0 < a.T && base <= s; t0 += kThreads) {
-            const int32_t t = t0 + tid, nt = t < a.T ? token_keys<Q4>(a, t, false).tiles() : 0;
+        for (int32_t t0 = 0; t0 < a.T && base <= s; t0 += kScan) {
+            const int32_t t = t0 + tid, nt = tiles_of(t, false);
             const int64_t bt = base + block_exclusive_scan<kThreads>(nt, ms->scan, &total);
             if (bt <= s && s < bt + nt) {
                 ms->run_t = t;
