@@ -424,9 +424,10 @@ csa_status_t csa_indexer_topk_noalloc(const csa_bf16_t *q, const csa_bf16_t *k, 
  * r % page_size of pool page pages[b, r / page_size]. Pages may have any size
  * and order, and sequences may share pages they only read. Entries outside
  * [0, num_pages) stand for absent pages: a call that needs one skips its rows
- * and records it in the device error word. CSA_PAGE_EVICTED stands for a page
- * given back on purpose (csa_cache_evict writes it): calls that read rows skip
- * its rows and record nothing.
+ * and records it in the device error word. CSA_PAGE_EVICTED in a table of
+ * compressed rows stands for a page given back on purpose (csa_cache_evict
+ * writes it): calls that read rows skip its rows and record nothing. In a table
+ * of window rows it is an absent page like any other.
  *
  * New tokens are rows t of the call's tensors: q_pos[t] (or row_pos[t]) is the
  * token's position in its sequence, from 0, itself included in what it sees,

@@ -199,14 +199,15 @@ __device__ __forceinline__ Slot slot_page(const MlaPagedArgs &a, const Keys &k, 
     return {in, pg < (uint32_t)p.max_pages ? __ldg(p.pages + (int64_t)k.seq * p.max_pages + pg) : -1, win};
 }
 
-// nullptr: no key, or its page is evicted or absent (recorded). Rows of the
+// nullptr: no key, or its page is evicted or absent (recorded). Window rows are
+// never evicted by weight: their table's mark is an absent page. Rows of the
 // compressed cache may be of 384 bytes: the caller knows the slot's kind.
 template <bool Q4>
 __device__ __forceinline__ const __nv_bfloat16 *slot_ptr(const MlaPagedArgs &a, const Slot &s) {
     if (s.in < 0) return nullptr;
     const PagedRows &p = s.win ? a.ori : a.cmp;
     if ((uint32_t)s.phys >= (uint32_t)p.num_pages) {
-        if (s.phys != CSA_PAGE_EVICTED) report_error(a.err, kErrCheck, kKerMlaPaged, 3);
+        if (s.win || s.phys != CSA_PAGE_EVICTED) report_error(a.err, kErrCheck, kKerMlaPaged, 3);
         return nullptr;
     }
     const int64_t row = (int64_t)s.phys * p.page_size + s.in;
