@@ -678,13 +678,18 @@ csa_status_t csa_sparse_mla_paged_q4(
  * (csa_sparse_mla_paged, csa_sparse_mla_paged_q4) and cmp_cache in `format`.
  * Rows are those of the sequence: mass, out [batch, max_pages * page_size]
  * fp32; mass NULL counts as zeros, out may be mass itself. Rows that received
- * nothing keep mass's bits. A row listed twice counts twice; entries that are
- * negative or not visible count nothing, and neither do rows without a page
- * (recorded unless evicted) and heads whose lse is -inf. A row's weight from
- * one token that is NaN counts as 0, one above the number of heads (an lse
- * that is not this attention's) as that number; a token that lists a row more
- * than three times with such an lse gives it no defined weight. Sums do not
- * depend on the order of the tokens' work: equal calls give equal bits.
+ * nothing keep mass's bits. A row's weight from one token is computed in fp32 and
+ * rounded to a multiple of 2^(2 a + b - 119), a = ceil(log2 total_tokens), b =
+ * ceil(log2 topk) with lists and 0 without, so that a call of one token holds
+ * weights down to 2^-119, one of 65535 tokens and lists of 512 down to 2^-78.
+ * A row listed twice counts twice; entries that are negative or not visible
+ * count nothing, and neither do rows without a page (recorded unless evicted)
+ * and heads whose lse is -inf. A row's weight from one token that is NaN counts
+ * as 0, one above the number of heads (an lse that is not this attention's) as
+ * that number; a token that lists a row more than three times with such an lse
+ * gives it no defined weight. The weights of a call are added up without further
+ * rounding, whatever the order of the tokens' work, and rounded to fp32 with
+ * mass: equal calls give equal bits.
  * workspace: csa_attn_mass_paged_workspace_size(total_tokens, topk with
  * cmp_sparse_indices, else max_pages * page_size) bytes, 256-byte aligned; its
  * contents do not matter before the call and mean nothing after it, and calls

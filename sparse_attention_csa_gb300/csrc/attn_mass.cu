@@ -18,14 +18,17 @@
 // rows and 64 KB of q a tile in place of 300 KB. Rows in bf16 are the operand
 // in shared memory as they come.
 //
-// Sums. Weights are added as fixed-point numbers of 64 bits, whose sums have no
-// order (a row may be listed twice, and by several tokens). With lists a block
-// has 2048 rows of one sequence in shared memory; without them 1024 in
-// registers (six long rows 38.2 us; in shared memory as well 42.1).
+// Sums. Weights are added in fixed point, two words of 64 bits, whose sums have
+// no order (a row may be listed twice, and by several tokens): whole units, which
+// leave room for every head of every token, and what they leave of a small
+// weight. (In whole units alone, 2^-40 with 65535 tokens, weights below half of
+// one were lost.) With lists a block has 2048 rows of one sequence in shared
+// memory; without them 1024 in registers (six long rows, of units alone: 38.2 us;
+// in shared memory as well 42.1).
 //
 // Bound by the latencies of both kernels' steps with few rows: one token of 512
-// listed rows 12.4 us. 81 tokens' 41472 bf16 rows (42 MB) 22.6 us: at most three
-// tiles a CTA, and the sums. Six long rows (84 MB in 4 bits) 38.2 us, 2.2 TB/s:
+// listed rows 11.6 us. 81 tokens' 41472 bf16 rows (42 MB) 23.5 us: at most three
+// tiles a CTA, and the sums. Six long rows (84 MB in 4 bits) 38.4 us, 2.2 TB/s:
 // 128 rows' MMAs take 67 clocks each, 2150 a tile, and the issuing thread some
 // 600 a chunk besides; the turning of the rows takes as long beside it.
 #include "common.cuh"
@@ -560,9 +563,33 @@ attn_weight_kernel(const __grid_constant__ MassArgs a) {
 
 // ---------------------------------------------------------------------- sums
 // One block on an SM is asked for: left to itself the compiler keeps to 32
-// registers and spills (one token 14.0 us in place of 12.4).
+// registers and spills (one token, of units alone: 14.0 us in place of 12.4).
 constexpr int kSumThreads = 256;
 constexpr int kTokens = 512;  // of the sequence, known at a time
+
+// Weights in fixed point: whole units of 2^-lg_unit, and what they leave in parts
+// of 2^-lg_part of a unit. Shifts of the mantissa, exact but for the rounding
+// below one part. (Conversions to 64 bits in their place, of which the SM does
+// few: 2048 tokens' weights of all rows 1560 us in place of 914.)
+struct Fixed {
+    unsigned long long units, parts;
+};
+__device__ __forceinline__ Fixed fixed_point(const MassArgs &a, float x) {
+    const uint32_t bits = __float_as_uint(x);  // not negative
+    if (bits < 0x800000u) return {0, 0};       // below any part: lg_unit + lg_part <= 119
+    const uint32_t m = (bits & 0x7fffffu) | 0x800000u;
+    const int e = (int)(bits >> 23) - 150 + a.lg_unit;  // m 2^e units
+    if (e >= 0) return {(unsigned long long)m << e, 0};
+    const int below = min(-e, 24), up = a.lg_part + e;
+    const uint32_t left = m & ((1u << below) - 1u);
+    return {m >> below, up >= 0    ? (unsigned long long)left << up
+                        : up > -25 ? (unsigned long long)((left + (1u << (-up - 1))) >> -up)
+                                   : 0};
+}
+__device__ __forceinline__ float weight_of(const MassArgs &a, const Fixed &f) {
+    return fmaf(__ull2float_rn(f.parts), q4::pow2(-a.lg_unit - a.lg_part),
+                __ull2float_rn(f.units) * q4::pow2(-a.lg_unit));
+}
 
 // Without lists: a thread's four rows keep their sums in registers.
 constexpr int kAllMine = 4;
@@ -582,7 +609,7 @@ __global__ void __launch_bounds__(kSumThreads, 1) attn_mass_all_kernel(const __g
     // what the sums are added to is on its way while they are formed (in place
     // only rows with weight are touched)
     float old[kAllMine];
-    unsigned long long sum[kAllMine] = {};
+    Fixed sum[kAllMine] = {};
 #pragma unroll
     for (int i = 0; i < kAllMine; ++i)
         old[i] = !in_place && a.mass && tid + i * kSumThreads < n ? __ldg(a.mass + row + tid + i * kSumThreads) : 0.0f;
@@ -611,16 +638,20 @@ __global__ void __launch_bounds__(kSumThreads, 1) attn_mass_all_kernel(const __g
 #pragma unroll
             for (int i = 0; i < kAllMine; ++i) x[i] = tid + i * kSumThreads < m ? w[tid + i * kSumThreads] : 0.0f;
 #pragma unroll
-            for (int i = 0; i < kAllMine; ++i) sum[i] += __float2ull_rn(x[i] * a.fixed);
+            for (int i = 0; i < kAllMine; ++i) {
+                const Fixed f = fixed_point(a, x[i]);
+                sum[i].units += f.units;
+                sum[i].parts += f.parts;
+            }
         }
         __syncthreads();
     }
-    const float unit = 1.0f / a.fixed;  // a power of two
 #pragma unroll
     for (int i = 0; i < kAllMine; ++i) {
         const int r = tid + i * kSumThreads;
         if (r >= n) break;
-        if (sum[i]) a.out[row + r] = (in_place ? a.out[row + r] : old[i]) + __ull2float_rn(sum[i]) * unit;
+        if (sum[i].units | sum[i].parts)
+            a.out[row + r] = (in_place ? a.out[row + r] : old[i]) + weight_of(a, sum[i]);
         else if (!in_place) a.out[row + r] = old[i];
     }
 }
@@ -630,14 +661,14 @@ constexpr int kListRows = 2048;
 constexpr int kListMine = kListRows / kSumThreads;  // rows a thread finishes
 
 __global__ void __launch_bounds__(kSumThreads, 1) attn_mass_list_kernel(const __grid_constant__ MassArgs a) {
-    __shared__ unsigned long long acc[kListRows];
+    __shared__ unsigned long long units[kListRows], parts[kListRows];
     __shared__ int32_t token[kTokens], slots[kTokens], seen[kTokens];
     __shared__ int32_t n_tokens;
     const int tid = threadIdx.x;
     const int32_t b = blockIdx.y, r0 = blockIdx.x * kListRows, n = min(kListRows, a.max_rows - r0);
     const int64_t row = (int64_t)b * a.max_rows + r0;
     const bool in_place = a.out == a.mass;
-    for (int i = tid; i < n; i += kSumThreads) acc[i] = 0;
+    for (int i = tid; i < n; i += kSumThreads) units[i] = parts[i] = 0;
     if (tid == 0) n_tokens = 0;
     __syncthreads();
     grid_dependency_wait();
@@ -671,27 +702,35 @@ __global__ void __launch_bounds__(kSumThreads, 1) attn_mass_list_kernel(const __
             const float *w = a.weights + (int64_t)token[k] * a.slot_pad;
             const int32_t *list = a.idx + (int64_t)token[k] * a.topk;
             const int32_t end = min(r0 + n, seen[k]);
-#pragma unroll 4
-            for (int32_t i = tid; i < slots[k]; i += kSumThreads) {
-                const int32_t r = __ldg(list + i);
-                const float x = w[i];
-                if (r >= r0 && r < end && x != 0.0f) atomicAdd(&acc[r - r0], __float2ull_rn(x * a.fixed));
+            // two entries at a time, added one after the other: the code of an
+            // addition four times over took 0.6 us more for 81 tokens
+            for (int32_t i = tid; i < slots[k]; i += 2 * kSumThreads) {
+                const bool two = i + kSumThreads < slots[k];
+                int32_t r = __ldg(list + i), r_next = two ? __ldg(list + i + kSumThreads) : -1;
+                float x = w[i], x_next = two ? w[i + kSumThreads] : 0.0f;
+#pragma unroll 1
+                for (int y = 0; y < 2; ++y, r = r_next, x = x_next) {
+                    if (r < r0 || r >= end || x == 0.0f) continue;
+                    const Fixed f = fixed_point(a, x);
+                    if (f.units) atomicAdd(&units[r - r0], f.units);
+                    if (f.parts) atomicAdd(&parts[r - r0], f.parts);
+                }
             }
         }
         __syncthreads();
     }
-    const float unit = 1.0f / a.fixed;  // a power of two
-    if (in_place) {
+    Fixed sum[kListMine];
 #pragma unroll
-        for (int i = 0; i < kListMine; ++i)
-            if (tid + i * kSumThreads < n && acc[tid + i * kSumThreads]) old[i] = a.out[row + tid + i * kSumThreads];
+    for (int i = 0; i < kListMine; ++i) {
+        const int r = tid + i * kSumThreads;
+        sum[i] = r < n ? Fixed{units[r], parts[r]} : Fixed{0, 0};
+        if (in_place && (sum[i].units | sum[i].parts)) old[i] = a.out[row + r];
     }
 #pragma unroll
     for (int i = 0; i < kListMine; ++i) {
         const int r = tid + i * kSumThreads;
         if (r >= n) break;
-        const unsigned long long sum = acc[r];
-        if (sum) a.out[row + r] = old[i] + __ull2float_rn(sum) * unit;
+        if (sum[i].units | sum[i].parts) a.out[row + r] = old[i] + weight_of(a, sum[i]);
         else if (!in_place) a.out[row + r] = old[i];
     }
 }

@@ -178,7 +178,7 @@ struct MassArgs {
     int64_t slot_pad;
     int32_t T, H, batch, topk, cmp_ratio, max_rows, q4;
     float softmax_scale;
-    float fixed;             // fixed-point units of a weight of 1: a power of two
+    int32_t lg_unit, lg_part;  // fixed-point units of a weight of 1, parts of a unit: their log2
     uint64_t wait_ns;
 };
 

@@ -446,9 +446,13 @@ csa_status_t csa_attn_mass_paged(const csa_bf16_t *q, const float *softmax_lse,
     a.q4 = format == CSA_ROWS_Q4;
     a.softmax_scale = softmax_scale;
     // the weights of a call add up to less than heads * total_tokens <= 2^(6 + lg)
-    int lg = 0;
+    // and what whole units leave of them to less than slots * total_tokens units,
+    // of a row that a list of `slots` entries may repeat
+    int lg = 0, lg_list = 0;
     while ((1 << lg) < total_tokens) ++lg;
-    a.fixed = std::ldexp(1.0f, 63 - 7 - lg);
+    while (cmp_sparse_indices && (1 << lg_list) < topk) ++lg_list;  // topk <= 2^27
+    a.lg_unit = 63 - 7 - lg;
+    a.lg_part = 63 - lg - lg_list;
     a.wait_ns = csa::pipeline_wait_limit_ns();
     return from_cuda(csa::launch_attn_mass(a, (cudaStream_t)stream));
 }
