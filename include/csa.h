@@ -689,7 +689,8 @@ csa_status_t csa_sparse_mla_paged_q4(
  * that number; a token that lists a row more than three times with such an lse
  * gives it no defined weight. The weights of a call are added up without further
  * rounding, whatever the order of the tokens' work, and rounded to fp32 with
- * mass: equal calls give equal bits.
+ * mass: equal calls give equal bits. After a wait that gave up (csa_device_error)
+ * out holds no defined values, nor does mass where it is out.
  * workspace: csa_attn_mass_paged_workspace_size(total_tokens, topk with
  * cmp_sparse_indices, else max_pages * page_size) bytes, 256-byte aligned; its
  * contents do not matter before the call and mean nothing after it, and calls
