@@ -658,7 +658,8 @@ csa_status_t csa_cache_read_q4(const uint8_t *cache, const int32_t *pages, const
 /*
  * csa_sparse_mla_paged with the compressed rows held in 4 bits: cmp_cache
  * [cmp_num_pages, cmp_page_size, 384]. The window rows stay bf16. The attention
- * is that over the held values; arguments, workspace and errors are the same.
+ * is that over the held values; arguments, workspace and errors are the same. It
+ * saves memory, not time: 1.1 to 1.2 times that of the bf16 form.
  */
 csa_status_t csa_sparse_mla_paged_q4(
     const csa_bf16_t *q, const csa_bf16_t *ori_cache, const uint8_t *cmp_cache,

@@ -19,9 +19,10 @@
 // back, in blocks of 256 threads, 15.8 us with one, 16.4 and 22.7. Blocks of 128
 // threads 15.2; warps that take rows in turn, the next one's on its way, spill.)
 //
-// The append is bound by its 420 instructions a row, which issue 41 % of the time
-// behind the look-up of their slot (16368 bf16 rows, 23 MB: 9 us of the 15.2);
-// the read by memory and the look-up (40955 rows, 58 MB: 12.6 us, 4.6 TB/s).
+// The append is bound by the latency of a row's way, two dependent look-ups ahead
+// of its first store, beside 420 instructions that issue 42 % of the time (16368
+// bf16 rows, 23 MB: 9 us of the 15.3); the read by memory and the look-up (40955
+// rows, 58 MB: 12.6 us, 4.6 TB/s).
 #include "common.cuh"
 #include "internal.h"
 #include "paged.h"
@@ -213,7 +214,10 @@ cudaError_t launch_cache_read_q4(const Q4RowsArgs &a, cudaStream_t stream) {
     int sms;
     const cudaError_t e = sm_count(&sms);
     if (e != cudaSuccess) return e;
-    return a.T >= 64 * sms  // two rows a warp while that leaves an SM 32 warps
+    // two rows a warp while that leaves an SM 32 warps: 16384, 40955 and 120000 rows
+    // 6.4, 12.5 and 30.1 us, with one 6.6, 13.1 and 33.6; 64 and 6000 rows 1.9 and
+    // 4.1 us, with one 1.6 and 3.7
+    return a.T >= 64 * sms
                ? launch_early(cache_read_q4_kernel<2>, dim3(row_blocks(a.T, 2)), dim3(kThreads), 0, stream, a)
                : launch_early(cache_read_q4_kernel<1>, dim3(row_blocks(a.T, 1)), dim3(kThreads), 0, stream, a);
 }

@@ -50,7 +50,7 @@
 // so that a tile is of one kind. A tile of 4-bit rows comes to shared memory as
 // it is (24 KB, three on their way) and eight more warps turn it into a bf16
 // tile, of which two fit beside them; what follows is as above, over values
-// that bf16 holds exactly. The same cases: one token 14.8 us, 64 tokens 29.1,
+// that bf16 holds exactly. The same cases: one token 14.6 us, 64 tokens 29.0,
 // long rows (85 MB read) 71.1 or 1.2 TB/s. Long rows are bound by a tile's way
 // through the two stages: turning it 2000 clocks beside the softmax (1320 by
 // itself), scores 1400 and 650 until they are seen, softmax 1400, O^T 830 and
